@@ -15,8 +15,6 @@
 #include <cstring>
 #include <vector>
 
-#define GDN_API extern "C" __attribute__((visibility("default")))
-
 using gdn::kBlock;
 using gdn::LaunchCommon;
 
@@ -91,11 +89,22 @@ gdn_status check_state(const gdn_layer_desc *d, const gdn_session *s, const char
     return GDN_OK;
 }
 
+Timing g_timing;
+
+// Bounded waits: default poll limit, and the test hook that makes the next launches' waits run out.
+constexpr long long kDefaultWaitLimit = 1LL << 24;
+long long g_wait_limit = kDefaultWaitLimit;
+int g_skip_first_copy = 0;
+
 }  // namespace gdn_host
 
 using namespace gdn_host;
 
 namespace {
+
+const char *const kKindName[K_KINDS] = {"prep_wy", "conv_commit", "state_output", "state_copy", "decode", "gates",
+                                        "prep_wy_tail", "prefill_fused", "kv_plan", "kv_append", "kv_state",
+                                        "kv_attention", "kv_join"};
 
 // Workspace layout for a launch of up to nblk blocks. Offsets count from the workspace pointer
 // rounded up to 256 bytes (the kernels' widest stores want 32-byte alignment); `bytes` includes
@@ -139,11 +148,6 @@ std::atomic<unsigned long long> g_epoch{[] {
     return ((unsigned long long)rd() << 32) ^ (unsigned long long)rd() ^ 0x9e3779b97f4a7c15ULL;
 }()};
 
-// Bounded waits: default poll limit, and the test hook that makes the next launches' waits run out.
-constexpr long long kDefaultWaitLimit = 1LL << 24;
-long long g_wait_limit = kDefaultWaitLimit;
-int g_skip_first_copy = 0;
-
 void fill_common(LaunchCommon &p, const gdn_layer_desc *d, const void *xq, const void *xk, const void *xv,
                  const float *g, const float *beta, const void *conv_w, void *out) {
     std::memset(&p, 0, sizeof(p));
@@ -182,37 +186,6 @@ cudaError_t encode_rows_map(CUtensorMap *m, const void *base, int64_t rows, int6
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-// ---- optional per-kernel event timing ----
-enum Kind { K_PREP = 0, K_CONV = 1, K_STATE = 2, K_COPY = 3, K_DECODE = 4, K_GATES = 5, K_PREP_TAIL = 6, K_FUSED = 7,
-            K_KINDS = 8 };
-const char *const kKindName[K_KINDS] = {"prep_wy", "conv_commit", "state_output", "state_copy", "decode", "gates",
-                                        "prep_wy_tail", "prefill_fused"};
-
-struct Timing {
-    bool on = false;
-    int cap = 0, used = 0;
-    std::vector<cudaEvent_t> ev;  // 2 per timed launch
-    std::vector<int> kind;
-    int64_t launches[K_KINDS] = {};
-};
-Timing g_timing;
-
-template <class F>
-cudaError_t launch_k(Kind k, cudaStream_t st, F &&f) {
-    Timing &T = g_timing;
-    if (!T.on) return f();
-    T.launches[k]++;
-    if (T.used >= T.cap) return f();
-    cudaEvent_t a = T.ev[2 * T.used], b = T.ev[2 * T.used + 1];
-    cudaError_t e = cudaEventRecord(a, st);
-    if (e != cudaSuccess) return e;
-    e = f();
-    if (e != cudaSuccess) return e;
-    e = cudaEventRecord(b, st);
-    if (e == cudaSuccess) T.kind[T.used++] = k;
-    return e;
 }
 
 }  // namespace
@@ -704,6 +677,9 @@ GDN_API gdn_status gdn_device_status(gdn_stream_t stream) {
     cudaError_t e = gdn_take_device_error(&word, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "device status read");
     if (word & 1u) return fail(GDN_ERR_TIMEOUT, "a kernel gave up waiting for its operand copies");
+    if (word & 2u)
+        return fail(GDN_ERR_INVALID_ARG, "a key/value plan reached outside the sizes given with it (rows, max_new, "
+                    "max_len, pages or slots): its out-of-range units or blocks were left out");
     return GDN_OK;
 }
 
@@ -734,6 +710,7 @@ GDN_API const char *gdn_status_string(gdn_status s) {
         case GDN_ERR_TIMEOUT: return "GDN_ERR_TIMEOUT";
         case GDN_ERR_NOT_FOUND: return "GDN_ERR_NOT_FOUND";
         case GDN_ERR_IO: return "GDN_ERR_IO";
+        case GDN_ERR_CAPACITY: return "GDN_ERR_CAPACITY";
     }
     return "unknown status";
 }

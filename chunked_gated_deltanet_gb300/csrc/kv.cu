@@ -1,0 +1,414 @@
+// The paged 8-bit key/value cache's bookkeeping and writes: the plan of a batch (block tables and unit map from
+// request lengths), the append (quantisation of complete blocks, raw copies into the tail), forks and releases.
+#include "kv.cuh"
+
+#include <algorithm>
+#include <cfloat>
+
+namespace gdn {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanPer = kKvMaxRequests / kPlanThreads;   // requests per thread
+
+struct Sum3 {
+    long long rows;
+    int units, pages;
+};
+__device__ __forceinline__ Sum3 add(const Sum3 &a, const Sum3 &b) {
+    return {a.rows + b.rows, a.units + b.units, a.pages + b.pages};
+}
+
+// Exclusive sum over the CTA's threads in thread order; *total receives the sum of all. ws: one Sum3 per warp.
+template <int NT>
+__device__ Sum3 block_exclusive(Sum3 x, Sum3 *ws, Sum3 *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sum3 in = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sum3 y = {__shfl_up_sync(0xffffffffu, in.rows, o), __shfl_up_sync(0xffffffffu, in.units, o),
+                        __shfl_up_sync(0xffffffffu, in.pages, o)};
+        if (lane >= o) in = add(in, y);
+    }
+    if (lane == 31) ws[warp] = in;
+    __syncthreads();
+    if (warp == 0) {
+        Sum3 w = lane < NT / 32 ? ws[lane] : Sum3{0, 0, 0};
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Sum3 y = {__shfl_up_sync(0xffffffffu, w.rows, o), __shfl_up_sync(0xffffffffu, w.units, o),
+                            __shfl_up_sync(0xffffffffu, w.pages, o)};
+            if (lane >= o) w = add(w, y);
+        }
+        ws[lane] = w;
+    }
+    __syncthreads();
+    *total = ws[NT / 32 - 1];
+    const Sum3 before = warp > 0 ? ws[warp - 1] : Sum3{0, 0, 0};
+    return {before.rows + in.rows - x.rows, before.units + in.units - x.units, before.pages + in.pages - x.pages};
+}
+
+// Per request, in shared memory: what the expansion into units needs.
+struct PlanReq {
+    int ctx, count, slot, buf, unit0, page0, row0, pad;
+};
+
+// Plan of a batch in one CTA: per request i with ctx tokens held and n_new[i] to come, rows[i] = sum of earlier
+// requests' new tokens, one unit per touched block, one page popped from the free stack per block that completes.
+// Sums go in request order, so pages are handed out in unit order. A batch that does not fit (pages, table, unit
+// map, a bad slot or count) leaves the cache as it was, with no unit and the reason in counts[1].
+// Bound: latency (about 1 KB in and out per 16 requests); one CTA keeps the free stack's update in place and
+// race-free without a second launch.
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvCache c, const int32_t *slots, const int32_t *n_new,
+                                                                int n, int32_t *rows, int32_t *units, int32_t *counts,
+                                                                int max_units, int32_t *state_out, int32_t *n_free_out) {
+    grid_dep_wait();
+    grid_dep_launch();
+    extern __shared__ __align__(16) unsigned char plan_smem[];
+    PlanReq *req = reinterpret_cast<PlanReq *>(plan_smem);
+    __shared__ Sum3 ws[32];
+    __shared__ unsigned bad_all;
+    const int t = threadIdx.x;
+    const int per = (n + kPlanThreads - 1) / kPlanThreads;   // contiguous requests of this thread
+    if (t == 0) bad_all = 0;
+    const int n_free = *c.n_free;
+    int slot[kPlanPer], cnt[kPlanPer], ctx[kPlanPer], buf[kPlanPer];
+    Sum3 mine = {0, 0, 0};
+    unsigned bad = 0;
+#pragma unroll
+    for (int j = 0; j < kPlanPer; ++j) {
+        const int i = t * per + j;
+        slot[j] = cnt[j] = ctx[j] = buf[j] = 0;
+        if (j < per && i < n) {
+            slot[j] = slots[i];
+            cnt[j] = n_new[i];
+            if ((unsigned)slot[j] >= (unsigned)c.n_slots || cnt[j] < 0) {
+                bad |= 8u;
+                slot[j] = cnt[j] = 0;
+            } else {
+                const int2 s = reinterpret_cast<const int2 *>(c.state)[slot[j]];
+                ctx[j] = s.x;
+                buf[j] = s.y & 1;
+                const long long end = (long long)ctx[j] + cnt[j];
+                if (ctx[j] < 0 || end / kKvBlock > c.max_blocks || end > INT32_MAX - kKvBlock) {
+                    bad |= ctx[j] < 0 ? 8u : 2u;
+                    ctx[j] = cnt[j] = 0;
+                }
+            }
+            const int end = ctx[j] + cnt[j];
+            mine.rows += cnt[j];
+            if (cnt[j] > 0) mine.units += (end + kKvBlock - 1) / kKvBlock - ctx[j] / kKvBlock;
+            mine.pages += end / kKvBlock - ctx[j] / kKvBlock;
+        }
+    }
+    Sum3 total;
+    Sum3 at = block_exclusive<kPlanThreads>(mine, ws, &total);
+    if (bad) atomicOr(&bad_all, bad);
+    if (t == 0) {
+        if (total.pages > n_free || n_free > c.n_pages) atomicOr(&bad_all, 1u);
+        if (total.units > max_units || total.rows > INT32_MAX) atomicOr(&bad_all, 4u);
+    }
+    __syncthreads();   // every read of the state and of the free stack's height is done
+    const unsigned status = bad_all;
+#pragma unroll
+    for (int j = 0; j < kPlanPer; ++j) {
+        const int i = t * per + j;
+        if (j < per && i < n) {
+            if (status == 0) {
+                rows[i] = (int)at.rows;
+                const int end = ctx[j] + cnt[j];
+                const int fb = ctx[j] / kKvBlock, eb = end / kKvBlock;
+                req[i] = {ctx[j], cnt[j], slot[j], buf[j], at.units, at.pages, (int)at.rows, 0};
+                // the open block moves to the other tail buffer when it is a new block, so that the rows of the
+                // block that closes in this call stay readable after its append
+                reinterpret_cast<int2 *>(state_out)[slot[j]] = make_int2(end, eb != fb ? buf[j] ^ 1 : buf[j]);
+                at.rows += cnt[j];
+                if (cnt[j] > 0) at.units += (end + kKvBlock - 1) / kKvBlock - fb;
+                at.pages += eb - fb;
+            } else {
+                rows[i] = 0;
+            }
+        }
+    }
+    if (t == 0) {
+        rows[n] = status == 0 ? (int)total.rows : 0;
+        counts[0] = status == 0 ? total.units : 0;
+        counts[1] = (int)status;
+        *n_free_out = status == 0 ? n_free - total.pages : n_free;
+    }
+    if (status != 0) return;
+    __syncthreads();
+    // one thread per unit; its request is the last one whose first unit is not after it
+    for (int u = t; u < total.units; u += kPlanThreads) {
+        int lo = 0, hi = n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (req[mid].unit0 <= u) lo = mid;
+            else hi = mid - 1;
+        }
+        const PlanReq r = req[lo];
+        const int j = u - r.unit0, fb = r.ctx / kKvBlock, block = fb + j, end = r.ctx + r.count;
+        const int start = max(r.ctx, block * kKvBlock), stop = min(end, block * kKvBlock + kKvBlock);
+        const bool closes = stop == block * kKvBlock + kKvBlock;
+        int page = -1;
+        if (closes) {
+            page = c.free_pages[n_free - 1 - (r.page0 + j)];
+            if ((unsigned)page < (unsigned)c.n_pages) {
+                c.table[(int64_t)r.slot * c.max_blocks + block] = page;
+                c.refs[page] = 1;
+            }
+        }
+        int4 *o = reinterpret_cast<int4 *>(units) + 2 * (int64_t)u;
+        o[0] = make_int4(r.slot, block, page, start - block * kKvBlock);
+        o[1] = make_int4(stop - start, r.row0 + start - r.ctx, r.buf, closes ? -1 : (end / kKvBlock != fb ? r.buf ^ 1 : r.buf));
+    }
+}
+
+// ---- append ----
+
+// x / scale rounded to nearest even, as an IEEE division and rint would give: the product with the reciprocal is
+// within 1e-4 of the quotient for |x / scale| <= 127, so only quotients that near a tie need the division.
+__device__ __forceinline__ int kv_quant(float x, float scale, float inv) {
+    float y = x * inv;
+    float q = rintf(y);
+    if (!(fabsf(fabsf(y - q) - 0.5f) > 1e-3f)) {
+        y = x / scale;
+        q = rintf(y);
+    }
+    return q == q ? (int)fminf(fmaxf(q, -127.f), 127.f) : 0;   // 0 / 0 of an all-zero block, or a NaN: 0
+}
+
+template <typename T> struct Vec16;   // 16 bytes of T as floats
+template <> struct Vec16<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void get(const uint4 &u, float (&f)[4]) {
+        f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+    }
+};
+template <> struct Vec16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void get(const uint4 &u, float (&f)[8]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+
+// CTA (unit, kv head, k or v). A block that closes: its 64 rows (tail rows before `first`, then new ones) go through
+// registers once: absmax, scale, int8 page. A block that stays open: its new rows are copied into the tail.
+template <typename InT, int D>
+__global__ void __launch_bounds__(256) kv_append_kernel(const KvCache c, const int32_t *units, const int32_t *counts,
+                                                        const InT *kx, const InT *vx, int64_t n_rows, int Hkv,
+                                                        unsigned *err) {
+    grid_dep_wait();
+    grid_dep_launch();
+    if ((int)blockIdx.x >= counts[0]) return;
+    constexpr int VN = Vec16<InT>::N, VPR = D / VN, NV = kKvBlock * VPR / 256;   // vectors per row, per thread
+    __shared__ float red[8];
+    const KvUnit u = kv_load_unit(units, blockIdx.x);
+    if (!kv_unit_ok(u, c, n_rows)) {
+        if (threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) atomicOr(err, kErrKvBounds);
+        return;
+    }
+    const int h = blockIdx.y, kv = blockIdx.z, t = threadIdx.x;
+    const InT *x = kv ? vx : kx;
+    const InT *old = static_cast<const InT *>(c.tail) + kv_tail_offset(u.slot, u.src, kv, h, Hkv, D);
+    uint4 w[NV];
+    const bool closes = u.page >= 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = t + 256 * i, r = e / VPR, col = (e % VPR) * VN;
+        const int o = r - u.first;
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (o >= 0 && o < u.count) w[i] = *reinterpret_cast<const uint4 *>(x + ((int64_t)(u.row + o) * Hkv + h) * D + col);
+        else if (o < 0 && closes) w[i] = *reinterpret_cast<const uint4 *>(old + r * D + col);
+    }
+    if (!closes) {
+        InT *tail = static_cast<InT *>(c.tail) + kv_tail_offset(u.slot, u.dst, kv, h, Hkv, D);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = t + 256 * i, r = e / VPR, col = (e % VPR) * VN;
+            const int o = r - u.first;
+            if (o >= 0 && o < u.count) *reinterpret_cast<uint4 *>(tail + r * D + col) = w[i];
+        }
+        return;
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float f[VN];
+        Vec16<InT>::get(w[i], f);
+#pragma unroll
+        for (int j = 0; j < VN; ++j) {
+            const float a = fabsf(f[j]);
+            m = fmaxf(m, a <= FLT_MAX ? a : 0.f);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((t & 31) == 0) red[t >> 5] = m;
+    __syncthreads();
+    m = red[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i]);
+    const float scale = m / 127.f, inv = 1.f / scale;
+    const int64_t ph = (int64_t)u.page * Hkv + h;
+    int8_t *page = (kv ? c.v : c.k) + ph * kKvBlock * D;
+    if (t == 0) (kv ? c.v_scale : c.k_scale)[ph] = scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float f[VN];
+        Vec16<InT>::get(w[i], f);
+        uint32_t b[VN / 4];
+#pragma unroll
+        for (int j = 0; j < VN / 4; ++j) {
+            b[j] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) b[j] |= (uint32_t)(kv_quant(f[4 * j + k], scale, inv) & 0xff) << (8 * k);
+        }
+        const int e = t + 256 * i, r = e / VPR, col = (e % VPR) * VN;
+        if (VN == 8) *reinterpret_cast<uint2 *>(page + r * D + col) = make_uint2(b[0], b[VN / 4 - 1]);
+        else *reinterpret_cast<uint32_t *>(page + r * D + col) = b[0];
+    }
+}
+
+// ---- forks and releases ----
+
+// Every slot empty, every page free (page 0 on top of the stack).
+__global__ void __launch_bounds__(256) kv_init_kernel(const KvCache c) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i < c.n_pages) {
+        c.free_pages[i] = c.n_pages - 1 - i;
+        c.refs[i] = 0;
+    }
+    if (i < c.n_slots) reinterpret_cast<int2 *>(c.state)[i] = make_int2(0, 0);
+    if (i == 0) *c.n_free = c.n_pages;
+}
+
+// Drops the slot's hold on its pages (CTA-wide): pages that no slot names any more go back on the free stack in
+// block order. The slot then holds nothing.
+__device__ void kv_drop(const KvCache &c, int slot, Sum3 *ws) {
+    const int len = c.state[2 * slot], nb = min(max(len, 0) / kKvBlock, c.max_blocks);
+    int height = *c.n_free;
+    __syncthreads();
+    for (int b0 = 0; b0 < nb; b0 += kPlanThreads) {
+        const int b = b0 + threadIdx.x;
+        int page = -1;
+        bool freed = false;
+        if (b < nb) {
+            page = c.table[(int64_t)slot * c.max_blocks + b];
+            if ((unsigned)page < (unsigned)c.n_pages) freed = --c.refs[page] == 0;
+        }
+        Sum3 total;
+        const Sum3 at = block_exclusive<kPlanThreads>({0, 0, freed ? 1 : 0}, ws, &total);
+        if (freed && height + at.pages < c.n_pages) c.free_pages[height + at.pages] = page;
+        height += total.pages;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        *c.n_free = min(height, c.n_pages);
+        c.state[2 * slot] = 0;
+    }
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(const KvCache c, int slot) {
+    __shared__ Sum3 ws[32];
+    grid_dep_wait();
+    grid_dep_launch();
+    kv_drop(c, slot, ws);
+}
+
+// CTA 0: dst drops what it holds, then names src's complete blocks. The other CTAs copy src's open rows into the same
+// tail buffer of dst (nothing they read is written here).
+__global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const KvCache c, int src, int dst, int Hkv, int row_vec) {
+    __shared__ Sum3 ws[32];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int2 s = reinterpret_cast<const int2 *>(c.state)[src];
+    const int len = max(s.x, 0), buf = s.y & 1;
+    if (blockIdx.x == 0) {
+        kv_drop(c, dst, ws);
+        const int nb = min(len / kKvBlock, c.max_blocks);
+        for (int b = threadIdx.x; b < nb; b += kPlanThreads) {
+            const int page = c.table[(int64_t)src * c.max_blocks + b];
+            c.table[(int64_t)dst * c.max_blocks + b] = page;
+            if ((unsigned)page < (unsigned)c.n_pages) ++c.refs[page];
+        }
+        if (threadIdx.x == 0) reinterpret_cast<int2 *>(c.state)[dst] = make_int2(len, buf);
+        return;
+    }
+    const int open = len % kKvBlock, per_head = open * row_vec;
+    const int64_t n = 2LL * Hkv * per_head, stride = (int64_t)(gridDim.x - 1) * kPlanThreads;
+    const uint4 *from = static_cast<const uint4 *>(c.tail) + ((int64_t)src * 2 + buf) * 2 * Hkv * kKvBlock * row_vec;
+    uint4 *to = static_cast<uint4 *>(c.tail) + ((int64_t)dst * 2 + buf) * 2 * Hkv * kKvBlock * row_vec;
+    for (int64_t i = (int64_t)(blockIdx.x - 1) * kPlanThreads + threadIdx.x; i < n; i += stride) {
+        const int64_t e = i / per_head * kKvBlock * row_vec + i % per_head;
+        to[e] = from[e];
+    }
+}
+
+template <typename InT, int D>
+cudaError_t launch_append(const KvCache &c, const int32_t *units, const int32_t *counts, int unit_bound, const void *k,
+                          const void *v, int64_t n_rows, int Hkv, unsigned *err, cudaStream_t st) {
+    const dim3 grid((unsigned)unit_bound, (unsigned)Hkv, 2);
+    const cudaError_t e = gdn_launch_pdl(kv_append_kernel<InT, D>, grid, 256, 0, st, c, units, counts,
+                                         static_cast<const InT *>(k), static_cast<const InT *>(v), n_rows, Hkv, err);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace gdn
+
+cudaError_t gdn_launch_kv_plan(const gdn::KvCache &c, const int32_t *slots, const int32_t *n_new, int n, int32_t *rows,
+                               int32_t *units, int32_t *counts, int max_units, int32_t *state_out, int32_t *n_free_out,
+                               cudaStream_t st) {
+    using namespace gdn;
+    const size_t smem = (size_t)n * sizeof(PlanReq);
+    cudaError_t e = cudaSuccess;
+    if (smem > 32 * 1024) {
+        e = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(kKvMaxRequests * sizeof(PlanReq)));
+        if (e != cudaSuccess) return e;
+    }
+    e = gdn_launch_pdl(kv_plan_kernel, 1, kPlanThreads, smem, st, c, slots, n_new, n, rows, units, counts, max_units,
+                       state_out, n_free_out);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t gdn_launch_kv_append(const gdn::KvCache &c, const int32_t *units, const int32_t *counts, int unit_bound,
+                                 const void *k, const void *v, int64_t n_rows, int Hkv, int d, int bf16, unsigned *err,
+                                 cudaStream_t st) {
+    using namespace gdn;
+    using bf = __nv_bfloat16;
+    if (d == 64)
+        return bf16 ? launch_append<bf, 64>(c, units, counts, unit_bound, k, v, n_rows, Hkv, err, st)
+                    : launch_append<float, 64>(c, units, counts, unit_bound, k, v, n_rows, Hkv, err, st);
+    if (d == 128)
+        return bf16 ? launch_append<bf, 128>(c, units, counts, unit_bound, k, v, n_rows, Hkv, err, st)
+                    : launch_append<float, 128>(c, units, counts, unit_bound, k, v, n_rows, Hkv, err, st);
+    return bf16 ? launch_append<bf, 256>(c, units, counts, unit_bound, k, v, n_rows, Hkv, err, st)
+                : launch_append<float, 256>(c, units, counts, unit_bound, k, v, n_rows, Hkv, err, st);
+}
+
+cudaError_t gdn_launch_kv_init(const gdn::KvCache &c, cudaStream_t st) {
+    const int n = std::max(c.n_pages, c.n_slots);
+    const cudaError_t e = gdn_launch_pdl(gdn::kv_init_kernel, (unsigned)((n + 255LL) / 256), 256, 0, st, c);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t gdn_launch_kv_fork(const gdn::KvCache &c, int src, int dst, int Hkv, int d, int elt, cudaStream_t st) {
+    using namespace gdn;
+    const int row_vec = d * elt / 16;
+    const int copy = std::min<int64_t>(64, (2LL * Hkv * kKvBlock * row_vec + kPlanThreads - 1) / kPlanThreads);
+    const cudaError_t e = gdn_launch_pdl(kv_fork_kernel, 1 + copy, kPlanThreads, 0, st, c, src, dst, Hkv, row_vec);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t gdn_launch_kv_release(const gdn::KvCache &c, int slot, cudaStream_t st) {
+    const cudaError_t e = gdn_launch_pdl(gdn::kv_release_kernel, 1, gdn::kPlanThreads, 0, st, c, slot);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}

@@ -17,8 +17,6 @@
 #include <sys/stat.h>
 #include <unistd.h>
 
-#define GDN_API extern "C" __attribute__((visibility("default")))
-
 using namespace gdn_host;
 
 namespace {

@@ -25,12 +25,15 @@ GDN_ERR_CUDA = 6
 GDN_ERR_TIMEOUT = 7
 GDN_ERR_NOT_FOUND = 8
 GDN_ERR_IO = 9
+GDN_ERR_CAPACITY = 10
 GDN_FP32 = 0
 GDN_BF16 = 1
 GDN_CONV_NONE = 0
 GDN_CONV_SILU = 1
 GDN_ALLOW_PARTIAL = 1
 GDN_MAX_SESSIONS = 4096
+GDN_KV_BLOCK = 64
+GDN_KV_MAX_REQUESTS = 4096
 
 EXPORTED = ["gdn_desc_tag", "gdn_desc_check", "gdn_state_bytes", "gdn_conv_state_bytes", "gdn_session_init",
             "gdn_workspace_size", "gdn_prefill_chunks", "gdn_prefill_varlen", "gdn_state_capture",
@@ -38,7 +41,10 @@ EXPORTED = ["gdn_desc_tag", "gdn_desc_check", "gdn_state_bytes", "gdn_conv_state
             "gdn_prefill_chunks_noalloc", "gdn_device_status", "gdn_debug_inject_wait_timeout", "gdn_gates",
             "gdn_last_error", "gdn_status_string", "gdn_state_blob_bytes", "gdn_state_serialize",
             "gdn_state_deserialize", "gdn_state_save", "gdn_state_load", "gdn_prefill_branches",
-            "gdn_prefill_chunks_checkpoint", "gdn_prefill_varlen_checkpoint"]
+            "gdn_prefill_chunks_checkpoint", "gdn_prefill_varlen_checkpoint", "gdn_attn_desc_check",
+            "gdn_kv_max_units", "gdn_kv_cache_init", "gdn_kv_plan", "gdn_kv_status", "gdn_kv_append",
+            "gdn_kv_attention_workspace", "gdn_kv_attention_workspace_min", "gdn_kv_attention", "gdn_kv_fork",
+            "gdn_kv_release"]
 
 
 class gdn_layer_desc(ctypes.Structure):
@@ -51,6 +57,22 @@ class gdn_layer_desc(ctypes.Structure):
 class gdn_session(ctypes.Structure):
     _fields_ = [("S", ctypes.c_void_p), ("conv", ctypes.c_void_p), ("committed", ctypes.c_int64),
                 ("tag", ctypes.c_uint64)]
+
+
+class gdn_attn_desc(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class gdn_kv_cache(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("k", "v", "k_scale", "v_scale", "tail", "state", "table",
+                                               "free_pages", "n_free", "refs")] + \
+               [(f, ctypes.c_int32) for f in ("n_pages", "n_slots", "max_blocks")]
+
+
+class gdn_kv_map(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("units", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+                ("max_requests", ctypes.c_int32), ("max_units", ctypes.c_int32)]
 
 
 class gdn_kernel_time(ctypes.Structure):
@@ -80,6 +102,7 @@ def load_library(path: Optional[str] = None):
     D = ctypes.POINTER(gdn_layer_desc)
     Sp = ctypes.POINTER(gdn_session)
     I64p = ctypes.POINTER(ctypes.c_int64)
+    A, Kp, Mp = (ctypes.POINTER(t) for t in (gdn_attn_desc, gdn_kv_cache, gdn_kv_map))
     sig = {
         "gdn_desc_tag": (ctypes.c_uint64, [D]),
         "gdn_desc_check": (ctypes.c_int, [D]),
@@ -109,6 +132,17 @@ def load_library(path: Optional[str] = None):
         "gdn_gates": (ctypes.c_int, [D, vp, vp, vp, vp, i64, vp, vp, vp]),
         "gdn_last_error": (ctypes.c_char_p, []),
         "gdn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
+        "gdn_attn_desc_check": (ctypes.c_int, [A]),
+        "gdn_kv_max_units": (i32, [i64, i32]),
+        "gdn_kv_cache_init": (ctypes.c_int, [A, Kp, vp]),
+        "gdn_kv_plan": (ctypes.c_int, [A, Kp, vp, vp, i32, Mp, vp, vp, vp]),
+        "gdn_kv_status": (ctypes.c_int, [Mp, vp]),
+        "gdn_kv_append": (ctypes.c_int, [A, Kp, Mp, vp, vp, i64, vp]),
+        "gdn_kv_attention_workspace": (ctypes.c_size_t, [A, i64, i32, i64]),
+        "gdn_kv_attention_workspace_min": (ctypes.c_size_t, [A, i64]),
+        "gdn_kv_attention": (ctypes.c_int, [A, Kp, Mp, vp, vp, vp, vp, i64, i32, i64, vp, ctypes.c_size_t, vp]),
+        "gdn_kv_fork": (ctypes.c_int, [A, Kp, i32, i32, vp]),
+        "gdn_kv_release": (ctypes.c_int, [A, Kp, i32, vp]),
         "gdn_state_blob_bytes": (ctypes.c_size_t, [D]),
         "gdn_state_serialize": (ctypes.c_int, [D, Sp, vp, ctypes.c_size_t, vp]),
         "gdn_state_deserialize": (ctypes.c_int, [D, vp, ctypes.c_size_t, Sp, vp]),
@@ -341,6 +375,140 @@ def gdn_gates(desc, a: torch.Tensor, b: torch.Tensor, A_log: torch.Tensor, dt_bi
                                     _ptr(beta), _stream(stream)))
 
 
+# ---- attention over a paged key/value cache held in 8 bits ----
+
+def make_attn_desc(n_q_heads: int, n_kv_heads: int, head_dim: int, in_dtype: int = GDN_BF16,
+                   scale: Optional[float] = None) -> gdn_attn_desc:
+    """scale: 1 / sqrt(head_dim) unless given."""
+    return gdn_attn_desc(n_q_heads, n_kv_heads, head_dim, in_dtype, head_dim ** -0.5 if scale is None else scale)
+
+
+def gdn_attn_desc_check(desc: gdn_attn_desc) -> int:
+    return int(load_library().gdn_attn_desc_check(ctypes.byref(desc)))
+
+
+def _same_shape(name: str, t: torch.Tensor, shape, dtype):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+class KvCache:
+    """A key/value cache: device buffers held by PyTorch plus the C struct.
+
+    KvCache(desc, n_pages, n_slots, max_blocks) allocates every buffer and empties the cache. With buffers given by
+    name it wraps those as they are and allocates nothing (a buffer that no call on this handle needs may be left
+    out)."""
+
+    def __init__(self, desc: gdn_attn_desc, n_pages: int, n_slots: int, max_blocks: int, device=None, stream=None,
+                 **buffers: torch.Tensor):
+        device = torch.device(device or "cuda")
+        Hkv, d, dt = desc.n_kv_heads, desc.head_dim, _TORCH_DT[desc.in_dtype]
+        shapes = {"k": ((n_pages, Hkv, GDN_KV_BLOCK, d), torch.int8), "v": ((n_pages, Hkv, GDN_KV_BLOCK, d), torch.int8),
+                  "k_scale": ((n_pages, Hkv), torch.float32), "v_scale": ((n_pages, Hkv), torch.float32),
+                  "tail": ((n_slots, 2, 2, Hkv, GDN_KV_BLOCK, d), dt), "state": ((n_slots, 2), torch.int32),
+                  "table": ((n_slots, max_blocks), torch.int32), "free": ((n_pages,), torch.int32),
+                  "n_free": ((1,), torch.int32), "refs": ((n_pages,), torch.int32)}
+        unknown = set(buffers) - set(shapes)
+        if unknown:
+            raise ValueError(f"unknown buffers: {sorted(unknown)}")
+        self.desc, self.n_pages, self.n_slots, self.max_blocks = desc, n_pages, n_slots, max_blocks
+        for name, (shape, dtype) in shapes.items():
+            if buffers:
+                t = buffers.get(name)
+                if t is not None:
+                    _same_shape(name, t, shape, dtype)
+            else:
+                t = torch.empty(shape, dtype=dtype, device=device)
+            setattr(self, name, t)
+        self.c = gdn_kv_cache(*[_ptr(getattr(self, n)) for n in shapes], n_pages, n_slots, max_blocks)
+        if not buffers:
+            gdn_kv_cache_init(desc, self, stream)
+
+
+class KvPlan:
+    """A plan's buffers plus the C struct; KvPlan.new(max_tokens, max_requests) allocates them."""
+
+    def __init__(self, rows: torch.Tensor, units: torch.Tensor, counts: torch.Tensor):
+        for name, t, shape in (("rows", rows, rows.shape[:1]), ("units", units, (units.shape[0], 8)),
+                               ("counts", counts, (2,))):
+            _same_shape(name, t, shape, torch.int32)
+        self.rows, self.units, self.counts = rows, units, counts
+        self.c = gdn_kv_map(_ptr(rows), _ptr(units), _ptr(counts), rows.shape[0] - 1, units.shape[0])
+
+    @classmethod
+    def new(cls, max_tokens: int, max_requests: int, device=None) -> "KvPlan":
+        z = lambda *s: torch.zeros(s, dtype=torch.int32, device=device or "cuda")   # noqa: E731
+        return cls(z(max_requests + 1), z(gdn_kv_max_units(max_tokens, max_requests), 8), z(2))
+
+
+def gdn_kv_max_units(max_tokens: int, max_requests: int) -> int:
+    return int(load_library().gdn_kv_max_units(max_tokens, max_requests))
+
+
+def gdn_kv_cache_init(desc, cache: KvCache, stream=None):
+    _check(load_library().gdn_kv_cache_init(ctypes.byref(desc), ctypes.byref(cache.c), _stream(stream)))
+
+
+def gdn_kv_plan(desc, cache: KvCache, slots: torch.Tensor, n_new: torch.Tensor, plan: KvPlan,
+                state_out: Optional[torch.Tensor] = None, n_free_out: Optional[torch.Tensor] = None, stream=None):
+    """slots, n_new: int32 [n_requests] on the GPU. Advances the cache in place unless state_out / n_free_out are given."""
+    n = slots.shape[0]
+    if slots.dtype != torch.int32 or n_new.dtype != torch.int32 or n_new.shape != slots.shape:
+        raise ValueError("slots and n_new must be int32 of one length")
+    _check(load_library().gdn_kv_plan(ctypes.byref(desc), ctypes.byref(cache.c), _ptr(slots), _ptr(n_new), n,
+                                      ctypes.byref(plan.c), _ptr(state_out), _ptr(n_free_out), _stream(stream)))
+
+
+def gdn_kv_status(plan: KvPlan, stream=None) -> int:
+    """GDN_OK, or GDN_ERR_CAPACITY if the last plan did not fit its cache (synchronises)."""
+    return int(load_library().gdn_kv_status(ctypes.byref(plan.c), _stream(stream)))
+
+
+def _check_rows(desc, n_rows: int, dtype, **arrays):
+    for name, (t, heads) in arrays.items():
+        if t.dtype != dtype or tuple(t.shape) != (n_rows, heads, desc.head_dim):
+            raise ValueError(f"{name} must be {dtype} {[n_rows, heads, desc.head_dim]}, got {t.dtype} {list(t.shape)}")
+
+
+def gdn_kv_append(desc, cache: KvCache, plan: KvPlan, k: torch.Tensor, v: torch.Tensor, stream=None):
+    """k, v: [n_rows][Hkv][d] in the plan's row order."""
+    n, Hkv = k.shape[0], desc.n_kv_heads
+    _check_rows(desc, n, _TORCH_DT[desc.in_dtype], k=(k, Hkv), v=(v, Hkv))
+    _check(load_library().gdn_kv_append(ctypes.byref(desc), ctypes.byref(cache.c), ctypes.byref(plan.c), _ptr(k),
+                                        _ptr(v), n, _stream(stream)))
+
+
+def gdn_kv_attention_workspace(desc, max_tokens: int, max_requests: int, max_len: int) -> int:
+    return int(load_library().gdn_kv_attention_workspace(ctypes.byref(desc), max_tokens, max_requests, max_len))
+
+
+def gdn_kv_attention_workspace_min(desc, max_len: int) -> int:
+    return int(load_library().gdn_kv_attention_workspace_min(ctypes.byref(desc), max_len))
+
+
+def kv_attention_workspace(desc, max_tokens: int, max_requests: int, max_len: int, device=None) -> torch.Tensor:
+    n = gdn_kv_attention_workspace(desc, max_tokens, max_requests, max_len)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def gdn_kv_attention(desc, cache: KvCache, plan: KvPlan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     out: torch.Tensor, ws: Optional[torch.Tensor], max_new: int, max_len: int, stream=None):
+    """q, out: [n_rows][Hq][d]; k, v: the arrays given to gdn_kv_append; max_new, max_len: bounds over the batch."""
+    n, Hq, Hkv = q.shape[0], desc.n_q_heads, desc.n_kv_heads
+    _check_rows(desc, n, _TORCH_DT[desc.in_dtype], q=(q, Hq), k=(k, Hkv), v=(v, Hkv), out=(out, Hq))
+    _check(load_library().gdn_kv_attention(ctypes.byref(desc), ctypes.byref(cache.c), ctypes.byref(plan.c), _ptr(q),
+                                           _ptr(k), _ptr(v), _ptr(out), n, max_new, max_len, _ptr(ws),
+                                           ws.numel() if ws is not None else 0, _stream(stream)))
+
+
+def gdn_kv_fork(desc, cache: KvCache, src_slot: int, dst_slot: int, stream=None):
+    _check(load_library().gdn_kv_fork(ctypes.byref(desc), ctypes.byref(cache.c), src_slot, dst_slot, _stream(stream)))
+
+
+def gdn_kv_release(desc, cache: KvCache, slot: int, stream=None):
+    _check(load_library().gdn_kv_release(ctypes.byref(desc), ctypes.byref(cache.c), slot, _stream(stream)))
+
+
 def gdn_state_blob_bytes(desc) -> int:
     return int(load_library().gdn_state_blob_bytes(ctypes.byref(desc)))
 
@@ -374,11 +542,11 @@ def gdn_timing_begin(max_launches: int):
 
 def gdn_timing_end() -> dict:
     """{kind: (launches, timed launches, total device ms)} since gdn_timing_begin."""
-    arr = (gdn_kernel_time * 8)()
+    arr = (gdn_kernel_time * 16)()
     n = ctypes.c_int32(0)
-    _check(load_library().gdn_timing_end(arr, 8, ctypes.byref(n)))
+    _check(load_library().gdn_timing_end(arr, 16, ctypes.byref(n)))
     return {arr[i].name.decode(): (int(arr[i].launches), int(arr[i].timed), float(arr[i].total_ms))
-            for i in range(min(n.value, 8))}
+            for i in range(min(n.value, 16))}
 
 
 def gdn_device_status(stream=None) -> int:

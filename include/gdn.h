@@ -56,7 +56,8 @@ typedef enum gdn_status {
     GDN_ERR_CUDA = 6,           /* a CUDA call or launch failed */
     GDN_ERR_TIMEOUT = 7,        /* a bounded device wait ran out (see gdn_device_status) */
     GDN_ERR_NOT_FOUND = 8,      /* no saved state at the given path */
-    GDN_ERR_IO = 9              /* a file could not be written or read */
+    GDN_ERR_IO = 9,             /* a file could not be written or read */
+    GDN_ERR_CAPACITY = 10       /* a batch does not fit its key/value cache (see gdn_kv_status) */
 } gdn_status;
 
 enum { GDN_FP32 = 0, GDN_BF16 = 1 };
@@ -305,6 +306,137 @@ gdn_status gdn_decode_step(const gdn_layer_desc *desc, gdn_session *sessions, in
 gdn_status gdn_gates(const gdn_layer_desc *desc, const float *a, const float *b, const float *A_log,
                      const float *dt_bias, int64_t n_tokens, float *g, float *beta, gdn_stream_t stream);
 
+/* ---- Attention over a paged key/value cache held in 8 bits ----
+ *
+ * The full-attention layers beside the GDN layers of a hybrid model: their
+ * sessions' keys and values, and the attention of new tokens over them. Sources:
+ * the attention layers' KV rows per session ("The shadow reader", section "One
+ * session's state"), an 8-bit KV cache and split-K attention whose merge order
+ * depends on positions only ("Long context and sessions").
+ *
+ * A cache holds sessions ("slots") in blocks of GDN_KV_BLOCK tokens at absolute
+ * positions. A complete block lives in a page as int8, [Hkv][64][d] for keys
+ * and for values, with one fp32 scale per (page, head): scale = absmax / 127
+ * over the block's 64 d elements, q = x / scale rounded to nearest even, value =
+ * q * scale (all zero: scale 0). Keys and values are finite; a NaN is held as 0 and an infinity
+ * as 127 times a scale taken from the block's finite elements. The open block at a slot's end is kept in
+ * in_dtype as it came, in the slot's tail. A query at position p reads the
+ * blocks before its own (p / 64) from 8 bits and its own block's positions
+ * <= p as they came. So the pages' content and every row of the attention
+ * depend on the session's tokens and positions only, not on how they were split
+ * into calls; a complete block never changes, and forks share its page.
+ *
+ * One step for a batch of requests, whether prompts or single tokens:
+ *   gdn_kv_plan       from the slots' lengths and the counts of new tokens: pages, block tables, unit map
+ *   gdn_kv_append     the new keys and values into pages and tails
+ *   gdn_kv_attention  the new tokens' queries over the cache and the new keys and values
+ * Lengths, tables and the free pages are device memory and no call reads them
+ * on the host, so a step can be captured in a CUDA graph and replayed: each
+ * replay advances the slots. Calls that touch one cache are ordered by their
+ * stream (or by the caller's events); calls on one cache must not overlap. */
+#define GDN_KV_BLOCK 64
+#define GDN_KV_MAX_REQUESTS 4096
+
+typedef struct gdn_attn_desc {
+    int32_t n_q_heads;  /* Hq, a multiple of Hkv: query head h reads key/value head h / (Hq / Hkv) */
+    int32_t n_kv_heads; /* Hkv >= 1 */
+    int32_t head_dim;   /* d: 64, 128 or 256 */
+    int32_t in_dtype;   /* GDN_BF16 or GDN_FP32: q, k, v, the tails and out */
+    float scale;        /* multiplies q . k (1 / sqrt(d) usually), finite and > 0 */
+} gdn_attn_desc;
+
+/* A cache: caller-owned device buffers (16-byte aligned; int32 ones 8-byte) and
+ * their sizes. gdn_kv_cache_init sets an empty one up. */
+typedef struct gdn_kv_cache {
+    int8_t *k, *v;         /* [n_pages][Hkv][64][d] */
+    float *k_scale;        /* [n_pages][Hkv] */
+    float *v_scale;
+    void *tail;            /* in_dtype [n_slots][2][2][Hkv][64][d]: (slot, buffer, k then v): the open block */
+    int32_t *state;        /* [n_slots][2]: tokens held; the tail buffer (0 or 1) of the open block */
+    int32_t *table;        /* [n_slots][max_blocks]: page of each complete block */
+    int32_t *free_pages;   /* [n_pages]: stack of free pages, entries [0, *n_free) valid, popped from the end */
+    int32_t *n_free;       /* [1] */
+    int32_t *refs;         /* [n_pages]: slots that name the page */
+    int32_t n_pages, n_slots, max_blocks;
+} gdn_kv_cache;
+
+/* A plan's device buffers: rows [max_requests + 1] (prefix sums of the new
+ * tokens), units [max_units][8] and counts [2] = {units, status}. A unit is the
+ * new tokens of one request inside one block, in request and position order:
+ * {slot, block, page or -1 while the block stays open, offset of the first new
+ * token, their number, row of the first one in the packed inputs, tail buffer
+ * that holds the block's earlier tokens, tail buffer that receives an open
+ * block's tokens or -1}. gdn_kv_max_units() of a batch is enough for max_units. */
+typedef struct gdn_kv_map {
+    int32_t *rows, *units, *counts;
+    int32_t max_requests, max_units;
+} gdn_kv_map;
+
+/* GDN_OK if the description is supported. */
+gdn_status gdn_attn_desc_check(const gdn_attn_desc *desc);
+
+/* Units that max_requests requests of max_tokens new tokens in total can have. */
+int32_t gdn_kv_max_units(int64_t max_tokens, int32_t max_requests);
+
+/* Empties the cache: every slot of length 0, every page free (page 0 is popped first). */
+gdn_status gdn_kv_cache_init(const gdn_attn_desc *desc, const gdn_kv_cache *cache, gdn_stream_t stream);
+
+/* Plans n_requests requests: slots, n_new: int32 device [n_requests], distinct
+ * slots and their numbers of new tokens (0 allowed). Writes the map, the
+ * block-table entries, reference counts and free pages' height of the blocks
+ * that complete, and the slots' new states. state_out [n_slots][2] and
+ * n_free_out [1] receive the advanced states (of the listed slots only) and
+ * height; NULL, or the cache's own buffers, advances the cache in place.
+ * A batch that does not fit changes nothing, has no units (later calls with
+ * this map do nothing) and leaves the reason in counts[1] (gdn_kv_status). */
+gdn_status gdn_kv_plan(const gdn_attn_desc *desc, const gdn_kv_cache *cache, const int32_t *slots,
+                       const int32_t *n_new, int32_t n_requests, const gdn_kv_map *map, int32_t *state_out,
+                       int32_t *n_free_out, gdn_stream_t stream);
+
+/* Outcome of the last plan written to `map` (synchronises `stream`): GDN_OK, or
+ * GDN_ERR_CAPACITY with the reason: too few free pages, a request past
+ * max_blocks, too few units, or a slot or count out of range. */
+gdn_status gdn_kv_status(const gdn_kv_map *map, gdn_stream_t stream);
+
+/* Writes the planned tokens' keys and values, in_dtype [n_rows][Hkv][d] in the
+ * plan's row order: complete blocks quantised into their pages (with the
+ * block's earlier tokens from the tail), open blocks' tokens into the tail. */
+gdn_status gdn_kv_append(const gdn_attn_desc *desc, const gdn_kv_cache *cache, const gdn_kv_map *map, const void *k,
+                         const void *v, int64_t n_rows, gdn_stream_t stream);
+
+/* Workspace of an attention call over up to max_tokens new tokens of up to
+ * max_requests requests and up to max_len tokens per slot. A smaller workspace
+ * of at least gdn_kv_attention_workspace_min bytes works in more launches.
+ * Scratch of one call, 16-byte aligned; nothing to clear. */
+size_t gdn_kv_attention_workspace(const gdn_attn_desc *desc, int64_t max_tokens, int32_t max_requests,
+                                  int64_t max_len);
+size_t gdn_kv_attention_workspace_min(const gdn_attn_desc *desc, int64_t max_len);
+
+/* Attention of the planned tokens, after their append: q, out in_dtype
+ * [n_rows][Hq][d]; k, v the arrays given to the append. max_new bounds every
+ * request's new tokens and max_len every slot's length after the plan (they
+ * size the launches; a unit outside them is left out and reported by
+ * gdn_device_status). Rows of out that belong to no unit are untouched.
+ * Softmax, sums and outputs are accumulated in fp32. With bf16 inputs the
+ * weights enter the second product rounded to bf16; fp32 inputs run in fp32
+ * throughout. Deterministic; a row's bits depend on the session and on whether
+ * the call is of the few-row form (max_new * Hq / Hkv <= 16), not on the rest
+ * of the batch. */
+gdn_status gdn_kv_attention(const gdn_attn_desc *desc, const gdn_kv_cache *cache, const gdn_kv_map *map,
+                            const void *q, const void *k, const void *v, void *out, int64_t n_rows, int32_t max_new,
+                            int64_t max_len, void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/* dst becomes a copy of src: it drops what it held, shares src's complete
+ * blocks (their pages go back to the free stack when no slot names them any
+ * more) and gets its own copy of the open block. A checkpoint, a restore or a
+ * fork of a session, as gdn_state_capture / gdn_state_restore are for its
+ * recurrent states. */
+gdn_status gdn_kv_fork(const gdn_attn_desc *desc, const gdn_kv_cache *cache, int32_t src_slot, int32_t dst_slot,
+                       gdn_stream_t stream);
+
+/* Empties a slot; pages that no other slot names go back to the free stack. */
+gdn_status gdn_kv_release(const gdn_attn_desc *desc, const gdn_kv_cache *cache, int32_t slot, gdn_stream_t stream);
+
 /* Per-kernel timing with CUDA events, for benchmarks (off by default).
  * gdn_timing_begin(max_launches) creates 2 * max_launches events and starts
  * recording: every kernel the library launches afterwards, on whatever stream
@@ -317,7 +449,8 @@ gdn_status gdn_gates(const gdn_layer_desc *desc, const float *a, const float *b,
 typedef struct gdn_kernel_time {
     char name[32];        /* kernel kind: prep_wy, prep_wy_tail (the prologue of a call's last blocks, run
                              beside the state pass of its first ones), conv_commit, state_output, state_copy,
-                             decode, gates */
+                             decode, gates, prefill_fused, kv_plan, kv_append, kv_state (init, forks, releases),
+                             kv_attention, kv_join */
     int64_t launches;     /* launches while recording */
     int64_t timed;        /* launches with an event pair */
     double total_ms;      /* summed device time of the timed launches */
@@ -331,7 +464,8 @@ gdn_status gdn_timing_end(gdn_kernel_time *out, int32_t max_kinds, int32_t *n_ki
  * of hanging; they then record the fact in a device error word, leave their
  * results incomplete and exit. This call synchronises `stream`, reads and
  * clears that word, and returns GDN_ERR_TIMEOUT if it was set, else GDN_OK.
- * (A timeout does not happen in normal operation.) */
+ * (A timeout does not happen in normal operation.) GDN_ERR_INVALID_ARG: a
+ * key/value plan's unit or page lay outside the sizes given with a call. */
 gdn_status gdn_device_status(gdn_stream_t stream);
 
 /* Test hook for the timeout path above: while enabled, prefill launches of the
