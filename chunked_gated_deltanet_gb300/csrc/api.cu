@@ -690,7 +690,7 @@ GDN_API gdn_status gdn_debug_inject_wait_timeout(int32_t enable, int64_t wait_li
         return GDN_OK;
     }
     if (wait_limit < 1) return fail(GDN_ERR_INVALID_ARG, "wait_limit must be >= 1");
-    if (enable != 1 && enable != 2) return fail(GDN_ERR_INVALID_ARG, "enable must be 0, 1 or 2");
+    if (enable < 1 || enable > 3) return fail(GDN_ERR_INVALID_ARG, "enable must be 0, 1, 2 or 3");
     g_skip_first_copy = enable;
     g_wait_limit = wait_limit;
     return GDN_OK;

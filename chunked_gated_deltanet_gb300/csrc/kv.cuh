@@ -71,7 +71,8 @@ struct KvAttn {
     int tok_stride;                 // most tokens of a unit: min(64, max_new)
     int seg_blocks, n_seg;          // keys [s * seg_blocks, (s + 1) * seg_blocks) * 64 belong to segment s
     int max_new;                    // the caller's bound on a request's new tokens
-    long long wait_limit;
+    long long wait_limit;           // polls before a bounded wait gives up
+    int skip_first_copy;            // test hook: 3 = the prompt kernel never announces its first key tile
     unsigned int *err;
 };
 
@@ -94,5 +95,7 @@ cudaError_t gdn_launch_kv_init(const gdn::KvCache &c, cudaStream_t st);
 // rows_max: the most rows (new tokens of one block x G) of a unit; few: the few-row form
 cudaError_t gdn_launch_kv_attn_simt(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int rows_max, int few,
                                     cudaStream_t st);
+// The many-row form for bf16 inputs, over n_units units from a.unit0.
+cudaError_t gdn_launch_kv_attn_prompt(const gdn::KvAttn &a, int d, int n_units, cudaStream_t st);
 // Joins the segments' partial results of every row that has more than one.
 cudaError_t gdn_launch_kv_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, cudaStream_t st);

@@ -210,6 +210,7 @@ GDN_API gdn_status gdn_kv_attention(const gdn_attn_desc *d, const gdn_kv_cache *
     a.seg_blocks = f.seg_blocks; a.n_seg = (int)f.n_seg;
     a.max_new = max_new; a.tok_stride = f.tok_stride;
     a.wait_limit = g_wait_limit;
+    a.skip_first_copy = g_skip_first_copy;
     cudaError_t e = gdn_device_error_word(&a.err);
     if (e != cudaSuccess) return cuda_fail(e, "device error word lookup");
     cudaStream_t cst = (cudaStream_t)stream;
@@ -222,7 +223,10 @@ GDN_API gdn_status gdn_kv_attention(const gdn_attn_desc *d, const gdn_kv_cache *
             a.part_ml = reinterpret_cast<float2 *>(ws);
             a.part_o = reinterpret_cast<float *>(ws + (((size_t)f.n_seg * a.part_rows * sizeof(float2) + 255) & ~size_t(255)));
         }
-        e = launch_k(K_KV_ATTN, cst, [&] { return gdn_launch_kv_attn_simt(a, d->head_dim, bf16, n, f.rows_max, f.few, cst); });
+        e = launch_k(K_KV_ATTN, cst, [&] {
+            return bf16 && !f.few ? gdn_launch_kv_attn_prompt(a, d->head_dim, n, cst)
+                                  : gdn_launch_kv_attn_simt(a, d->head_dim, bf16, n, f.rows_max, f.few, cst);
+        });
         if (e != cudaSuccess) return cuda_fail(e, "attention kernel");
         if (f.n_seg > 1) {
             e = launch_k(K_KV_JOIN, cst, [&] { return gdn_launch_kv_join(a, d->head_dim, bf16, n, cst); });

@@ -555,5 +555,5 @@ def gdn_device_status(stream=None) -> int:
 
 
 def gdn_debug_inject_wait_timeout(enable: int, wait_limit: int = 1000):
-    """enable: 0 off, 1 the state kernel, 2 the tcgen05 prologue skips its first copy."""
+    """enable: 0 off, 1 the state kernel, 2 the tcgen05 prologue, 3 the tcgen05 attention skips its first copy."""
     _check(load_library().gdn_debug_inject_wait_timeout(int(enable), wait_limit))

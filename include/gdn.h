@@ -471,9 +471,9 @@ gdn_status gdn_device_status(gdn_stream_t stream);
 /* Test hook for the timeout path above: while enabled, prefill launches of the
  * bf16 path give up after `wait_limit` polls, and one kernel never issues its
  * first operand copy, so its wait runs out without any fault: enable = 1, the
- * state kernel; enable = 2, the tcgen05 prologue (d_k = d_v = 128). enable = 0
- * restores normal operation; other values are refused with
- * GDN_ERR_INVALID_ARG. Process-global; for tests only. */
+ * state kernel; enable = 2, the tcgen05 prologue (d_k = d_v = 128); enable = 3,
+ * the tcgen05 attention kernel. enable = 0 restores normal operation; other
+ * values are refused with GDN_ERR_INVALID_ARG. Process-global; for tests only. */
 gdn_status gdn_debug_inject_wait_timeout(int32_t enable, int64_t wait_limit);
 
 /* Message of the last failing call on this host thread ("" if none). */

@@ -238,3 +238,23 @@ def test_other_streams(cuda_device):
             got = b.step([0], [new], data=data)
         side.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_wait_timeout_is_reported_and_context_survives(cuda_device, d):
+    """The tcgen05 attention's waits are bounded: with its first key tile never announced they run out, the status says
+    so, and the next call is right."""
+    m = Model((8, 2), d, BF, seed=8)
+    gdn.gdn_debug_inject_wait_timeout(3, 2000)
+    try:
+        q, k = m.draw(300, 8).cuda(), m.draw(300, 2).cuda()
+        plan, out = gdn.KvPlan.new(300, 1), torch.zeros_like(q)
+        gdn.gdn_kv_plan(m.desc, m.cache, m.i32([4]), m.i32([300]), plan)
+        gdn.gdn_kv_append(m.desc, m.cache, plan, k, k)
+        gdn.gdn_kv_attention(m.desc, m.cache, plan, q, k, k, out, None, 300, 300)
+        status = gdn.gdn_device_status()
+    finally:
+        gdn.gdn_debug_inject_wait_timeout(0)
+    assert status == gdn.GDN_ERR_TIMEOUT
+    assert gdn.gdn_device_status() == gdn.GDN_OK
+    m.step([1], [200])
