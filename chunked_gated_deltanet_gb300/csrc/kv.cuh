@@ -92,10 +92,12 @@ cudaError_t gdn_launch_kv_append(const gdn::KvCache &c, const int32_t *units, co
 cudaError_t gdn_launch_kv_fork(const gdn::KvCache &c, int src, int dst, int Hkv, int d, int elt, cudaStream_t st);
 cudaError_t gdn_launch_kv_release(const gdn::KvCache &c, int slot, cudaStream_t st);
 cudaError_t gdn_launch_kv_init(const gdn::KvCache &c, cudaStream_t st);
-// rows_max: the most rows (new tokens of one block x G) of a unit; few: the few-row form
-cudaError_t gdn_launch_kv_attn_simt(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int rows_max, int few,
-                                    cudaStream_t st);
-// The many-row form for bf16 inputs, over n_units units from a.unit0.
-cudaError_t gdn_launch_kv_attn_prompt(const gdn::KvAttn &a, int d, int n_units, cudaStream_t st);
+// Attention over unit_bound units from a.unit0. rows_max: the most rows (new tokens of one block x G) of a unit.
+// fp32 inputs, few rows or many:
+cudaError_t gdn_launch_kv_attn_simt(const gdn::KvAttn &a, int d, int unit_bound, int rows_max, int few, cudaStream_t st);
+// bf16 inputs, rows_max <= 16:
+cudaError_t gdn_launch_kv_attn_token(const gdn::KvAttn &a, int d, int unit_bound, int rows_max, cudaStream_t st);
+// bf16 inputs, many rows:
+cudaError_t gdn_launch_kv_attn_prompt(const gdn::KvAttn &a, int d, int unit_bound, cudaStream_t st);
 // Joins the segments' partial results of every row that has more than one.
 cudaError_t gdn_launch_kv_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, cudaStream_t st);

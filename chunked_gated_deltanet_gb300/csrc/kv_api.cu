@@ -214,7 +214,7 @@ GDN_API gdn_status gdn_kv_attention(const gdn_attn_desc *d, const gdn_kv_cache *
     cudaError_t e = gdn_device_error_word(&a.err);
     if (e != cudaSuccess) return cuda_fail(e, "device error word lookup");
     cudaStream_t cst = (cudaStream_t)stream;
-    const int bf16 = d->in_dtype == GDN_BF16;
+    const bool bf16 = d->in_dtype == GDN_BF16;
     for (int64_t u0 = 0; u0 < bound; u0 += per_launch) {
         const int n = (int)std::min(per_launch, bound - u0);
         a.unit0 = (int)u0;
@@ -224,8 +224,9 @@ GDN_API gdn_status gdn_kv_attention(const gdn_attn_desc *d, const gdn_kv_cache *
             a.part_o = reinterpret_cast<float *>(ws + (((size_t)f.n_seg * a.part_rows * sizeof(float2) + 255) & ~size_t(255)));
         }
         e = launch_k(K_KV_ATTN, cst, [&] {
-            return bf16 && !f.few ? gdn_launch_kv_attn_prompt(a, d->head_dim, n, cst)
-                                  : gdn_launch_kv_attn_simt(a, d->head_dim, bf16, n, f.rows_max, f.few, cst);
+            if (!bf16) return gdn_launch_kv_attn_simt(a, d->head_dim, n, f.rows_max, f.few, cst);
+            return f.few ? gdn_launch_kv_attn_token(a, d->head_dim, n, f.rows_max, cst)
+                         : gdn_launch_kv_attn_prompt(a, d->head_dim, n, cst);
         });
         if (e != cudaSuccess) return cuda_fail(e, "attention kernel");
         if (f.n_seg > 1) {

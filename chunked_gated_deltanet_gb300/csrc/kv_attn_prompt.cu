@@ -23,8 +23,7 @@
 // below 2^8, and O is rescaled (by the softmax warps, after the products before it) only then. Every decision is a row's
 // own and every block is one softmax step, so a row's bits do not depend on the rows beside it.
 // Bound: tensor pipe; per 128 keys and 128 rows the MMAs take 4 * 128 * 128 * d / 8192 cycles (1,024 for d = 128).
-#include "kv.cuh"
-#include "mma.cuh"
+#include "kv_attn.cuh"
 #include "umma.cuh"
 
 #include <algorithm>
@@ -46,38 +45,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// 4 int8 -> 4 bf16, exact: with a byte b under the upper byte 0x43 a bf16 reads 128 + (b & 127) once bit 7 (which is the
-// exponent's lowest) is cleared, and 128 or 256 from bit 7 alone; their difference is the signed value.
-__device__ __forceinline__ uint2 i8_to_bf16x4(uint32_t x) {
-    uint2 o;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t w = __byte_perm(x, 0x43434343u, i == 0 ? 0x4140 : 0x4342);
-        const uint32_t a = w & 0xFF7FFF7Fu, b = w & 0xFF80FF80u;
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
-        (i == 0 ? o.x : o.y) = *reinterpret_cast<const uint32_t *>(&d);
-    }
-    return o;
-}
-
 // named barrier `id` over n threads (whole warps)
 __device__ __forceinline__ void kv_named_barrier(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
-
-// 4 int8 -> 4 fp16, exact: 0x6400 | (b ^ 0x80) is 1024 + b + 128.
-__device__ __forceinline__ uint2 i8_to_f16x4(uint32_t x) {
-    x ^= 0x80808080u;
-    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
-    const uint32_t off = 0x64806480u;
-    const __half2 c = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&off));
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&b), *reinterpret_cast<const __half2 *>(&off));
-    return make_uint2(*reinterpret_cast<const uint32_t *>(&c), *reinterpret_cast<const uint32_t *>(&d));
-}
 
 template <int D>
 struct PromptPlan {
@@ -113,17 +82,6 @@ struct HalfInfo {
     float c, lvs, ivs;
 };
 
-// log2 of the value scale of block b of a slot; an all-zero block (any scale serves) counts with the nearest of the eight
-// blocks before it that has one
-__device__ __forceinline__ float kv_log2_vscale(const KvAttn &a, const int32_t *table, int b, int h) {
-    for (int i = 0; i <= 8 && b >= 0; ++i, --b) {
-        const int page = table[b];
-        if ((unsigned)page >= (unsigned)a.c.n_pages) break;
-        const float vs = a.c.v_scale[(int64_t)page * a.Hkv + h];
-        if (vs != 0.f) return log2f(vs);
-    }
-    return 0.f;
-}
 
 template <int D>
 __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(const KvAttn a, int row_tiles, int span, int n_units) {

@@ -312,10 +312,8 @@ cudaError_t launch_join(const KvAttn &a, int unit_bound, cudaStream_t st) {
 
 }  // namespace gdn
 
-cudaError_t gdn_launch_kv_attn_simt(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int rows_max, int few,
-                                    cudaStream_t st) {
-    return bf16 ? gdn::launch_simt_d<__nv_bfloat16>(a, d, unit_bound, rows_max, few, st)
-                : gdn::launch_simt_d<float>(a, d, unit_bound, rows_max, few, st);
+cudaError_t gdn_launch_kv_attn_simt(const gdn::KvAttn &a, int d, int unit_bound, int rows_max, int few, cudaStream_t st) {
+    return gdn::launch_simt_d<float>(a, d, unit_bound, rows_max, few, st);
 }
 
 cudaError_t gdn_launch_kv_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, cudaStream_t st) {
