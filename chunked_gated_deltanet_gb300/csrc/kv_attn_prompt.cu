@@ -27,6 +27,7 @@
 #include "umma.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gdn {
 
@@ -249,31 +250,80 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             else if (s == n_seq - 1) { kv = 1; step = steps - 1; }
             else { kv = (s + 1) & 1; step = (s + 1) / 2 - kv; }
         };
-        // 16-byte loads of tile (kv, step): load j is 8 keys x 64 columns, j = cw + CW i of (half, key group, column group)
-        uint4 nxt[P::kLoads];
+        // 16-byte loads of tile (kv, step): load i of this warp is 8 keys x 64 columns, number cw + CW i of (half, key group,
+        // column group). Both loops are unrolled over the loads only: the roles share the instruction cache.
+        uint4 w[P::kLoads];
         auto load8 = [&](int kv, int step) {
-            const int8_t *pool = kv ? a.c.v : a.c.k;
+            const int8_t *pool = (kv ? a.c.v : a.c.k) + (int64_t)h * (kKvBlock * D) + kr * D + ch * 16;
+            const int64_t stride = (int64_t)a.Hkv * (kKvBlock * D);
+            const int8_t *base[2];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) base[hh] = pool + half[min(2 * step + hh, nh - 1)].page * stride;
 #pragma unroll
             for (int i = 0; i < P::kLoads; ++i) {
-                const int j = cw + P::CW * i, hh = j / (8 * P::kVec), kg = j / P::kVec % 8, dg = j % P::kVec, hi = 2 * step + hh;
-                if (hi < n8)
-                    nxt[i] = __ldg(reinterpret_cast<const uint4 *>(pool + ((int64_t)half[hi].page * a.Hkv + h) * (kKvBlock * D) +
-                                                                   (kg * 8 + kr) * D + dg * 64 + ch * 16));
+                const int j = cw + P::CW * i, hh = P::CW * i / (8 * P::kVec), kg = j / P::kVec % 8, dg = j % P::kVec;
+                w[i] = __ldg(reinterpret_cast<const uint4 *>(base[hh] + kg * (8 * D) + dg * 64));
+            }
+        };
+        auto store8 = [&](auto is_v, unsigned char *dst, int n_half) {
+            constexpr bool f16 = decltype(is_v)::value;
+#pragma unroll
+            for (int i = 0; i < P::kLoads; ++i) {
+                const int j = cw + P::CW * i, hh = P::CW * i / (8 * P::kVec), kg = j / P::kVec % 8, dg = j % P::kVec;
+                if (hh >= n_half) break;
+                uint4 lo, hi;
+                if (f16) {
+                    const uint2 x0 = i8_to_f16x4(w[i].x), x1 = i8_to_f16x4(w[i].y), x2 = i8_to_f16x4(w[i].z), x3 = i8_to_f16x4(w[i].w);
+                    lo = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                    hi = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                } else {
+                    const uint2 x0 = i8_to_bf16x4(w[i].x), x1 = i8_to_bf16x4(w[i].y), x2 = i8_to_bf16x4(w[i].z), x3 = i8_to_bf16x4(w[i].w);
+                    lo = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                    hi = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                }
+                unsigned char *o = dst + (hh * 8 + kg) * (D * 16) + (dg * 8 + ch * 2) * 128 + kr * 16;
+                *reinterpret_cast<uint4 *>(o) = lo;
+                *reinterpret_cast<uint4 *>(o + 128) = hi;
+            }
+        };
+        // a raw block: the tail's rows, then the new ones, zero past the last
+        auto store_raw = [&](int kv, int hh, int block, unsigned char *dst) {
+#pragma unroll 1
+            for (int j = cw; j < 8 * P::kVec; j += P::CW) {
+                const int kg = j / P::kVec, dg = j % P::kVec, off = kg * 8 + kr, pos = block * kKvBlock + off;
+                const bf *src = nullptr;
+                if (pos < pos0) src = tail + kv_tail_offset(u.slot, u.src, kv, h, a.Hkv, D) + (int64_t)off * D;
+                else if (pos < pos0 + n_tok)
+                    src = static_cast<const bf *>(kv ? a.v_new : a.k_new) + ((int64_t)(u.row + pos - pos0) * a.Hkv + h) * D;
+                uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (src) {
+                    const uint4 *q4 = reinterpret_cast<const uint4 *>(src + dg * 64 + ch * 16);
+                    const uint4 y0 = q4[0], y1 = q4[1];
+                    x[0] = y0.x; x[1] = y0.y; x[2] = y0.z; x[3] = y0.w;
+                    x[4] = y1.x; x[5] = y1.y; x[6] = y1.z; x[7] = y1.w;
+                }
+                if (kv) {
+                    // a value that is not finite would reach rows that do not see it (0 * inf): left out here, and added by
+                    // the rows that do at the end
+                    bool any = false;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if ((x[k] & 0x7F80u) == 0x7F80u) { x[k] &= 0xFFFF0000u; any = true; }
+                        if ((x[k] & 0x7F800000u) == 0x7F800000u) { x[k] &= 0xFFFFu; any = true; }
+                    }
+                    if (any) atomicOr(&bad_v[block - blo], 1u);
+                }
+                unsigned char *o = dst + (hh * 8 + kg) * (D * 16) + (dg * 8 + ch * 2) * 128 + kr * 16;
+                *reinterpret_cast<uint4 *>(o) = make_uint4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4 *>(o + 128) = make_uint4(x[4], x[5], x[6], x[7]);
             }
         };
         load8(0, 0);
+#pragma unroll 1
         for (int s = 0; s < n_seq; ++s) {
             int kv, step;
             what(s, kv, step);
-            uint4 cur[P::kLoads];
-#pragma unroll
-            for (int i = 0; i < P::kLoads; ++i) cur[i] = nxt[i];
-            if (s + 1 < n_seq) {
-                int kv1, step1;
-                what(s + 1, kv1, step1);
-                load8(kv1, step1);
-            }
-            const int slot = step % NB;
+            const int slot = step % NB, n_half = min(max(n8 - 2 * step, 0), 2);
             if (step >= NB) {
                 if (!mbar_wait_bounded(&bar[(kv ? P::bVFree : P::bKFree) + slot], (step / NB - 1) & 1, limit)) {
                     alive = false;
@@ -281,52 +331,14 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 }
             }
             unsigned char *dst = sm + (kv ? P::kV : P::kK) + slot * P::kTile;
-#pragma unroll
-            for (int i = 0; i < P::kLoads; ++i) {
-                const int j = cw + P::CW * i, hh = j / (8 * P::kVec), kg = j / P::kVec % 8, dg = j % P::kVec, hi = 2 * step + hh;
-                if (hi >= nh) continue;
-                unsigned char *o = dst + (hh * 8 + kg) * (D * 16) + (dg * 8 + ch * 2) * 128 + kr * 16;
-                uint4 lo, hi4;
-                if (hi < n8) {
-                    const uint2 x0 = kv ? i8_to_f16x4(cur[i].x) : i8_to_bf16x4(cur[i].x);
-                    const uint2 x1 = kv ? i8_to_f16x4(cur[i].y) : i8_to_bf16x4(cur[i].y);
-                    const uint2 x2 = kv ? i8_to_f16x4(cur[i].z) : i8_to_bf16x4(cur[i].z);
-                    const uint2 x3 = kv ? i8_to_f16x4(cur[i].w) : i8_to_bf16x4(cur[i].w);
-                    lo = make_uint4(x0.x, x0.y, x1.x, x1.y);
-                    hi4 = make_uint4(x2.x, x2.y, x3.x, x3.y);
-                } else {
-                    // raw block: the tail's rows, then the new ones, zero past the last
-                    const int block = blo + hi - n8, off = kg * 8 + kr, pos = block * kKvBlock + off;
-                    const bf *src = nullptr;
-                    if (pos < pos0) src = tail + kv_tail_offset(u.slot, u.src, kv, h, a.Hkv, D) + (int64_t)off * D;
-                    else if (pos < pos0 + n_tok)
-                        src = static_cast<const bf *>(kv ? a.v_new : a.k_new) + ((int64_t)(u.row + pos - pos0) * a.Hkv + h) * D;
-                    lo = hi4 = make_uint4(0, 0, 0, 0);
-                    if (src) {
-                        const uint4 *p = reinterpret_cast<const uint4 *>(src + dg * 64 + ch * 16);
-                        lo = p[0];
-                        hi4 = p[1];
-                    }
-                    if (kv) {
-                        // a value that is not finite would reach rows that do not see it (0 * inf): left out here, and
-                        // added by the rows that do at the end
-                        uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi4.x, hi4.y, hi4.z, hi4.w};
-                        bool any = false;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            if ((w[k] & 0x7F80u) == 0x7F80u) { w[k] &= 0xFFFF0000u; any = true; }
-                            if ((w[k] & 0x7F800000u) == 0x7F800000u) { w[k] &= 0xFFFFu; any = true; }
-                        }
-                        if (any) {
-                            atomicOr(&bad_v[block - blo], 1u);
-                            lo = make_uint4(w[0], w[1], w[2], w[3]);
-                            hi4 = make_uint4(w[4], w[5], w[6], w[7]);
-                        }
-                    }
-                }
-                *reinterpret_cast<uint4 *>(o) = lo;
-                *reinterpret_cast<uint4 *>(o + 128) = hi4;
+            if (kv) store8(std::true_type{}, dst, n_half);
+            else store8(std::false_type{}, dst, n_half);
+            if (s + 1 < n_seq) {   // the next tile's loads are under way while this one is finished and the next slot waited for
+                int kv1, step1;
+                what(s + 1, kv1, step1);
+                load8(kv1, step1);
             }
+            for (int hh = n_half; hh < 2 && 2 * step + hh < nh; ++hh) store_raw(kv, hh, blo + 2 * step + hh - n8, dst);
             fence_proxy_async();
             if (s > 0 || a.skip_first_copy != 3) mbar_arrive(&bar[(kv ? P::bVFull : P::bKFull) + slot]);   // 3: the test hook
         }
@@ -346,11 +358,12 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             if (!alive) break;
             tc_fence_after();
             const int halves = min(2, nh - 2 * step);
-            for (int hh = 0; hh < halves; ++hh) {
+            auto half_step = [&](auto is_raw, int hh) {
+                constexpr bool raw = decltype(is_raw)::value;
                 const int hi = 2 * step + hh;
                 const HalfInfo x = half[hi];
                 // keys of the half that the row sees: all or none of an 8-bit block, up to its own offset of its raw block
-                const int see = hi < n8 ? (blk > c0 + hi ? kKvBlock : 0) : (blk == blo + hi - n8 ? off + 1 : 0);
+                const int see = raw ? (blk == blo + hi - n8 ? off + 1 : 0) : (blk > c0 + hi ? kKvBlock : 0);
                 float s[64];
                 {
                     uint32_t w[4][16];
@@ -363,7 +376,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                         for (int k = 0; k < 16; ++k) s[16 * j + k] = __uint_as_float(w[j][k]);
                     }
                 }
-                if (hi >= n8) {
+                if (raw) {
 #pragma unroll
                     for (int j = 0; j < 64; ++j) s[j] = j < see ? s[j] : -INFINITY;
                 }
@@ -379,10 +392,11 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 }
                 // O is rescaled once the products that are under way on it are done (a row's first keys meet O = 0)
                 if ((step > 0 || hh > 0) && __any_sync(0xffffffffu, f != 1.f)) {
-                    if (step > 0) alive = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bPV + 2 * tile + 1], (step - 1) & 1, limit));
-                    if (alive && hh == 1)
-                        alive = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bPV + 2 * tile], step & 1, limit));
-                    if (!alive) break;
+                    bool done = true;
+                    if (step > 0) done = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bPV + 2 * tile + 1], (step - 1) & 1, limit));
+                    if (done && hh == 1)
+                        done = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bPV + 2 * tile], step & 1, limit));
+                    if (!done) return false;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
@@ -395,11 +409,11 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                     }
                     tmem_wait_st();
                 }
-                // the weights (8-bit blocks: times the value scale, which the sum takes out again)
-                const bool raw = hi >= n8;
+                // the weights (8-bit blocks: times the value scale, which the sum takes out again); none of a block that
+                // the row does not see
                 const uint64_t cc = f2_pack(x.c, x.c);
-                const float base = (m == -INFINITY ? 0.f : m) - (raw ? 0.f : x.lvs);
-                const uint64_t bb = f2_pack(-base, -base);
+                const float add = see == 0 ? -INFINITY : (raw ? 0.f : x.lvs) - (m == -INFINITY ? 0.f : m);
+                const uint64_t bb = f2_pack(add, add);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -411,7 +425,6 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                         f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), cc, bb), p0, p1);
                         p0 = ex2(p0);
                         p1 = ex2(p1);
-                        if (see == 0) p0 = p1 = 0.f;
                         sum[k & 1] = f2_add(sum[k & 1], f2_pack(p0, p1));
                         if (raw) {
                             uint32_t x1;
@@ -430,7 +443,11 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&bar[P::bP + 2 * b + hh]);
-            }
+                return true;
+            };
+#pragma unroll 1
+            for (int hh = 0; alive && hh < halves; ++hh)
+                alive = 2 * step + hh < n8 ? half_step(std::false_type{}, hh) : half_step(std::true_type{}, hh);
         }
         // every product is done, and the convert warps have said what they left out: the rows
         kv_named_barrier(1, P::kMma);
