@@ -1,28 +1,32 @@
 // Attention of many query rows over the paged 8-bit key/value cache on the 5th-generation tensor core (bf16 inputs).
 //
-// The mathematics is that of kv_attn_simt.cu; here the two products of a step of 128 keys are tcgen05 MMAs:
-//   S = Q K^T     128 rows x 128 keys, K = d: both operands bf16 in shared memory. An int8 key is exact in bf16, so S is
-//                 exact up to fp32 accumulation; the block's scale and the softmax scale multiply S afterwards.
+// The mathematics is that of kv_attn_simt.cu; here the two products of a block of 64 keys are tcgen05 MMAs:
+//   S = Q K^T     128 rows x 64 keys, K = d, operands fp16 in shared memory. A row of Q is scaled by a power of two to a
+//                 largest element in [2^14, 2^15), which is exact (but for elements 2^-32 of the largest), and taken out
+//                 of the scores again. An int8 key q is fed as 1152 + q, the fp16 that a byte under 0x64 reads as: the
+//                 scores are then off by 1152 times the row's sum of Q, which the softmax's fma subtracts. A key of the
+//                 row's own block, which is read as it came, is scaled by a power of two like a row of Q.
 //   O += P V      128 rows x d, K = 64 keys: P in TMEM as the A operand, V in shared memory. An 8-bit block: V int8 -> fp16
 //                 (exact), P = 2^{c s + log2 vs - m} with the block's value scale vs in the weight and m the running
 //                 maximum of exactly that exponent, so P <= 2^8 whatever the scales, and fp16 rounds it by 2^-11 of its
-//                 size (2^-25 absolute below 2^-14, where a key adds next to nothing). The row's own block as it came: V
-//                 bf16, P in two bf16 products, its upper and lower 8 bits: a row with few keys has nothing to average a
-//                 rounding out. The sum l takes the unrounded weights, 2^{c s - m}.
+//                 size (2^-25 absolute below 2^-14, where a key adds next to nothing). The row's own block: V bf16, P in
+//                 two bf16 products, its upper and lower 8 bits: a row with few keys has nothing to average a rounding
+//                 out. The sum l takes the unrounded weights, 2^{c s - m}.
 //
 // CTA: one row tile of R = 256 rows (two MMA tiles of 128; d = 256: one tile) of one kv head, over one segment of keys.
 // Rows are the (token, query head of the group) pairs of a span: consecutive blocks of one request, aligned to `span`
 // blocks, so that 64 span G >= R where it can be. Warp roles:
 //   softmax   a warpgroup per MMA tile, one row per thread: TMEM scores -> weights -> TMEM P, running maximum and sum
-//   convert   4 warps (d = 256: 8): pages from global memory, int8 -> bf16 in registers, into the operand layout
-//   MMA       one thread issues every product
-// With two tiles the tensor core works on one tile while the other's softmax runs; with one tile the two score buffers
-// take alternate steps.
+//   keys, values   4 warps each: pages from global memory, int8 -> fp16 in registers, into the operand layout
+//   MMA       a thread per MMA tile, in warps of their own, issues its products
+// Each MMA tile has two score buffers of 64 columns, so the next block's scores are computed while a block's weights are
+// (N = 64 makes S smem-bound, 48 cycles an MMA against 32, measured; with one 128-column buffer the softmax and the
+// tensor core waited for each other, 5,600 against 2,560 cycles per 128 keys of the two tiles). The weights overwrite the
+// scores that they came from.
 //
-// The running maximum m only moves when a half step (64 keys, one block) exceeds it by 8 (log2 domain): weights stay
-// below 2^8, and O is rescaled (by the softmax warps, after the products before it) only then. Every decision is a row's
-// own and every block is one softmax step, so a row's bits do not depend on the rows beside it.
-// Bound: tensor pipe; per 128 keys and 128 rows the MMAs take 4 * 128 * 128 * d / 8192 cycles (1,024 for d = 128).
+// The running maximum m only moves when a block exceeds it by 8 (log2 domain): O is rescaled (by the softmax warps, after
+// the product before it) only then. Every decision is a row's own and every block is one softmax step, so a row's bits do
+// not depend on the rows beside it.
 #include "kv_attn.cuh"
 #include "umma.cuh"
 
@@ -49,36 +53,69 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // named barrier `id` over n threads (whole warps)
 __device__ __forceinline__ void kv_named_barrier(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
 
+__device__ __forceinline__ void b8_to_f(const uint4 &u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+// The power of two that brings x > 0 into [2^14, 2^15), and its inverse; 1 for 0 and what is not finite, at most 2^100.
+__device__ __forceinline__ float pow2_to_2_15(float x, float &back) {
+    int e = 14 + 127 - (int)(__float_as_uint(x) >> 23);   // x >= 0
+    if (x == 0.f || !(x <= 3.4e38f)) e = 0;
+    e = min(e, 100);
+    back = __uint_as_float((uint32_t)(127 - e) << 23);
+    return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+// Zeroes the bf16 of a vector that are not finite; whether there was one.
+__device__ __forceinline__ bool drop_not_finite(uint4 &u) {
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if ((w[k] & 0x7F80u) == 0x7F80u) { w[k] &= 0xFFFF0000u; any = true; }
+        if ((w[k] & 0x7F800000u) == 0x7F800000u) { w[k] &= 0xFFFFu; any = true; }
+    }
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+    return any;
+}
+
 template <int D>
 struct PromptPlan {
     static constexpr int NQ = D == 256 ? 1 : 2;              // MMA tiles of 128 rows
     static constexpr int R = 128 * NQ;
-    static constexpr int NB = D == 256 ? 1 : 2;              // K and V buffers of 128 keys each
-    static constexpr int CW = D == 256 ? 8 : 4;              // convert warps
-    static constexpr int NT = 128 * NQ + 32 * CW + 32;
-    static constexpr int kConvert0 = 128 * NQ, kMma = NT - 32;   // first thread of the roles
-    static constexpr uint32_t kTile = 128 * D * 2;           // bytes of a 128 x D bf16 operand
-    static constexpr uint32_t kQ = 0, kK = NQ * kTile, kV = kK + NB * kTile, kHalf = kV + NB * kTile;
-    static constexpr int kMaxHalves = 64 + 4;                // int8 blocks of a segment and raw blocks of a span
-    static constexpr uint32_t kBar = kHalf + ((kMaxHalves + 2) * 16 + 15) / 16 * 16;
-    // barriers: kfull[NB], kfree[NB], vfull[NB], vfree[NB], sfull[2], pready[2][2], pvdone[NQ][2], drain
-    static constexpr int bKFull = 0, bKFree = NB, bVFull = 2 * NB, bVFree = 3 * NB, bS = 4 * NB, bP = bS + 2, bPV = bP + 4,
-                         bDrain = bPV + 2 * NQ, kNBar = bDrain + 1;
-    static constexpr uint32_t kSlot = kBar + kNBar * 8;
+    static constexpr int NS = D == 256 ? 2 : 4;              // key and value slots of 64 keys each
+    static constexpr int NT = 128 * NQ + 256 + 32 * NQ;
+    static constexpr int kKeys0 = 128 * NQ, kVals0 = kKeys0 + 128, kMma = kVals0 + 128;   // first thread of the roles
+    static constexpr uint32_t kTile = 128 * D * 2;           // bytes of a 128-row query tile
+    static constexpr uint32_t kBlk = 64 * D * 2;             // bytes of a slot
+    static constexpr uint32_t kQ = 0, kK = NQ * kTile, kV = kK + NS * kBlk, kInfo = kV + NS * kBlk;
+    static constexpr int kMaxBlocks = 64 + 4;                // 8-bit blocks of a segment and raw blocks of a span
+    static constexpr uint32_t kRow = kInfo + kMaxBlocks * 16;        // float2 [R]: what takes Q's scaling out, 1152 sum(Q)
+    static constexpr uint32_t kRawK = kRow + R * 8;                  // float [4][64]: the scalings of the raw blocks' keys
+    static constexpr uint32_t kBar = kRawK + 4 * 64 * 4;
+    // barriers: key and value slots full and free, scores, weights and products of (tile, buffer), all products
+    static constexpr int bKFull = 0, bKFree = NS, bVFull = 2 * NS, bVFree = 3 * NS, bS = 4 * NS, bP = bS + 2 * NQ,
+                         bPV = bP + 2 * NQ, bDrain = bPV + 2 * NQ, kNBar = bDrain + 1;
+    static constexpr uint32_t kSlot = kBar + (kNBar + 1) / 2 * 16;
     static constexpr uint32_t kBad = kSlot + 16;             // per raw block of the span: it has a value that is not finite
     static constexpr uint32_t kBytes = kBad + 16;
     static constexpr uint32_t kO = 256;                      // TMEM columns: scores [0, 256), outputs from here
     static constexpr uint32_t kTmemCols = 512;
     static constexpr int kVec = D / 64;                      // 64-column groups
-    static constexpr int kLoads = 16 * kVec / CW;            // 16-byte loads of a convert thread per 128-key tile
+    static constexpr int kLoads = 2 * kVec;                  // 16-byte loads of a key or value thread per block
+    // Registers per thread: two tiles launch 18 warps of 96 (an SM partition holds 5 of them at most), of which the key
+    // and value warps give 32 each to the softmax warps (1,728 per lane before and after); one tile launches 13 of 128.
+    static constexpr bool kSplitRegs = NQ == 2;
     static_assert(kBytes <= 227 * 1024, "shared memory");
-    static_assert(kLoads * CW == 16 * kVec, "convert split");
 };
 
-// A half step's block: its page, c = scale log2(e) k_scale, log2 of the value scale in the exponent that m is the maximum
+// A block of the pass: its page, c = scale log2(e) k_scale, log2 of the value scale in the exponent that m is the maximum
 // of, and the factor of its weights in the sum (1 / v_scale). A raw block counts with the value scale of the block before
 // it (so that m compares like with like), but its weights are of the values themselves.
-struct HalfInfo {
+struct BlockInfo {
     int page;
     float c, lvs, ivs;
 };
@@ -88,7 +125,7 @@ template <int D>
 __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(const KvAttn a, int row_tiles, int span, int n_units) {
     using P = PromptPlan<D>;
     using bf = __nv_bfloat16;
-    constexpr int NB = P::NB;
+    constexpr int NS = P::NS;
     grid_dep_wait();
     grid_dep_launch();
     // later units (longer contexts) first: a causal launch then ends on its short ones
@@ -121,29 +158,32 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + P::kBar);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + P::kSlot);
     uint32_t *bad_v = reinterpret_cast<uint32_t *>(sm + P::kBad);
-    HalfInfo *half = reinterpret_cast<HalfInfo *>(sm + P::kHalf);
+    BlockInfo *info = reinterpret_cast<BlockInfo *>(sm + P::kInfo);
+    float2 *row_q = reinterpret_cast<float2 *>(sm + P::kRow);
+    float *raw_k = reinterpret_cast<float *>(sm + P::kRawK);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int pos0 = u.block * kKvBlock + u.first;
     const int rows_here = min(P::R, n_row - r0);
     const int nt = rows_here > 128 ? 2 : 1;        // MMA tiles in use
-    // blocks of this tile's rows, and the halves: 8-bit blocks [c0, c0 + n8), then raw blocks from blo
+    // blocks of this tile's rows, and the blocks of the pass: 8-bit [c0, c0 + n8), then raw from blo
     const int blo = (pos0 + r0 / a.G) / kKvBlock, bhi = (pos0 + (r0 + rows_here - 1) / a.G) / kKvBlock;
     const int c0 = seg * a.seg_blocks;
     const int n8 = min(bhi - c0, a.seg_blocks);
-    const int nh = n8 + (seg == last_seg ? bhi - blo + 1 : 0);
-    const int steps = (nh + 1) / 2, n_items = steps * nt;
+    const int nb = n8 + (seg == last_seg ? bhi - blo + 1 : 0);
 
     if (t == 0) {
-        for (int i = 0; i < NB; ++i) {
-            mbar_init(&bar[P::bKFull + i], 32 * P::CW);
-            mbar_init(&bar[P::bVFull + i], 32 * P::CW);
-            mbar_init(&bar[P::bKFree + i], 1);
-            mbar_init(&bar[P::bVFree + i], 1);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&bar[P::bKFull + i], 128);
+            mbar_init(&bar[P::bVFull + i], 128);
+            mbar_init(&bar[P::bKFree + i], nt);
+            mbar_init(&bar[P::bVFree + i], nt);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&bar[P::bS + i], 1);
-        for (int i = 0; i < 4; ++i) mbar_init(&bar[P::bP + i], 128);
-        for (int i = 0; i < 2 * P::NQ; ++i) mbar_init(&bar[P::bPV + i], 1);
-        mbar_init(&bar[P::bDrain], 1);
+        for (int i = 0; i < 2 * P::NQ; ++i) {
+            mbar_init(&bar[P::bS + i], 1);
+            mbar_init(&bar[P::bP + i], 128);
+            mbar_init(&bar[P::bPV + i], 1);
+        }
+        mbar_init(&bar[P::bDrain], nt);
         mbar_init_fence();
         for (int i = 0; i < 4; ++i) bad_v[i] = 0;
     }
@@ -151,10 +191,10 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         tmem_alloc(tslot, P::kTmemCols);
         tmem_relinquish();
     }
-    // pages and scales of the segment's blocks
+    // pages and scales of the pass's blocks
     const int32_t *table = a.c.table + (int64_t)u.slot * a.c.max_blocks;
-    for (int i = t; i < nh; i += P::NT) {
-        HalfInfo x = {0, a.scale_log2, 0.f, 1.f};
+    for (int i = t; i < nb; i += P::NT) {
+        BlockInfo x = {0, a.scale_log2, 0.f, 1.f};
         if (i < n8) {
             x.page = table[c0 + i];
             x.lvs = kv_log2_vscale(a, table, c0 + i, h);
@@ -169,18 +209,37 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         } else {
             x.lvs = kv_log2_vscale(a, table, blo + i - n8 - 1, h);
         }
-        half[i] = x;
+        info[i] = x;
     }
-    // Q: K-major core matrices (8 rows x 16 bytes), rows past the end zero
-    const bf *q = static_cast<const bf *>(a.q);
-    for (int e = t; e < nt * 128 * (D / 8); e += P::NT) {
-        const int r = e / (D / 8), c = e % (D / 8);
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (r < rows_here) {
-            const int rr = r0 + r;
-            w = *reinterpret_cast<const uint4 *>(q + ((int64_t)(u.row + rr / a.G) * a.Hq + h * a.G + rr % a.G) * D + c * 8);
+    // Q: a warp takes 32 / (d / 8) rows at a time, a lane 8 columns; K-major core matrices (8 rows x 16 bytes)
+    {
+        constexpr int LPR = D / 8, RPW = 32 / LPR;
+        const int c = lane % LPR;
+        for (int rb = warp * RPW; rb < nt * 128; rb += P::NT / 32 * RPW) {
+            const int r = rb + lane / LPR, rr = r0 + r;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (r < rows_here)
+                w = *reinterpret_cast<const uint4 *>(static_cast<const bf *>(a.q) +
+                                                     ((int64_t)(u.row + rr / a.G) * a.Hq + h * a.G + rr % a.G) * D + c * 8);
+            float f[8], top = 0.f, sum = 0.f;
+            b8_to_f(w, f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]));
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float back;
+            const float up = pow2_to_2_15(top, back);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] *= up;
+            w = f8_to_h8(f);
+            h8_to_f(w, f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += f[k];
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            *reinterpret_cast<uint4 *>(sm + P::kQ + (r >> 7) * P::kTile + ((r & 127) >> 3) * (D * 16) + c * 128 + (r & 7) * 16) = w;
+            if (c == 0) row_q[r] = make_float2(back, 1152.f * sum);
         }
-        *reinterpret_cast<uint4 *>(sm + P::kQ + (r >> 7) * P::kTile + ((r & 127) >> 3) * (D * 16) + c * 128 + (r & 7) * 16) = w;
     }
     fence_proxy_async();
     tc_fence_before();
@@ -191,265 +250,249 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     bool alive = true;
 
     if (t >= P::kMma) {
-        // ---- the issuing thread ----
-        if (t == P::kMma) {
-            constexpr uint32_t idS = umma_idesc_bf16(128, 128, 0, 0), idO8 = umma_idesc_f16(128, D, 0, 1),
+        // ---- the issuing threads, lane 0 of a warp per tile ----
+        const int tile = (t - P::kMma) >> 5;
+        if (lane == 0 && tile < nt) {
+            constexpr uint32_t idS = umma_idesc_f16(128, 64, 0, 0), idO8 = umma_idesc_f16(128, D, 0, 1),
                                idOraw = umma_idesc_bf16(128, D, 0, 1);
-            auto issue_s = [&](int i) {
-                const int step = i / nt, tile = i - step * nt, slot = step % NB, b = i & 1;
-                if (tile == 0 && !mbar_wait_bounded(&bar[P::bKFull + slot], (step / NB) & 1, limit)) return false;
+            const uint64_t dq = umma_smem_desc(sm + P::kQ + tile * P::kTile, 128, D * 16),
+                           dk0 = umma_smem_desc(sm + P::kK, 128, D * 16), dv0 = umma_smem_desc(sm + P::kV, D * 16, 128);
+            const uint32_t s0_tm = tmem + 128 * tile, o_tm = tmem + P::kO + tile * D;
+            auto issue_s = [&](int n) {
+                const int slot = n % NS, b = n & 1;
+                if (!mbar_wait_bounded(&bar[P::bKFull + slot], (n / NS) & 1, limit)) return false;
                 tc_fence_after();
-                const uint64_t dq = umma_smem_desc(sm + P::kQ + tile * P::kTile, 128, D * 16);
-                const uint64_t dk = umma_smem_desc(sm + P::kK + slot * P::kTile, 128, D * 16);
+                const uint64_t dk = dk0 + slot * (P::kBlk >> 4);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) umma_bf16(tmem + 128 * b, dq + 16 * k, dk + 16 * k, idS, k > 0);
-                umma_commit(&bar[P::bS + b]);
-                if (tile == nt - 1) umma_commit(&bar[P::bKFree + slot]);
+                for (int k = 0; k < D / 16; ++k) umma_bf16(s0_tm + 64 * b, dq + 16 * k, dk + 16 * k, idS, k > 0);
+                umma_commit(&bar[P::bS + 2 * tile + b]);
+                umma_commit(&bar[P::bKFree + slot]);
                 return true;
             };
-            alive = issue_s(0) && (n_items < 2 || issue_s(1));
-            for (int i = 0; alive && i < n_items; ++i) {
-                const int step = i / nt, tile = i - step * nt, slot = step % NB, b = i & 1;
-                const int halves = min(2, nh - 2 * step);
-                if (tile == 0) alive = mbar_wait_bounded(&bar[P::bVFull + slot], (step / NB) & 1, limit);
-                for (int hh = 0; alive && hh < halves; ++hh) {
-                    alive = mbar_wait_bounded(&bar[P::bP + 2 * b + hh], (i / 2) & 1, limit);
-                    if (!alive) break;
-                    tc_fence_after();
-                    const bool raw = 2 * step + hh >= n8;
-                    const uint32_t idO = raw ? idOraw : idO8;
-                    const uint64_t dv = umma_smem_desc(sm + P::kV + slot * P::kTile + hh * (8 * D * 16), D * 16, 128);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_bf16_ts(tmem + P::kO + tile * D, tmem + 128 * b + 64 * hh + 8 * k, dv + (uint64_t)(2 * D * k), idO,
-                                     step > 0 || hh > 0 || k > 0);
-                    if (raw) {   // the low parts of the raw block's weights
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma_bf16_ts(tmem + P::kO + tile * D, tmem + 128 * b + 64 * hh + 32 + 8 * k, dv + (uint64_t)(2 * D * k),
-                                         idO, 1);
-                    }
-                    umma_commit(&bar[P::bPV + 2 * tile + hh]);
-                }
+            alive = issue_s(0) && (nb < 2 || issue_s(1));
+#pragma unroll 1
+            for (int n = 0; alive && n < nb; ++n) {
+                const int slot = n % NS, b = n & 1;
+                alive = mbar_wait_bounded(&bar[P::bVFull + slot], (n / NS) & 1, limit) &&
+                        mbar_wait_bounded(&bar[P::bP + 2 * tile + b], (n >> 1) & 1, limit);
                 if (!alive) break;
-                if (tile == nt - 1) umma_commit(&bar[P::bVFree + slot]);
-                if (i + 2 < n_items) alive = issue_s(i + 2);
+                tc_fence_after();
+                const uint64_t dv = dv0 + slot * (P::kBlk >> 4);
+                const uint32_t p_tm = s0_tm + 64 * b, idO = n < n8 ? idO8 : idOraw;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_bf16_ts(o_tm, p_tm + 8 * k, dv + (uint64_t)(2 * D * k), idO, n > 0 || k > 0);
+                if (n >= n8) {   // the low parts of the raw block's weights
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) umma_bf16_ts(o_tm, p_tm + 32 + 8 * k, dv + (uint64_t)(2 * D * k), idO, 1);
+                }
+                umma_commit(&bar[P::bPV + 2 * tile + b]);
+                umma_commit(&bar[P::bVFree + slot]);
+                if (n + 2 < nb) alive = issue_s(n + 2);
             }
             if (!alive) atomicOr(a.err, kErrTimeout);
             umma_commit(&bar[P::bDrain]);
             if (!mbar_wait_bounded(&bar[P::bDrain], 0, limit)) atomicOr(a.err, kErrTimeout);
         }
-    } else if (t >= P::kConvert0) {
-        // ---- convert warps ----
-        const int cw = warp - P::kConvert0 / 32;
-        const int kr = lane & 7, ch = lane >> 3;   // key of 8 and 16-byte chunk of 64
+    } else if (t >= P::kKeys0) {
+        // ---- key and value warps: 4 warps each convert a block at a time, its loads one block ahead ----
+        if constexpr (P::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+        const bool is_v = t >= P::kVals0;
+        const int cw = warp & 3, kr = lane & 7, ch = lane >> 3;   // warp of the role; key of 8 and 16-byte chunk of 64
         const bf *tail = static_cast<const bf *>(a.c.tail);
-        const int n_seq = 2 * steps;               // K(0), K(1), V(0), K(2), V(1), ..., V(steps - 1)
-        auto what = [&](int s, int &kv, int &step) {
-            if (s == 0) { kv = 0; step = 0; }
-            else if (s == n_seq - 1) { kv = 1; step = steps - 1; }
-            else { kv = (s + 1) & 1; step = (s + 1) / 2 - kv; }
-        };
-        // 16-byte loads of tile (kv, step): load i of this warp is 8 keys x 64 columns, number cw + CW i of (half, key group,
-        // column group). Both loops are unrolled over the loads only: the roles share the instruction cache.
+        const int8_t *pool = (is_v ? a.c.v : a.c.k) + (int64_t)h * (kKvBlock * D) + kr * D + ch * 16;
+        const int64_t stride = (int64_t)a.Hkv * (kKvBlock * D);
+        uint64_t *full = &bar[is_v ? P::bVFull : P::bKFull], *free = &bar[is_v ? P::bVFree : P::bKFree];
+        unsigned char *slots = sm + (is_v ? P::kV : P::kK) + kr * 16 + ch * 256;
+        // load i of this warp: 8 keys x 64 columns, key group (cw + 4 i) / kVec, column group (cw + 4 i) % kVec
         uint4 w[P::kLoads];
-        auto load8 = [&](int kv, int step) {
-            const int8_t *pool = (kv ? a.c.v : a.c.k) + (int64_t)h * (kKvBlock * D) + kr * D + ch * 16;
-            const int64_t stride = (int64_t)a.Hkv * (kKvBlock * D);
-            const int8_t *base[2];
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) base[hh] = pool + half[min(2 * step + hh, nh - 1)].page * stride;
+        auto load = [&](int n) {
+            const int8_t *src = pool + info[n].page * stride;
 #pragma unroll
             for (int i = 0; i < P::kLoads; ++i) {
-                const int j = cw + P::CW * i, hh = P::CW * i / (8 * P::kVec), kg = j / P::kVec % 8, dg = j % P::kVec;
-                w[i] = __ldg(reinterpret_cast<const uint4 *>(base[hh] + kg * (8 * D) + dg * 64));
+                const int j = cw + 4 * i;
+                w[i] = __ldg(reinterpret_cast<const uint4 *>(src + j / P::kVec * (8 * D) + j % P::kVec * 64));
             }
         };
-        auto store8 = [&](auto is_v, unsigned char *dst, int n_half) {
-            constexpr bool f16 = decltype(is_v)::value;
+        auto store = [&](auto vals, unsigned char *dst) {
+            constexpr bool V = decltype(vals)::value;
 #pragma unroll
             for (int i = 0; i < P::kLoads; ++i) {
-                const int j = cw + P::CW * i, hh = P::CW * i / (8 * P::kVec), kg = j / P::kVec % 8, dg = j % P::kVec;
-                if (hh >= n_half) break;
-                uint4 lo, hi;
-                if (f16) {
-                    const uint2 x0 = i8_to_f16x4(w[i].x), x1 = i8_to_f16x4(w[i].y), x2 = i8_to_f16x4(w[i].z), x3 = i8_to_f16x4(w[i].w);
-                    lo = make_uint4(x0.x, x0.y, x1.x, x1.y);
-                    hi = make_uint4(x2.x, x2.y, x3.x, x3.y);
-                } else {
-                    const uint2 x0 = i8_to_bf16x4(w[i].x), x1 = i8_to_bf16x4(w[i].y), x2 = i8_to_bf16x4(w[i].z), x3 = i8_to_bf16x4(w[i].w);
-                    lo = make_uint4(x0.x, x0.y, x1.x, x1.y);
-                    hi = make_uint4(x2.x, x2.y, x3.x, x3.y);
-                }
-                unsigned char *o = dst + (hh * 8 + kg) * (D * 16) + (dg * 8 + ch * 2) * 128 + kr * 16;
-                *reinterpret_cast<uint4 *>(o) = lo;
-                *reinterpret_cast<uint4 *>(o + 128) = hi;
+                const int j = cw + 4 * i;
+                const uint2 x0 = i8_to_f16x4<V>(w[i].x), x1 = i8_to_f16x4<V>(w[i].y), x2 = i8_to_f16x4<V>(w[i].z), x3 = i8_to_f16x4<V>(w[i].w);
+                unsigned char *o = dst + j / P::kVec * (D * 16) + j % P::kVec * 1024;
+                *reinterpret_cast<uint4 *>(o) = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                *reinterpret_cast<uint4 *>(o + 128) = make_uint4(x2.x, x2.y, x3.x, x3.y);
             }
         };
         // a raw block: the tail's rows, then the new ones, zero past the last
-        auto store_raw = [&](int kv, int hh, int block, unsigned char *dst) {
+        auto store_raw = [&](int block, unsigned char *dst) {
 #pragma unroll 1
-            for (int j = cw; j < 8 * P::kVec; j += P::CW) {
-                const int kg = j / P::kVec, dg = j % P::kVec, off = kg * 8 + kr, pos = block * kKvBlock + off;
+            for (int kg = cw; kg < 8; kg += 4) {
+                const int off = kg * 8 + kr, pos = block * kKvBlock + off;
                 const bf *src = nullptr;
-                if (pos < pos0) src = tail + kv_tail_offset(u.slot, u.src, kv, h, a.Hkv, D) + (int64_t)off * D;
+                if (pos < pos0) src = tail + kv_tail_offset(u.slot, u.src, is_v, h, a.Hkv, D) + (int64_t)off * D;
                 else if (pos < pos0 + n_tok)
-                    src = static_cast<const bf *>(kv ? a.v_new : a.k_new) + ((int64_t)(u.row + pos - pos0) * a.Hkv + h) * D;
-                uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                if (src) {
-                    const uint4 *q4 = reinterpret_cast<const uint4 *>(src + dg * 64 + ch * 16);
-                    const uint4 y0 = q4[0], y1 = q4[1];
-                    x[0] = y0.x; x[1] = y0.y; x[2] = y0.z; x[3] = y0.w;
-                    x[4] = y1.x; x[5] = y1.y; x[6] = y1.z; x[7] = y1.w;
-                }
-                if (kv) {
-                    // a value that is not finite would reach rows that do not see it (0 * inf): left out here, and added by
-                    // the rows that do at the end
-                    bool any = false;
+                    src = static_cast<const bf *>(is_v ? a.v_new : a.k_new) + ((int64_t)(u.row + pos - pos0) * a.Hkv + h) * D;
+                float top = 0.f, up = 1.f;
+#pragma unroll 1
+                for (int pass = is_v ? 1 : 0; pass < 2; ++pass) {   // keys: the largest element first, then the scaled key
+#pragma unroll 1
+                    for (int dg = 0; dg < P::kVec; ++dg) {
+                        uint4 y[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                        if (src) {
+                            y[0] = reinterpret_cast<const uint4 *>(src + dg * 64 + ch * 16)[0];
+                            y[1] = reinterpret_cast<const uint4 *>(src + dg * 64 + ch * 16)[1];
+                        }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        if ((x[k] & 0x7F80u) == 0x7F80u) { x[k] &= 0xFFFF0000u; any = true; }
-                        if ((x[k] & 0x7F800000u) == 0x7F800000u) { x[k] &= 0xFFFFu; any = true; }
+                        for (int k = 0; k < 2; ++k) {
+                            if (is_v) {
+                                // a value that is not finite would reach rows that do not see it (0 * inf): left out here,
+                                // and added by the rows that do at the end
+                                if (drop_not_finite(y[k])) atomicOr(&bad_v[block - blo], 1u);
+                            } else {
+                                float f[8];
+                                b8_to_f(y[k], f);
+#pragma unroll
+                                for (int x = 0; x < 8; ++x) {
+                                    top = fmaxf(top, fabsf(f[x]));
+                                    f[x] *= up;
+                                }
+                                y[k] = f8_to_h8(f);
+                            }
+                            if (pass == 1) *reinterpret_cast<uint4 *>(dst + kg * (D * 16) + dg * 1024 + k * 128) = y[k];
+                        }
                     }
-                    if (any) atomicOr(&bad_v[block - blo], 1u);
+                    if (pass == 0) {
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        float back;
+                        up = pow2_to_2_15(top, back);
+                        if (ch == 0) raw_k[(block - blo) * 64 + off] = back;
+                    }
                 }
-                unsigned char *o = dst + (hh * 8 + kg) * (D * 16) + (dg * 8 + ch * 2) * 128 + kr * 16;
-                *reinterpret_cast<uint4 *>(o) = make_uint4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<uint4 *>(o + 128) = make_uint4(x[4], x[5], x[6], x[7]);
             }
         };
-        load8(0, 0);
+        load(0);
 #pragma unroll 1
-        for (int s = 0; s < n_seq; ++s) {
-            int kv, step;
-            what(s, kv, step);
-            const int slot = step % NB, n_half = min(max(n8 - 2 * step, 0), 2);
-            if (step >= NB) {
-                if (!mbar_wait_bounded(&bar[(kv ? P::bVFree : P::bKFree) + slot], (step / NB - 1) & 1, limit)) {
-                    alive = false;
-                    break;
-                }
+        for (int n = 0; n < nb; ++n) {
+            const int slot = n % NS;
+            if (n >= NS && !mbar_wait_bounded(&free[slot], (n / NS - 1) & 1, limit)) {
+                alive = false;
+                break;
             }
-            unsigned char *dst = sm + (kv ? P::kV : P::kK) + slot * P::kTile;
-            if (kv) store8(std::true_type{}, dst, n_half);
-            else store8(std::false_type{}, dst, n_half);
-            if (s + 1 < n_seq) {   // the next tile's loads are under way while this one is finished and the next slot waited for
-                int kv1, step1;
-                what(s + 1, kv1, step1);
-                load8(kv1, step1);
+            unsigned char *dst = slots + slot * P::kBlk;
+            if (n < n8) {
+                if (is_v) store(std::true_type{}, dst);
+                else store(std::false_type{}, dst);
+                load(min(n + 1, nb - 1));   // a raw block: page 0, not used
+            } else {
+                store_raw(blo + n - n8, dst);
             }
-            for (int hh = n_half; hh < 2 && 2 * step + hh < nh; ++hh) store_raw(kv, hh, blo + 2 * step + hh - n8, dst);
             fence_proxy_async();
-            if (s > 0 || a.skip_first_copy != 3) mbar_arrive(&bar[(kv ? P::bVFull : P::bKFull) + slot]);   // 3: the test hook
+            if (n > 0 || is_v || a.skip_first_copy != 3) mbar_arrive(&full[slot]);   // 3: the test hook
         }
         if (!alive && lane == 0) atomicOr(a.err, kErrTimeout);
         kv_named_barrier(1, P::kMma);
     } else if (warp / 4 < nt) {
         // ---- softmax warps ----
+        if constexpr (P::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;\n");
         const int tile = warp >> 2, r = r0 + t;    // t = 128 tile + row
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int pos = pos0 + r / a.G, blk = pos / kKvBlock, off = pos % kKvBlock;
         const uint32_t o_tm = tmem + lanes + P::kO + tile * D;
+        const float2 rq = row_q[t];
         float m = -INFINITY, l = 0.f;
-        for (int step = 0; alive && step < steps; ++step) {
-            const int i = step * nt + tile, b = i & 1;
-            const uint32_t s_tm = tmem + lanes + 128 * b;
-            alive = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bS + b], (i / 2) & 1, limit));
-            if (!alive) break;
+        auto block_step = [&](auto is_raw, int n) {
+            constexpr bool raw = decltype(is_raw)::value;
+            const int b = 2 * tile + (n & 1);
+            const uint32_t s_tm = tmem + lanes + 64 * b;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bS + b], (n >> 1) & 1, limit))) return false;
+            // the key warps' scalings; no later block takes the slot (the pass ends with its at most NS raw blocks)
+            if (raw && !__all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bKFull + n % NS], (n / NS) & 1, limit))) return false;
             tc_fence_after();
-            const int halves = min(2, nh - 2 * step);
-            auto half_step = [&](auto is_raw, int hh) {
-                constexpr bool raw = decltype(is_raw)::value;
-                const int hi = 2 * step + hh;
-                const HalfInfo x = half[hi];
-                // keys of the half that the row sees: all or none of an 8-bit block, up to its own offset of its raw block
-                const int see = raw ? (blk == blo + hi - n8 ? off + 1 : 0) : (blk > c0 + hi ? kKvBlock : 0);
-                float s[64];
-                {
-                    uint32_t w[4][16];
+            const BlockInfo x = info[n];
+            // keys of the block that the row sees: all or none of an 8-bit block, up to its own offset of its raw block
+            const int see = raw ? (blk == blo + n - n8 ? off + 1 : 0) : (blk > c0 + n ? kKvBlock : 0);
+            const float c = x.c * rq.x, c1152 = raw ? 0.f : -c * rq.y;
+            float s[64];
+            {
+                uint32_t w[4][16];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) tmem_ld16_nowait(s_tm + 64 * hh + 16 * j, w[j]);
+                for (int j = 0; j < 4; ++j) tmem_ld16_nowait(s_tm + 16 * j, w[j]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        tmem_wait_ld(w[j]);
+                for (int j = 0; j < 4; ++j) {
+                    tmem_wait_ld(w[j]);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) s[16 * j + k] = __uint_as_float(w[j][k]);
-                    }
+                    for (int k = 0; k < 16; ++k) s[16 * j + k] = __uint_as_float(w[j][k]);
                 }
-                if (raw) {
+            }
+            if (raw) {
+                const float *kf = raw_k + (n - n8) * 64;
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) s[j] = j < see ? s[j] : -INFINITY;
-                }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
+                for (int j = 0; j < 64; ++j) s[j] = j < see ? s[j] * kf[j] : -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int j = 4; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * x.c + x.lvs;
-                float f = 1.f;
-                if (see > 0 && top > m + 8.f) {    // also the row's first keys (m = -inf)
-                    f = ex2(m - top);              // 0 then
-                    m = top;
-                    l *= f;
-                }
-                // O is rescaled once the products that are under way on it are done (a row's first keys meet O = 0)
-                if ((step > 0 || hh > 0) && __any_sync(0xffffffffu, f != 1.f)) {
-                    bool done = true;
-                    if (step > 0) done = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bPV + 2 * tile + 1], (step - 1) & 1, limit));
-                    if (done && hh == 1)
-                        done = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bPV + 2 * tile], step & 1, limit));
-                    if (!done) return false;
-                    tc_fence_after();
+            for (int j = 4; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+            const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, c1152 + x.lvs);
+            float f = 1.f;
+            if (see > 0 && top > m + 8.f) {    // also the row's first keys (m = -inf)
+                f = ex2(m - top);              // 0 then
+                m = top;
+                l *= f;
+            }
+            // O is rescaled once the product that is under way on it is done (a row's first keys meet O = 0)
+            if (n > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bPV + 2 * tile + ((n - 1) & 1)], ((n - 1) >> 1) & 1, limit)))
+                    return false;
+                tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t w[16];
-                        tmem_ld16_nowait(o_tm + c, w);
-                        tmem_wait_ld(w);
+                for (int k0 = 0; k0 < D; k0 += 16) {
+                    uint32_t w[16];
+                    tmem_ld16_nowait(o_tm + k0, w);
+                    tmem_wait_ld(w);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
-                        tmem_st16(o_tm + c, w);
-                    }
-                    tmem_wait_st();
+                    for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
+                    tmem_st16(o_tm + k0, w);
                 }
-                // the weights (8-bit blocks: times the value scale, which the sum takes out again); none of a block that
-                // the row does not see
-                const uint64_t cc = f2_pack(x.c, x.c);
-                const float add = see == 0 ? -INFINITY : (raw ? 0.f : x.lvs) - (m == -INFINITY ? 0.f : m);
-                const uint64_t bb = f2_pack(add, add);
-                uint64_t sum[2] = {0, 0};
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t w[16], lo[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int e = 32 * j + 2 * k;
-                        float p0, p1;
-                        f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), cc, bb), p0, p1);
-                        p0 = ex2(p0);
-                        p1 = ex2(p1);
-                        sum[k & 1] = f2_add(sum[k & 1], f2_pack(p0, p1));
-                        if (raw) {
-                            uint32_t x1;
-                            split_bf16x2(p0, p1, x1, lo[k]);
-                            w[k] = x1;
-                        } else {
-                            w[k] = f2_to_h2(p0, p1);
-                        }
-                    }
-                    tmem_st16(s_tm + 64 * hh + 16 * j, w);
-                    if (raw) tmem_st16(s_tm + 64 * hh + 32 + 16 * j, lo);
-                }
-                float s0, s1;
-                f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
-                l = fmaf(s0 + s1, x.ivs, l);
                 tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(&bar[P::bP + 2 * b + hh]);
-                return true;
-            };
+            }
+            // the weights (8-bit blocks: times the value scale, which the sum takes out again); none of a block that the
+            // row does not see
+            const uint64_t cc = f2_pack(c, c);
+            const float add = see == 0 ? -INFINITY : c1152 + ((raw ? 0.f : x.lvs) - (m == -INFINITY ? 0.f : m));
+            const uint64_t bb = f2_pack(add, add);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint32_t w[16], lo[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int e = 32 * j + 2 * k;
+                    float p0, p1;
+                    f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), cc, bb), p0, p1);
+                    p0 = ex2(p0);
+                    p1 = ex2(p1);
+                    sum[k & 1] = f2_add(sum[k & 1], f2_pack(p0, p1));
+                    if (raw) split_bf16x2(p0, p1, w[k], lo[k]);
+                    else w[k] = f2_to_h2(p0, p1);
+                }
+                tmem_st16(s_tm + 16 * j, w);
+                if (raw) tmem_st16(s_tm + 32 + 16 * j, lo);
+            }
+            float s0, s1;
+            f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+            l = fmaf(s0 + s1, x.ivs, l);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bar[P::bP + b]);
+            return true;
+        };
 #pragma unroll 1
-            for (int hh = 0; alive && hh < halves; ++hh)
-                alive = 2 * step + hh < n8 ? half_step(std::false_type{}, hh) : half_step(std::true_type{}, hh);
-        }
-        // every product is done, and the convert warps have said what they left out: the rows
+        for (int n = 0; alive && n < n8; ++n) alive = block_step(std::false_type{}, n);
+#pragma unroll 1
+        for (int n = n8; alive && n < nb; ++n) alive = block_step(std::true_type{}, n);
+        // every product is done, and the value warps have said what they left out: the rows
         kv_named_barrier(1, P::kMma);
         if (alive) alive = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bDrain], 0, limit));
         if (alive) {
@@ -504,6 +547,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             atomicOr(a.err, kErrTimeout);
         }
     } else {
+        if constexpr (P::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;\n");
         kv_named_barrier(1, P::kMma);   // the second tile's warps, without rows
     }
     tc_fence_before();
