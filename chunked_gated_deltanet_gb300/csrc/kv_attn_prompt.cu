@@ -18,7 +18,7 @@
 // blocks, so that 64 span G >= R where it can be. Warp roles:
 //   softmax   a warpgroup per MMA tile, one row per thread: TMEM scores -> weights -> TMEM P, running maximum and sum
 //   keys, values   4 warps each: pages from global memory, int8 -> fp16 in registers, into the operand layout
-//   MMA       a thread per MMA tile, in warps of their own, issues its products
+//   MMA       a warp per MMA tile issues its products
 // Each MMA tile has two score buffers of 64 columns, so the next block's scores are computed while a block's weights are
 // (N = 64 makes S smem-bound, 48 cycles an MMA against 32, measured; with one 128-column buffer the softmax and the
 // tensor core waited for each other, 5,600 against 2,560 cycles per 128 keys of the two tiles). The weights overwrite the
@@ -53,6 +53,36 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // named barrier `id` over n threads (whole warps)
 __device__ __forceinline__ void kv_named_barrier(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
 
+// One arrival per warp and one polling lane: an arrival or a test by 32 lanes is 32 passes through the shared-memory
+// pipe, which the MMA operands and the score loads fill already.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, long long limit) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded(bar, parity, limit);
+    return __shfl_sync(0xffffffffu, ok, 0);
+}
+// Three barriers tested together, their latencies overlapping.
+__device__ __forceinline__ bool wait3(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, uint64_t *b2, uint32_t p2, long long limit) {
+    for (long long i = 0; i < limit; ++i) {
+        const bool x = mbar_try_wait(b0, p0), y = mbar_try_wait(b1, p1), z = mbar_try_wait(b2, p2);
+        if (x && y && z) return true;
+    }
+    return false;
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ void b8_to_f(const uint4 &u, float (&f)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -87,8 +117,10 @@ struct PromptPlan {
     static constexpr int NQ = D == 256 ? 1 : 2;              // MMA tiles of 128 rows
     static constexpr int R = 128 * NQ;
     static constexpr int NS = D == 256 ? 2 : 4;              // key and value slots of 64 keys each
-    static constexpr int NT = 128 * NQ + 256 + 32 * NQ;
-    static constexpr int kKeys0 = 128 * NQ, kVals0 = kKeys0 + 128, kMma = kVals0 + 128;   // first thread of the roles
+    static constexpr int CW = D == 256 ? 8 : 4;              // warps that convert keys, and as many that convert values
+    // First thread of the roles. The issuing warps come first: a scheduler that prefers older warps then lets their few
+    // instructions through.
+    static constexpr int kSoft0 = 128, kKeys0 = kSoft0 + 128 * NQ, kVals0 = kKeys0 + 32 * CW, NT = kVals0 + 32 * CW;
     static constexpr uint32_t kTile = 128 * D * 2;           // bytes of a 128-row query tile
     static constexpr uint32_t kBlk = 64 * D * 2;             // bytes of a slot
     static constexpr uint32_t kQ = 0, kK = NQ * kTile, kV = kK + NS * kBlk, kInfo = kV + NS * kBlk;
@@ -96,19 +128,20 @@ struct PromptPlan {
     static constexpr uint32_t kRow = kInfo + kMaxBlocks * 16;        // float2 [R]: what takes Q's scaling out, 1152 sum(Q)
     static constexpr uint32_t kRawK = kRow + R * 8;                  // float [4][64]: the scalings of the raw blocks' keys
     static constexpr uint32_t kBar = kRawK + 4 * 64 * 4;
-    // barriers: key and value slots full and free, scores, weights and products of (tile, buffer), all products
+    // barriers: key and value slots full and free, scores and weights of (tile, buffer), a tile's product before its last,
+    // all products
     static constexpr int bKFull = 0, bKFree = NS, bVFull = 2 * NS, bVFree = 3 * NS, bS = 4 * NS, bP = bS + 2 * NQ,
-                         bPV = bP + 2 * NQ, bDrain = bPV + 2 * NQ, kNBar = bDrain + 1;
+                         bPV = bP + 2 * NQ, bDrain = bPV + NQ, kNBar = bDrain + 1;
     static constexpr uint32_t kSlot = kBar + (kNBar + 1) / 2 * 16;
     static constexpr uint32_t kBad = kSlot + 16;             // per raw block of the span: it has a value that is not finite
     static constexpr uint32_t kBytes = kBad + 16;
     static constexpr uint32_t kO = 256;                      // TMEM columns: scores [0, 256), outputs from here
     static constexpr uint32_t kTmemCols = 512;
     static constexpr int kVec = D / 64;                      // 64-column groups
-    static constexpr int kLoads = 2 * kVec;                  // 16-byte loads of a key or value thread per block
-    // Registers per thread: two tiles launch 18 warps of 96 (an SM partition holds 5 of them at most), of which the key
-    // and value warps give 32 each to the softmax warps (1,728 per lane before and after); one tile launches 13 of 128.
-    static constexpr bool kSplitRegs = NQ == 2;
+    static constexpr int kLoads = 8 * kVec / CW;             // 16-byte loads of a key or value thread per block
+    // Registers: an SM partition's 512 per lane hold 5 of the 20 warps (two tiles) at 96, or 6 of the 24 (one tile) at 80.
+    // The key and value warps go down to 64 and the softmax warps up to 128; per partition 2 x 32 given, 2 x 32 taken (two
+    // tiles), 4 x 16 given, 48 taken (one).
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -173,16 +206,16 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
 
     if (t == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&bar[P::bKFull + i], 128);
-            mbar_init(&bar[P::bVFull + i], 128);
+            mbar_init(&bar[P::bKFull + i], P::CW);
+            mbar_init(&bar[P::bVFull + i], P::CW);
             mbar_init(&bar[P::bKFree + i], nt);
             mbar_init(&bar[P::bVFree + i], nt);
         }
         for (int i = 0; i < 2 * P::NQ; ++i) {
             mbar_init(&bar[P::bS + i], 1);
-            mbar_init(&bar[P::bP + i], 128);
-            mbar_init(&bar[P::bPV + i], 1);
+            mbar_init(&bar[P::bP + i], 4);
         }
+        for (int i = 0; i < P::NQ; ++i) mbar_init(&bar[P::bPV + i], 1);
         mbar_init(&bar[P::bDrain], nt);
         mbar_init_fence();
         for (int i = 0; i < 4; ++i) bad_v[i] = 0;
@@ -249,67 +282,84 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     const long long limit = a.wait_limit;
     bool alive = true;
 
-    if (t >= P::kMma) {
-        // ---- the issuing threads, lane 0 of a warp per tile ----
-        const int tile = (t - P::kMma) >> 5;
-        if (lane == 0 && tile < nt) {
+    if (t < P::kSoft0) {
+        // ---- the issuing warps, one per tile: whole warps in step, one elected lane issues (a lane of its own in a divergent
+        // branch takes 84 cycles per MMA beside busy warps, an elected lane of a warp in step 53, measured) ----
+        const int tile = warp;
+        if (tile < nt) {
             constexpr uint32_t idS = umma_idesc_f16(128, 64, 0, 0), idO8 = umma_idesc_f16(128, D, 0, 1),
                                idOraw = umma_idesc_bf16(128, D, 0, 1);
+            const bool elected = elect_one();
             const uint64_t dq = umma_smem_desc(sm + P::kQ + tile * P::kTile, 128, D * 16),
                            dk0 = umma_smem_desc(sm + P::kK, 128, D * 16), dv0 = umma_smem_desc(sm + P::kV, D * 16, 128);
             const uint32_t s0_tm = tmem + 128 * tile, o_tm = tmem + P::kO + tile * D;
             auto issue_s = [&](int n) {
                 const int slot = n % NS, b = n & 1;
-                if (!mbar_wait_bounded(&bar[P::bKFull + slot], (n / NS) & 1, limit)) return false;
-                tc_fence_after();
                 const uint64_t dk = dk0 + slot * (P::kBlk >> 4);
+                if (elected) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) umma_bf16(s0_tm + 64 * b, dq + 16 * k, dk + 16 * k, idS, k > 0);
-                umma_commit(&bar[P::bS + 2 * tile + b]);
-                umma_commit(&bar[P::bKFree + slot]);
-                return true;
+                    for (int k = 0; k < D / 16; ++k) umma_bf16(s0_tm + 64 * b, dq + 16 * k, dk + 16 * k, idS, k > 0);
+                    umma_commit(&bar[P::bS + 2 * tile + b]);
+                    umma_commit(&bar[P::bKFree + slot]);
+                }
             };
-            alive = issue_s(0) && (nb < 2 || issue_s(1));
+            for (int n = 0; alive && n < min(nb, 2); ++n) {
+                alive = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bKFull + n % NS], (n / NS) & 1, limit));
+                tc_fence_after();
+                if (alive) issue_s(n);
+            }
 #pragma unroll 1
             for (int n = 0; alive && n < nb; ++n) {
                 const int slot = n % NS, b = n & 1;
-                alive = mbar_wait_bounded(&bar[P::bVFull + slot], (n / NS) & 1, limit) &&
-                        mbar_wait_bounded(&bar[P::bP + 2 * tile + b], (n >> 1) & 1, limit);
+                const bool more = n + 2 < nb;
+                const int nk = more ? n + 2 : n;   // the keys of the product that follows (n: there already)
+                alive = __all_sync(0xffffffffu, wait3(&bar[P::bVFull + slot], (n / NS) & 1, &bar[P::bKFull + nk % NS], (nk / NS) & 1,
+                                                      &bar[P::bP + 2 * tile + b], (n >> 1) & 1, limit));
                 if (!alive) break;
                 tc_fence_after();
                 const uint64_t dv = dv0 + slot * (P::kBlk >> 4);
                 const uint32_t p_tm = s0_tm + 64 * b, idO = n < n8 ? idO8 : idOraw;
+                if (elected) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) umma_bf16_ts(o_tm, p_tm + 8 * k, dv + (uint64_t)(2 * D * k), idO, n > 0 || k > 0);
-                if (n >= n8) {   // the low parts of the raw block's weights
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16_ts(o_tm, p_tm + 8 * k, dv + (uint64_t)(2 * D * k), idO, n > 0 || k > 0);
+                    if (n >= n8) {   // the low parts of the raw block's weights
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) umma_bf16_ts(o_tm, p_tm + 32 + 8 * k, dv + (uint64_t)(2 * D * k), idO, 1);
+                        for (int k = 0; k < 4; ++k)
+                            umma_bf16_ts(o_tm, p_tm + 32 + 8 * k, dv + (uint64_t)(2 * D * k), idO, 1);
+                    }
                 }
-                umma_commit(&bar[P::bPV + 2 * tile + b]);
-                umma_commit(&bar[P::bVFree + slot]);
-                if (n + 2 < nb) alive = issue_s(n + 2);
+                if (more) issue_s(n + 2);
+                if (elected) {
+                    umma_commit(&bar[P::bVFree + slot]);
+                    if (n == nb - 2) umma_commit(&bar[P::bPV + tile]);
+                }
             }
-            if (!alive) atomicOr(a.err, kErrTimeout);
-            umma_commit(&bar[P::bDrain]);
-            if (!mbar_wait_bounded(&bar[P::bDrain], 0, limit)) atomicOr(a.err, kErrTimeout);
+            if (elected) {
+                if (!alive) atomicOr(a.err, kErrTimeout);
+                umma_commit(&bar[P::bDrain]);
+                if (!mbar_wait_bounded(&bar[P::bDrain], 0, limit)) atomicOr(a.err, kErrTimeout);
+            }
         }
     } else if (t >= P::kKeys0) {
-        // ---- key and value warps: 4 warps each convert a block at a time, its loads one block ahead ----
-        if constexpr (P::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+        // ---- key and value warps: each role's convert a block at a time, its loads one block ahead (two ahead, with the
+        // loop unrolled by two, measured slower: the roles share one instruction cache) ----
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
         const bool is_v = t >= P::kVals0;
-        const int cw = warp & 3, kr = lane & 7, ch = lane >> 3;   // warp of the role; key of 8 and 16-byte chunk of 64
+        const int cw = warp % P::CW, kr = lane & 7, ch = lane >> 3;   // warp of the role; key of 8 and 16-byte chunk of 64
         const bf *tail = static_cast<const bf *>(a.c.tail);
         const int8_t *pool = (is_v ? a.c.v : a.c.k) + (int64_t)h * (kKvBlock * D) + kr * D + ch * 16;
         const int64_t stride = (int64_t)a.Hkv * (kKvBlock * D);
         uint64_t *full = &bar[is_v ? P::bVFull : P::bKFull], *free = &bar[is_v ? P::bVFree : P::bKFree];
         unsigned char *slots = sm + (is_v ? P::kV : P::kK) + kr * 16 + ch * 256;
-        // load i of this warp: 8 keys x 64 columns, key group (cw + 4 i) / kVec, column group (cw + 4 i) % kVec
+        // load i of this warp: 8 keys x 64 columns, key group (cw + CW i) / kVec, column group (cw + CW i) % kVec
         uint4 w[P::kLoads];
         auto load = [&](int n) {
+            n = min(n, nb - 1);   // a raw block: page 0, not used
             const int8_t *src = pool + info[n].page * stride;
 #pragma unroll
             for (int i = 0; i < P::kLoads; ++i) {
-                const int j = cw + 4 * i;
+                const int j = cw + P::CW * i;
                 w[i] = __ldg(reinterpret_cast<const uint4 *>(src + j / P::kVec * (8 * D) + j % P::kVec * 64));
             }
         };
@@ -317,7 +367,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             constexpr bool V = decltype(vals)::value;
 #pragma unroll
             for (int i = 0; i < P::kLoads; ++i) {
-                const int j = cw + 4 * i;
+                const int j = cw + P::CW * i;
                 const uint2 x0 = i8_to_f16x4<V>(w[i].x), x1 = i8_to_f16x4<V>(w[i].y), x2 = i8_to_f16x4<V>(w[i].z), x3 = i8_to_f16x4<V>(w[i].w);
                 unsigned char *o = dst + j / P::kVec * (D * 16) + j % P::kVec * 1024;
                 *reinterpret_cast<uint4 *>(o) = make_uint4(x0.x, x0.y, x1.x, x1.y);
@@ -327,7 +377,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         // a raw block: the tail's rows, then the new ones, zero past the last
         auto store_raw = [&](int block, unsigned char *dst) {
 #pragma unroll 1
-            for (int kg = cw; kg < 8; kg += 4) {
+            for (int kg = cw; kg < 8; kg += P::CW) {
                 const int off = kg * 8 + kr, pos = block * kKvBlock + off;
                 const bf *src = nullptr;
                 if (pos < pos0) src = tail + kv_tail_offset(u.slot, u.src, is_v, h, a.Hkv, D) + (int64_t)off * D;
@@ -376,7 +426,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
 #pragma unroll 1
         for (int n = 0; n < nb; ++n) {
             const int slot = n % NS;
-            if (n >= NS && !mbar_wait_bounded(&free[slot], (n / NS - 1) & 1, limit)) {
+            if (n >= NS && !warp_wait(&free[slot], (n / NS - 1) & 1, limit)) {
                 alive = false;
                 break;
             }
@@ -384,31 +434,31 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             if (n < n8) {
                 if (is_v) store(std::true_type{}, dst);
                 else store(std::false_type{}, dst);
-                load(min(n + 1, nb - 1));   // a raw block: page 0, not used
+                load(n + 1);
             } else {
                 store_raw(blo + n - n8, dst);
             }
             fence_proxy_async();
-            if (n > 0 || is_v || a.skip_first_copy != 3) mbar_arrive(&full[slot]);   // 3: the test hook
+            if (n > 0 || is_v || a.skip_first_copy != 3) warp_arrive(&full[slot]);   // 3: the test hook
         }
         if (!alive && lane == 0) atomicOr(a.err, kErrTimeout);
-        kv_named_barrier(1, P::kMma);
-    } else if (warp / 4 < nt) {
+        kv_named_barrier(1, P::NT - P::kSoft0);
+    } else if (warp / 4 <= nt) {
         // ---- softmax warps ----
-        if constexpr (P::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;\n");
-        const int tile = warp >> 2, r = r0 + t;    // t = 128 tile + row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;\n");
+        const int tr = t - P::kSoft0, tile = tr >> 7, r = r0 + tr;   // tr = 128 tile + row
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int pos = pos0 + r / a.G, blk = pos / kKvBlock, off = pos % kKvBlock;
         const uint32_t o_tm = tmem + lanes + P::kO + tile * D;
-        const float2 rq = row_q[t];
+        const float2 rq = row_q[tr];
         float m = -INFINITY, l = 0.f;
         auto block_step = [&](auto is_raw, int n) {
             constexpr bool raw = decltype(is_raw)::value;
             const int b = 2 * tile + (n & 1);
             const uint32_t s_tm = tmem + lanes + 64 * b;
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bS + b], (n >> 1) & 1, limit))) return false;
+            if (!warp_wait(&bar[P::bS + b], (n >> 1) & 1, limit)) return false;
             // the key warps' scalings; no later block takes the slot (the pass ends with its at most NS raw blocks)
-            if (raw && !__all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bKFull + n % NS], (n / NS) & 1, limit))) return false;
+            if (raw && !warp_wait(&bar[P::bKFull + n % NS], (n / NS) & 1, limit)) return false;
             tc_fence_after();
             const BlockInfo x = info[n];
             // keys of the block that the row sees: all or none of an 8-bit block, up to its own offset of its raw block
@@ -433,7 +483,11 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             }
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int j = 4; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+            for (int j = 4; j < 60; j += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[j + k], s[j + 4 + k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[60 + k]);
             const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, c1152 + x.lvs);
             float f = 1.f;
             if (see > 0 && top > m + 8.f) {    // also the row's first keys (m = -inf)
@@ -443,7 +497,9 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             }
             // O is rescaled once the product that is under way on it is done (a row's first keys meet O = 0)
             if (n > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bPV + 2 * tile + ((n - 1) & 1)], ((n - 1) >> 1) & 1, limit)))
+                // the next scores were issued after that product
+                const bool last = n == nb - 1;
+                if (!warp_wait(&bar[last ? P::bPV + tile : P::bS + 2 * tile + ((n + 1) & 1)], last ? 0 : ((n + 1) >> 1) & 1, limit))
                     return false;
                 tc_fence_after();
 #pragma unroll 1
@@ -485,7 +541,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             l = fmaf(s0 + s1, x.ivs, l);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&bar[P::bP + b]);
+            warp_arrive(&bar[P::bP + b]);
             return true;
         };
 #pragma unroll 1
@@ -493,11 +549,11 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
 #pragma unroll 1
         for (int n = n8; alive && n < nb; ++n) alive = block_step(std::true_type{}, n);
         // every product is done, and the value warps have said what they left out: the rows
-        kv_named_barrier(1, P::kMma);
-        if (alive) alive = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bDrain], 0, limit));
+        kv_named_barrier(1, P::NT - P::kSoft0);
+        if (alive) alive = warp_wait(&bar[P::bDrain], 0, limit);
         if (alive) {
             tc_fence_after();
-            const bool live = t < rows_here;
+            const bool live = tr < rows_here;
             const int head = h * a.G + r % a.G, tok = r / a.G;
             const bool one = last_seg == 0;
             const float inv = one ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;   // no key: zero; NaN stays
@@ -547,8 +603,8 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             atomicOr(a.err, kErrTimeout);
         }
     } else {
-        if constexpr (P::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;\n");
-        kv_named_barrier(1, P::kMma);   // the second tile's warps, without rows
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;\n");
+        kv_named_barrier(1, P::NT - P::kSoft0);   // the second tile's warps, without rows
     }
     tc_fence_before();
     __syncthreads();
