@@ -40,10 +40,10 @@ __device__ __forceinline__ uint2 i8_to_f16x4(uint32_t x) {
     return make_uint2(*reinterpret_cast<const uint32_t *>(&c), *reinterpret_cast<const uint32_t *>(&d));
 }
 
-// log2 of the value scale of block b of a slot; an all-zero block (any scale serves) counts with the nearest of the eight
-// blocks before it that has one
-__device__ __forceinline__ float kv_log2_vscale(const KvAttn &a, const int32_t *table, int b, int h) {
-    for (int i = 0; i <= 8 && b >= 0; ++i, --b) {
+// log2 of the value scale of block b of a slot. An all-zero block (any scale serves) counts with the nearest before it
+// that has one, `tries` blocks looked at in all.
+__device__ __forceinline__ float kv_log2_vscale(const KvAttn &a, const int32_t *table, int b, int h, int tries) {
+    for (; tries > 0 && b >= 0; --tries, --b) {
         const int page = table[b];
         if ((unsigned)page >= (unsigned)a.c.n_pages) break;
         const float vs = a.c.v_scale[(int64_t)page * a.Hkv + h];

@@ -8,7 +8,7 @@
 //                 row's own block, which is read as it came, is scaled by a power of two like a row of Q.
 //   O += P V      128 rows x d, K = 64 keys: P in TMEM as the A operand, V in shared memory. An 8-bit block: V int8 -> fp16
 //                 (exact), P = 2^{c s + log2 vs - m} with the block's value scale vs in the weight and m the running
-//                 maximum of exactly that exponent, so P <= 2^8 whatever the scales, and fp16 rounds it by 2^-11 of its
+//                 maximum of exactly that exponent, so P <= 2^14 whatever the scales, and fp16 rounds it by 2^-11 of its
 //                 size (2^-25 absolute below 2^-14, where a key adds next to nothing). The row's own block: V bf16, P in
 //                 two bf16 products, its upper and lower 8 bits: a row with few keys has nothing to average a rounding
 //                 out. The sum l takes the unrounded weights, 2^{c s - m}.
@@ -24,7 +24,7 @@
 // tensor core waited for each other, 5,600 against 2,560 cycles per 128 keys of the two tiles). The weights overwrite the
 // scores that they came from.
 //
-// The running maximum m only moves when a block exceeds it by 8 (log2 domain): O is rescaled (by the softmax warps, after
+// The running maximum m only moves when a block exceeds it by 14 (log2 domain; fp16 ends at 2^16): O is rescaled (by the softmax warps, after
 // the product before it) only then. Every decision is a row's own and every block is one softmax step, so a row's bits do
 // not depend on the rows beside it.
 #include "kv_attn.cuh"
@@ -112,6 +112,8 @@ __device__ __forceinline__ bool drop_not_finite(uint4 &u) {
     return any;
 }
 
+constexpr float kSlack = 14.f;   // how far a weight's exponent may pass the running maximum
+
 template <int D>
 struct PromptPlan {
     static constexpr int NQ = D == 256 ? 1 : 2;              // MMA tiles of 128 rows
@@ -163,9 +165,9 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     grid_dep_launch();
     // later units (longer contexts) first: a causal launch then ends on its short ones
     const int ui = a.unit0 + n_units - 1 - (int)(blockIdx.x / row_tiles), rt = blockIdx.x % row_tiles, h = blockIdx.y, seg = blockIdx.z;
+    const KvUnit u = kv_load_unit(a.units, ui);   // inside the map whatever the count
     const int unit1 = min(a.unit0 + n_units, a.counts[0]);
     if (ui >= unit1) return;
-    const KvUnit u = kv_load_unit(a.units, ui);
     bool ok = kv_unit_ok(u, a.c, a.n_rows) && u.count <= a.max_new && u.block / a.seg_blocks < a.n_seg;
     // the span's first unit works for all of it
     if (ok && ui > a.unit0 && u.block % span != 0) {
@@ -224,68 +226,74 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         tmem_alloc(tslot, P::kTmemCols);
         tmem_relinquish();
     }
+    // Q: a warp takes 32 / (d / 8) rows at a time, a lane 8 columns; the loads are under way while the scales are fetched
+    constexpr int LPR = D / 8, RPW = 32 / LPR, IT = (P::R + P::NT / 32 * RPW - 1) / (P::NT / 32 * RPW);
+    uint4 qw[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int r = (i * (P::NT / 32) + warp) * RPW + lane / LPR, rr = r0 + r;
+        qw[i] = make_uint4(0, 0, 0, 0);
+        if (r < rows_here)
+            qw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const bf *>(a.q) +
+                                                          ((int64_t)(u.row + rr / a.G) * a.Hq + h * a.G + rr % a.G) * D + lane % LPR * 8));
+    }
     // pages and scales of the pass's blocks
     const int32_t *table = a.c.table + (int64_t)u.slot * a.c.max_blocks;
     for (int i = t; i < nb; i += P::NT) {
         BlockInfo x = {0, a.scale_log2, 0.f, 1.f};
         if (i < n8) {
             x.page = table[c0 + i];
-            x.lvs = kv_log2_vscale(a, table, c0 + i, h);
-            x.ivs = ex2(-x.lvs);
-            if ((unsigned)x.page < (unsigned)a.c.n_pages) {
-                x.c = a.scale_log2 * a.c.k_scale[(int64_t)x.page * a.Hkv + h];
-            } else {
+            const bool in = (unsigned)x.page < (unsigned)a.c.n_pages;
+            if (!in) {
                 x.page = 0;                        // in bounds; the result is reported as invalid
-                x.c = 0.f;
                 atomicOr(a.err, kErrKvBounds);
             }
+            const int64_t ph = (int64_t)x.page * a.Hkv + h;
+            const float ks = a.c.k_scale[ph], vs = a.c.v_scale[ph];
+            x.c = in ? a.scale_log2 * ks : 0.f;
+            x.lvs = in && vs != 0.f ? log2f(vs) : kv_log2_vscale(a, table, c0 + i - 1, h, 8);
+            x.ivs = ex2(-x.lvs);
         } else {
-            x.lvs = kv_log2_vscale(a, table, blo + i - n8 - 1, h);
+            x.lvs = kv_log2_vscale(a, table, blo + i - n8 - 1, h, 9);
         }
         info[i] = x;
     }
-    // Q: a warp takes 32 / (d / 8) rows at a time, a lane 8 columns; K-major core matrices (8 rows x 16 bytes)
-    {
-        constexpr int LPR = D / 8, RPW = 32 / LPR;
-        const int c = lane % LPR;
-        for (int rb = warp * RPW; rb < nt * 128; rb += P::NT / 32 * RPW) {
-            const int r = rb + lane / LPR, rr = r0 + r;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (r < rows_here)
-                w = *reinterpret_cast<const uint4 *>(static_cast<const bf *>(a.q) +
-                                                     ((int64_t)(u.row + rr / a.G) * a.Hq + h * a.G + rr % a.G) * D + c * 8);
-            float f[8], top = 0.f, sum = 0.f;
-            b8_to_f(w, f);
+    // Q into K-major core matrices (8 rows x 16 bytes)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]));
+    for (int i = 0; i < IT; ++i) {
+        const int r = (i * (P::NT / 32) + warp) * RPW + lane / LPR, c = lane % LPR;
+        float f[8], top = 0.f, sum = 0.f;
+        b8_to_f(qw[i], f);
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            float back;
-            const float up = pow2_to_2_15(top, back);
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]));
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] *= up;
-            w = f8_to_h8(f);
-            h8_to_f(w, f);
+        for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float back;
+        const float up = pow2_to_2_15(top, back);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum += f[k];
+        for (int k = 0; k < 8; ++k) f[k] *= up;
+        const uint4 w = f8_to_h8(f);
+        h8_to_f(w, f);
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            *reinterpret_cast<uint4 *>(sm + P::kQ + (r >> 7) * P::kTile + ((r & 127) >> 3) * (D * 16) + c * 128 + (r & 7) * 16) = w;
-            if (c == 0) row_q[r] = make_float2(back, 1152.f * sum);
-        }
+        for (int k = 0; k < 8; ++k) sum += f[k];
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (r >= P::R) continue;
+        *reinterpret_cast<uint4 *>(sm + P::kQ + (r >> 7) * P::kTile + ((r & 127) >> 3) * (D * 16) + c * 128 + (r & 7) * 16) = w;
+        if (c == 0) row_q[r] = make_float2(back, 1152.f * sum);
     }
     fence_proxy_async();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tslot;
+    constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's
     const long long limit = a.wait_limit;
     bool alive = true;
 
     if (t < P::kSoft0) {
         // ---- the issuing warps, one per tile: whole warps in step, one elected lane issues (a lane of its own in a divergent
         // branch takes 84 cycles per MMA beside busy warps, an elected lane of a warp in step 53, measured) ----
-        const int tile = warp;
+        const int tile = __shfl_sync(0xffffffffu, warp, 0);   // the same in every lane, and the compiler sees it
         if (tile < nt) {
             constexpr uint32_t idS = umma_idesc_f16(128, 64, 0, 0), idO8 = umma_idesc_f16(128, D, 0, 1),
                                idOraw = umma_idesc_bf16(128, D, 0, 1);
@@ -490,7 +498,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[60 + k]);
             const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, c1152 + x.lvs);
             float f = 1.f;
-            if (see > 0 && top > m + 8.f) {    // also the row's first keys (m = -inf)
+            if (see > 0 && top > m + kSlack) {    // also the row's first keys (m = -inf)
                 f = ex2(m - top);              // 0 then
                 m = top;
                 l *= f;
@@ -503,13 +511,17 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                     return false;
                 tc_fence_after();
 #pragma unroll 1
-                for (int k0 = 0; k0 < D; k0 += 16) {
-                    uint32_t w[16];
-                    tmem_ld16_nowait(o_tm + k0, w);
-                    tmem_wait_ld(w);
+                for (int k0 = 0; k0 < D; k0 += 32) {
+                    uint32_t w[2][16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
-                    tmem_st16(o_tm + k0, w);
+                    for (int j = 0; j < 2; ++j) tmem_ld16_nowait(o_tm + k0 + 16 * j, w[j]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        tmem_wait_ld(w[j]);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) w[j][k] = __float_as_uint(__uint_as_float(w[j][k]) * f);
+                        tmem_st16(o_tm + k0 + 16 * j, w[j]);
+                    }
                 }
                 tmem_wait_st();
             }
@@ -557,46 +569,59 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             const int head = h * a.G + r % a.G, tok = r / a.G;
             const bool one = last_seg == 0;
             const float inv = one ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;   // no key: zero; NaN stays
-            bf *out = static_cast<bf *>(a.out) + ((int64_t)(u.row + tok) * a.Hq + head) * D;
             int64_t pr = 0;
             if (live && !one) {
                 pr = kv_part_row(a, ui + blk - u.block, seg, blk == u.block ? tok : off, head);
                 a.part_ml[pr] = make_float2(m, l);
             }
             const bool fix = live && seg == last_seg && bad_v[min(max(blk - blo, 0), 3)] != 0;
+            // The warp's 32 rows pass through shared memory (Q's, which every product has read), 128 bytes of a row at a time
+            // with the 16-byte chunks of row i at chunk ^ (i % 8), so that the stores to global memory are of whole rows.
+            unsigned char *stage = sm + P::kQ + (warp - P::kSoft0 / 32) * (32 * 128);
+            const int64_t dst_row = one ? (int64_t)(u.row + tok) * a.Hq + head : pr;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-                uint32_t w[16];
-                tmem_ld16_nowait(o_tm + c, w);
-                tmem_wait_ld(w);
-                float v[16];
+            for (int c = 0; c < D; c += 32) {
+                uint32_t w[2][16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(w[k]) * inv;
+                for (int j = 0; j < 2; ++j) tmem_ld16_nowait(o_tm + c + 16 * j, w[j]);
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    tmem_wait_ld(w[j]);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[16 * j + k] = __uint_as_float(w[j][k]) * inv;
+                }
                 if (fix) {
                     for (int j = 0; j <= off; ++j) {
                         const int kp = blk * kKvBlock + j;
                         const bf *src = kp < pos0 ? static_cast<const bf *>(a.c.tail) + kv_tail_offset(u.slot, u.src, 1, h, a.Hkv, D) + (int64_t)j * D
                                                   : static_cast<const bf *>(a.v_new) + ((int64_t)(u.row + kp - pos0) * a.Hkv + h) * D;
-                        for (int k = 0; k < 16; ++k) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
                             const float y = to_f(src[c + k]);
                             if (!(fabsf(y) <= 3.4e38f)) v[k] += y;
                         }
                     }
                 }
-                if (!live) continue;
-                if (one) {
-                    uint32_t o[8];
+                __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-                        o[k] = *reinterpret_cast<const uint32_t *>(&x);
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<float4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                        make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                __syncwarp();
+#pragma unroll 1
+                for (int i = lane >> 3; i < 32; i += 4) {   // 4 rows of 8 chunks a time
+                    const int k = lane & 7;
+                    const float4 x = *reinterpret_cast<const float4 *>(stage + i * 128 + ((k ^ (i & 7)) << 4));
+                    const int64_t row = __shfl_sync(0xffffffffu, dst_row, i);
+                    if (tr - lane + i >= rows_here) continue;
+                    if (one) {
+                        const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.x, x.y), y1 = __floats2bfloat162_rn(x.z, x.w);
+                        *reinterpret_cast<uint2 *>(static_cast<bf *>(a.out) + row * D + c + 4 * k) =
+                            make_uint2(*reinterpret_cast<const uint32_t *>(&y0), *reinterpret_cast<const uint32_t *>(&y1));
+                    } else {
+                        *reinterpret_cast<float4 *>(a.part_o + row * D + c + 4 * k) = x;
                     }
-                    *reinterpret_cast<uint4 *>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(a.part_o + pr * D + c);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 }
             }
         } else if (lane == 0) {

@@ -123,10 +123,10 @@ __global__ void __launch_bounds__(32 * kTokenWarps) kv_attn_token_kernel(const K
 #pragma unroll
     for (int i = 0; i < kTokenBlocks; ++i)
         if (w0 + i < w1) {
-            lv[i] = kv_log2_vscale(a, table, w0 + i, h);
+            lv[i] = kv_log2_vscale(a, table, w0 + i, h, 9);
             iv[i] = ex2(-lv[i]);
         }
-    const float lraw = raw_here ? kv_log2_vscale(a, table, u.block - 1, h) : 0.f;
+    const float lraw = raw_here ? kv_log2_vscale(a, table, u.block - 1, h, 9) : 0.f;
     uint32_t qa[J][4][2 * RF];   // per k-step: columns 0, 1 and 2, 3 of the lane's four, rows g (and g + 8)
     const bf *q = static_cast<const bf *>(a.q);
 #pragma unroll
