@@ -53,24 +53,42 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // named barrier `id` over n threads (whole warps)
 __device__ __forceinline__ void kv_named_barrier(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
 
-// One arrival per warp and one polling lane: an arrival or a test by 32 lanes is 32 passes through the shared-memory
-// pipe, which the MMA operands and the score loads fill already.
-__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+// mbarriers by 32-bit shared-memory address, waits bounded by `limit` polls.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, long long limit) {
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded(bar, parity, limit);
-    return __shfl_sync(0xffffffffu, ok, 0);
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int limit) {
+    for (int i = 0; i < limit; ++i)
+        if (bar_test(bar, parity)) return true;
+    return false;
 }
 // Three barriers tested together, their latencies overlapping.
-__device__ __forceinline__ bool wait3(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, uint64_t *b2, uint32_t p2, long long limit) {
-    for (long long i = 0; i < limit; ++i) {
-        const bool x = mbar_try_wait(b0, p0), y = mbar_try_wait(b1, p1), z = mbar_try_wait(b2, p2);
+__device__ __forceinline__ bool bar_wait3(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2, int limit) {
+    for (int i = 0; i < limit; ++i) {
+        const bool x = bar_test(b0, p0), y = bar_test(b1, p1), z = bar_test(b2, p2);
         if (x && y && z) return true;
     }
     return false;
+}
+// One arrival per warp and one polling lane: an arrival or a test by 32 lanes is 32 passes through the shared-memory
+// pipe, which the MMA operands and the score loads fill already.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int limit) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = bar_wait(bar, parity, limit);
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void bar_commit(uint32_t bar) {   // once the MMAs this thread issued are done
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -131,9 +149,9 @@ struct PromptPlan {
     static constexpr uint32_t kRawK = kRow + R * 8;                  // float [4][64]: the scalings of the raw blocks' keys
     static constexpr uint32_t kBar = kRawK + 4 * 64 * 4;
     // barriers: key and value slots full and free, scores and weights of (tile, buffer), a tile's product before its last,
-    // all products
+    // all products, the queries and the blocks' scales
     static constexpr int bKFull = 0, bKFree = NS, bVFull = 2 * NS, bVFree = 3 * NS, bS = 4 * NS, bP = bS + 2 * NQ,
-                         bPV = bP + 2 * NQ, bDrain = bPV + NQ, kNBar = bDrain + 1;
+                         bPV = bP + 2 * NQ, bDrain = bPV + NQ, bReady = bDrain + 1, kNBar = bReady + 1;
     static constexpr uint32_t kSlot = kBar + (kNBar + 1) / 2 * 16;
     static constexpr uint32_t kBad = kSlot + 16;             // per raw block of the span: it has a value that is not finite
     static constexpr uint32_t kBytes = kBad + 16;
@@ -142,8 +160,8 @@ struct PromptPlan {
     static constexpr int kVec = D / 64;                      // 64-column groups
     static constexpr int kLoads = 8 * kVec / CW;             // 16-byte loads of a key or value thread per block
     // Registers: an SM partition's 512 per lane hold 5 of the 20 warps (two tiles) at 96, or 6 of the 24 (one tile) at 80.
-    // The key and value warps go down to 64 and the softmax warps up to 128; per partition 2 x 32 given, 2 x 32 taken (two
-    // tiles), 4 x 16 given, 48 taken (one).
+    // Then the issuing, key and value warps go down to 64 and the softmax warps up to 144: per partition
+    // 64 + 2 x 144 + 2 x 64 = 480 of 480 (two tiles), 64 + 144 + 4 x 64 = 464 of 480 (one tile).
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -190,7 +208,9 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     if (r0 >= n_row || seg > last_seg) return;
 
     extern __shared__ __align__(1024) unsigned char sm[];
-    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + P::kBar);
+    uint64_t *bar64 = reinterpret_cast<uint64_t *>(sm + P::kBar);
+    const uint32_t bar0 = smem_addr(bar64);
+    auto bar = [&](int i) { return bar0 + 8 * i; };
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + P::kSlot);
     uint32_t *bad_v = reinterpret_cast<uint32_t *>(sm + P::kBad);
     BlockInfo *info = reinterpret_cast<BlockInfo *>(sm + P::kInfo);
@@ -208,17 +228,18 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
 
     if (t == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&bar[P::bKFull + i], P::CW);
-            mbar_init(&bar[P::bVFull + i], P::CW);
-            mbar_init(&bar[P::bKFree + i], nt);
-            mbar_init(&bar[P::bVFree + i], nt);
+            mbar_init(&bar64[P::bKFull + i], P::CW);
+            mbar_init(&bar64[P::bVFull + i], P::CW);
+            mbar_init(&bar64[P::bKFree + i], nt);
+            mbar_init(&bar64[P::bVFree + i], nt);
         }
         for (int i = 0; i < 2 * P::NQ; ++i) {
-            mbar_init(&bar[P::bS + i], 1);
-            mbar_init(&bar[P::bP + i], 4);
+            mbar_init(&bar64[P::bS + i], 1);
+            mbar_init(&bar64[P::bP + i], 4);
         }
-        for (int i = 0; i < P::NQ; ++i) mbar_init(&bar[P::bPV + i], 1);
-        mbar_init(&bar[P::bDrain], nt);
+        for (int i = 0; i < P::NQ; ++i) mbar_init(&bar64[P::bPV + i], 1);
+        mbar_init(&bar64[P::bDrain], nt);
+        mbar_init(&bar64[P::bReady], P::NT / 32);
         mbar_init_fence();
         for (int i = 0; i < 4; ++i) bad_v[i] = 0;
     }
@@ -226,71 +247,63 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         tmem_alloc(tslot, P::kTmemCols);
         tmem_relinquish();
     }
-    // Q: a warp takes 32 / (d / 8) rows at a time, a lane 8 columns; the loads are under way while the scales are fetched
-    constexpr int LPR = D / 8, RPW = 32 / LPR, IT = (P::R + P::NT / 32 * RPW - 1) / (P::NT / 32 * RPW);
-    uint4 qw[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int r = (i * (P::NT / 32) + warp) * RPW + lane / LPR, rr = r0 + r;
-        qw[i] = make_uint4(0, 0, 0, 0);
-        if (r < rows_here)
-            qw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const bf *>(a.q) +
-                                                          ((int64_t)(u.row + rr / a.G) * a.Hq + h * a.G + rr % a.G) * D + lane % LPR * 8));
-    }
-    // pages and scales of the pass's blocks
-    const int32_t *table = a.c.table + (int64_t)u.slot * a.c.max_blocks;
-    for (int i = t; i < nb; i += P::NT) {
-        BlockInfo x = {0, a.scale_log2, 0.f, 1.f};
-        if (i < n8) {
-            x.page = table[c0 + i];
-            const bool in = (unsigned)x.page < (unsigned)a.c.n_pages;
-            if (!in) {
-                x.page = 0;                        // in bounds; the result is reported as invalid
-                atomicOr(a.err, kErrKvBounds);
-            }
-            const int64_t ph = (int64_t)x.page * a.Hkv + h;
-            const float ks = a.c.k_scale[ph], vs = a.c.v_scale[ph];
-            x.c = in ? a.scale_log2 * ks : 0.f;
-            x.lvs = in && vs != 0.f ? log2f(vs) : kv_log2_vscale(a, table, c0 + i - 1, h, 8);
-            x.ivs = ex2(-x.lvs);
-        } else {
-            x.lvs = kv_log2_vscale(a, table, blo + i - n8 - 1, h, 9);
-        }
-        info[i] = x;
-    }
-    // Q into K-major core matrices (8 rows x 16 bytes)
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int r = (i * (P::NT / 32) + warp) * RPW + lane / LPR, c = lane % LPR;
-        float f[8], top = 0.f, sum = 0.f;
-        b8_to_f(qw[i], f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]));
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float back;
-        const float up = pow2_to_2_15(top, back);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] *= up;
-        const uint4 w = f8_to_h8(f);
-        h8_to_f(w, f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum += f[k];
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (r >= P::R) continue;
-        *reinterpret_cast<uint4 *>(sm + P::kQ + (r >> 7) * P::kTile + ((r & 127) >> 3) * (D * 16) + c * 128 + (r & 7) * 16) = w;
-        if (c == 0) row_q[r] = make_float2(back, 1152.f * sum);
-    }
-    fence_proxy_async();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's
-    const long long limit = a.wait_limit;
+    const int limit = (int)min(a.wait_limit, 1LL << 30);
     bool alive = true;
 
+    if (t < P::kKeys0) {
+        // ---- the queries, by the issuing and the softmax warps while the first blocks are fetched: a warp takes 32 / (d / 8)
+        // rows at a time, a lane 8 columns; into K-major core matrices (8 rows x 16 bytes) ----
+        constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = P::kKeys0 / 32 * RPW, IT = 4;   // IT loads in flight
+        const int c = lane % LPR;
+#pragma unroll 1
+        for (int rb = warp * RPW + lane / LPR; rb - lane / LPR < nt * 128; rb += IT * STEP) {
+            uint4 qw[IT];
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int r = rb + i * STEP, rr = r0 + r;
+                qw[i] = make_uint4(0, 0, 0, 0);
+                if (r < rows_here)
+                    qw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const bf *>(a.q) +
+                                                                  ((int64_t)(u.row + rr / a.G) * a.Hq + h * a.G + rr % a.G) * D + c * 8));
+            }
+#pragma unroll 1
+            for (int i = 0; i < IT; ++i) {
+                const int r = rb + i * STEP;
+                uint4 w = qw[0];
+#pragma unroll
+                for (int k = 0; k + 1 < IT; ++k) qw[k] = qw[k + 1];
+                float f[8], top = 0.f, sum = 0.f;
+                b8_to_f(w, f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    top = fmaxf(top, fabsf(f[k]));
+                    sum += f[k];
+                }
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) {
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                }
+                float back;
+                const float up = pow2_to_2_15(top, back);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] *= up;
+                w = f8_to_h8(f);
+                if (r >= nt * 128) continue;
+                *reinterpret_cast<uint4 *>(sm + P::kQ + (r >> 7) * P::kTile + ((r & 127) >> 3) * (D * 16) + c * 128 + (r & 7) * 16) = w;
+                if (c == 0) row_q[r] = make_float2(back, 1152.f * up * sum);
+            }
+        }
+        fence_proxy_async();
+        warp_arrive(bar(P::bReady));
+        alive = warp_wait(bar(P::bReady), 0, limit);
+    }
     if (t < P::kSoft0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
         // ---- the issuing warps, one per tile: whole warps in step, one elected lane issues (a lane of its own in a divergent
         // branch takes 84 cycles per MMA beside busy warps, an elected lane of a warp in step 53, measured) ----
         const int tile = __shfl_sync(0xffffffffu, warp, 0);   // the same in every lane, and the compiler sees it
@@ -307,12 +320,13 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 if (elected) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) umma_bf16(s0_tm + 64 * b, dq + 16 * k, dk + 16 * k, idS, k > 0);
-                    umma_commit(&bar[P::bS + 2 * tile + b]);
-                    umma_commit(&bar[P::bKFree + slot]);
+                    bar_commit(bar(P::bS + 2 * tile + b));
+                    bar_commit(bar(P::bKFree + slot));
                 }
             };
+            tc_fence_after();
             for (int n = 0; alive && n < min(nb, 2); ++n) {
-                alive = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[P::bKFull + n % NS], (n / NS) & 1, limit));
+                alive = __all_sync(0xffffffffu, bar_wait(bar(P::bKFull + n % NS), (n / NS) & 1, limit));
                 tc_fence_after();
                 if (alive) issue_s(n);
             }
@@ -321,8 +335,8 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 const int slot = n % NS, b = n & 1;
                 const bool more = n + 2 < nb;
                 const int nk = more ? n + 2 : n;   // the keys of the product that follows (n: there already)
-                alive = __all_sync(0xffffffffu, wait3(&bar[P::bVFull + slot], (n / NS) & 1, &bar[P::bKFull + nk % NS], (nk / NS) & 1,
-                                                      &bar[P::bP + 2 * tile + b], (n >> 1) & 1, limit));
+                alive = __all_sync(0xffffffffu, bar_wait3(bar(P::bVFull + slot), (n / NS) & 1, bar(P::bKFull + nk % NS), (nk / NS) & 1,
+                                                      bar(P::bP + 2 * tile + b), (n >> 1) & 1, limit));
                 if (!alive) break;
                 tc_fence_after();
                 const uint64_t dv = dv0 + slot * (P::kBlk >> 4);
@@ -339,14 +353,14 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 }
                 if (more) issue_s(n + 2);
                 if (elected) {
-                    umma_commit(&bar[P::bVFree + slot]);
-                    if (n == nb - 2) umma_commit(&bar[P::bPV + tile]);
+                    bar_commit(bar(P::bVFree + slot));
+                    if (n == nb - 2) bar_commit(bar(P::bPV + tile));
                 }
             }
             if (elected) {
                 if (!alive) atomicOr(a.err, kErrTimeout);
-                umma_commit(&bar[P::bDrain]);
-                if (!mbar_wait_bounded(&bar[P::bDrain], 0, limit)) atomicOr(a.err, kErrTimeout);
+                bar_commit(bar(P::bDrain));
+                if (!bar_wait(bar(P::bDrain), 0, limit)) atomicOr(a.err, kErrTimeout);
             }
         }
     } else if (t >= P::kKeys0) {
@@ -354,11 +368,34 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         // loop unrolled by two, measured slower: the roles share one instruction cache) ----
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
         const bool is_v = t >= P::kVals0;
+        // pages and scales of the pass's blocks, which the softmax warps read as well
+        const int32_t *table = a.c.table + (int64_t)u.slot * a.c.max_blocks;
+        for (int i = t - P::kKeys0; i < nb; i += 64 * P::CW) {
+            BlockInfo x = {0, a.scale_log2, 0.f, 1.f};
+            if (i < n8) {
+                x.page = table[c0 + i];
+                const bool in = (unsigned)x.page < (unsigned)a.c.n_pages;
+                if (!in) {
+                    x.page = 0;                        // in bounds; the result is reported as invalid
+                    atomicOr(a.err, kErrKvBounds);
+                }
+                const int64_t ph = (int64_t)x.page * a.Hkv + h;
+                const float ks = a.c.k_scale[ph], vs = a.c.v_scale[ph];
+                x.c = in ? a.scale_log2 * ks : 0.f;
+                x.lvs = in && vs != 0.f ? log2f(vs) : kv_log2_vscale(a, table, c0 + i - 1, h, 8);
+                x.ivs = ex2(-x.lvs);
+            } else {
+                x.lvs = kv_log2_vscale(a, table, blo + i - n8 - 1, h, 9);
+            }
+            info[i] = x;
+        }
+        kv_named_barrier(2, 64 * P::CW);
+        warp_arrive(bar(P::bReady));
         const int cw = warp % P::CW, kr = lane & 7, ch = lane >> 3;   // warp of the role; key of 8 and 16-byte chunk of 64
         const bf *tail = static_cast<const bf *>(a.c.tail);
         const int8_t *pool = (is_v ? a.c.v : a.c.k) + (int64_t)h * (kKvBlock * D) + kr * D + ch * 16;
         const int64_t stride = (int64_t)a.Hkv * (kKvBlock * D);
-        uint64_t *full = &bar[is_v ? P::bVFull : P::bKFull], *free = &bar[is_v ? P::bVFree : P::bKFree];
+        const uint32_t full = bar(is_v ? P::bVFull : P::bKFull), free = bar(is_v ? P::bVFree : P::bKFree);
         unsigned char *slots = sm + (is_v ? P::kV : P::kK) + kr * 16 + ch * 256;
         // load i of this warp: 8 keys x 64 columns, key group (cw + CW i) / kVec, column group (cw + CW i) % kVec
         uint4 w[P::kLoads];
@@ -434,7 +471,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
 #pragma unroll 1
         for (int n = 0; n < nb; ++n) {
             const int slot = n % NS;
-            if (n >= NS && !warp_wait(&free[slot], (n / NS - 1) & 1, limit)) {
+            if (n >= NS && !warp_wait(free + 8 * slot, (n / NS - 1) & 1, limit)) {
                 alive = false;
                 break;
             }
@@ -447,13 +484,13 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 store_raw(blo + n - n8, dst);
             }
             fence_proxy_async();
-            if (n > 0 || is_v || a.skip_first_copy != 3) warp_arrive(&full[slot]);   // 3: the test hook
+            if (n > 0 || is_v || a.skip_first_copy != 3) warp_arrive(full + 8 * slot);   // 3: the test hook
         }
         if (!alive && lane == 0) atomicOr(a.err, kErrTimeout);
         kv_named_barrier(1, P::NT - P::kSoft0);
     } else if (warp / 4 <= nt) {
         // ---- softmax warps ----
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;\n");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;\n");
         const int tr = t - P::kSoft0, tile = tr >> 7, r = r0 + tr;   // tr = 128 tile + row
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int pos = pos0 + r / a.G, blk = pos / kKvBlock, off = pos % kKvBlock;
@@ -464,9 +501,9 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             constexpr bool raw = decltype(is_raw)::value;
             const int b = 2 * tile + (n & 1);
             const uint32_t s_tm = tmem + lanes + 64 * b;
-            if (!warp_wait(&bar[P::bS + b], (n >> 1) & 1, limit)) return false;
+            if (!warp_wait(bar(P::bS + b), (n >> 1) & 1, limit)) return false;
             // the key warps' scalings; no later block takes the slot (the pass ends with its at most NS raw blocks)
-            if (raw && !warp_wait(&bar[P::bKFull + n % NS], (n / NS) & 1, limit)) return false;
+            if (raw && !warp_wait(bar(P::bKFull + n % NS), (n / NS) & 1, limit)) return false;
             tc_fence_after();
             const BlockInfo x = info[n];
             // keys of the block that the row sees: all or none of an 8-bit block, up to its own offset of its raw block
@@ -507,7 +544,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             if (n > 0 && __any_sync(0xffffffffu, f != 1.f)) {
                 // the next scores were issued after that product
                 const bool last = n == nb - 1;
-                if (!warp_wait(&bar[last ? P::bPV + tile : P::bS + 2 * tile + ((n + 1) & 1)], last ? 0 : ((n + 1) >> 1) & 1, limit))
+                if (!warp_wait(bar(last ? P::bPV + tile : P::bS + 2 * tile + ((n + 1) & 1)), last ? 0 : ((n + 1) >> 1) & 1, limit))
                     return false;
                 tc_fence_after();
 #pragma unroll 1
@@ -553,7 +590,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             l = fmaf(s0 + s1, x.ivs, l);
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(&bar[P::bP + b]);
+            warp_arrive(bar(P::bP + b));
             return true;
         };
 #pragma unroll 1
@@ -562,7 +599,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         for (int n = n8; alive && n < nb; ++n) alive = block_step(std::true_type{}, n);
         // every product is done, and the value warps have said what they left out: the rows
         kv_named_barrier(1, P::NT - P::kSoft0);
-        if (alive) alive = warp_wait(&bar[P::bDrain], 0, limit);
+        if (alive) alive = warp_wait(bar(P::bDrain), 0, limit);
         if (alive) {
             tc_fence_after();
             const bool live = tr < rows_here;
@@ -628,7 +665,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             atomicOr(a.err, kErrTimeout);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;\n");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;\n");
         kv_named_barrier(1, P::NT - P::kSoft0);   // the second tile's warps, without rows
     }
     tc_fence_before();
