@@ -100,4 +100,4 @@ cudaError_t gdn_launch_kv_attn_token(const gdn::KvAttn &a, int d, int unit_bound
 // bf16 inputs, many rows:
 cudaError_t gdn_launch_kv_attn_prompt(const gdn::KvAttn &a, int d, int unit_bound, cudaStream_t st);
 // Joins the segments' partial results of every row that has more than one.
-cudaError_t gdn_launch_kv_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, cudaStream_t st);
+cudaError_t gdn_launch_kv_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int few, cudaStream_t st);

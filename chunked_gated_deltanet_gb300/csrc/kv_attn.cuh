@@ -4,7 +4,7 @@
 #include <cuda_fp16.h>
 
 #include "kv.cuh"
-#include "mma.cuh"
+#include "umma.cuh"
 
 namespace gdn {
 
@@ -38,6 +38,36 @@ __device__ __forceinline__ uint2 i8_to_f16x4(uint32_t x) {
     const __half2 c = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&off));
     const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&b), *reinterpret_cast<const __half2 *>(&off));
     return make_uint2(*reinterpret_cast<const uint32_t *>(&c), *reinterpret_cast<const uint32_t *>(&d));
+}
+
+__device__ __forceinline__ void b8_to_f(const uint4 &u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+// The power of two that brings x > 0 into [2^14, 2^15), and its inverse; 1 for 0 and what is not finite, at most 2^100.
+__device__ __forceinline__ float pow2_to_2_15(float x, float &back) {
+    int e = 14 + 127 - (int)(__float_as_uint(x) >> 23);   // x >= 0
+    if (x == 0.f || !(x <= 3.4e38f)) e = 0;
+    e = min(e, 100);
+    back = __uint_as_float((uint32_t)(127 - e) << 23);
+    return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
+// Zeroes the bf16 of a vector that are not finite; whether there was one.
+__device__ __forceinline__ bool drop_not_finite(uint4 &u) {
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if ((w[k] & 0x7F80u) == 0x7F80u) { w[k] &= 0xFFFF0000u; any = true; }
+        if ((w[k] & 0x7F800000u) == 0x7F800000u) { w[k] &= 0xFFFFu; any = true; }
+    }
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+    return any;
 }
 
 // log2 of the value scale of block b of a slot. An all-zero block (any scale serves) counts with the nearest before it

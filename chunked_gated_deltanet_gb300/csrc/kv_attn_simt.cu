@@ -280,6 +280,63 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttn a) {
     }
 }
 
+// The same for the few-row form, whose rows have many segments: a CTA per (token, query head), warp w taking segments
+// w, w + 8, ... and the eight sums added in order.
+template <typename InT, int D>
+__global__ void __launch_bounds__(256) kv_join_few_kernel(const KvAttn a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int ui = a.unit0 + blockIdx.x, r = blockIdx.y;
+    const KvUnit u = kv_load_unit(a.units, ui);
+    if (ui >= a.counts[0]) return;
+    const int n_seg = u.block / a.seg_blocks + 1;
+    if (!kv_unit_ok(u, a.c, a.n_rows) || u.count > a.max_new || n_seg > a.n_seg || n_seg == 1 || r >= u.count * a.Hq) return;
+    constexpr int W = D == 64 ? 2 : 4, N = D / (32 * W);
+    __shared__ float so[8][D], sl[8];
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int64_t stride = a.part_rows, pr = kv_part_row(a, ui, 0, 0, 0) + r;
+    float M = -INFINITY;
+    for (int s = lane; s < n_seg; s += 32) M = fmaxf(M, a.part_ml[s * stride + pr].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float base = M == -INFINITY ? 0.f : M;
+    float o[N][W], l = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int k = 0; k < W; ++k) o[j][k] = 0.f;
+#pragma unroll 4
+    for (int s = warp; s < n_seg; s += 8) {
+        const float2 ml = a.part_ml[s * stride + pr];
+        const float f = exp2f(ml.x - base);
+        l = fmaf(f, ml.y, l);
+        const float *src = a.part_o + (s * stride + pr) * D;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float v[W];
+            if constexpr (W == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(src + W * (lane + 32 * j));
+            else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src + W * (lane + 32 * j));
+#pragma unroll
+            for (int k = 0; k < W; ++k) o[j][k] = fmaf(f, v[k], o[j][k]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int k = 0; k < W; ++k) so[warp][W * (lane + 32 * j) + k] = o[j][k];
+    if (lane == 0) sl[warp] = l;
+    __syncthreads();
+    if (t >= D) return;
+    float x = 0.f, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        x += so[w][t];
+        L += sl[w];
+    }
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    static_cast<InT *>(a.out)[((int64_t)u.row * a.Hq + r) * D + t] = from_f<InT>(x * inv);
+}
+
 template <typename InT, int D, int R>
 cudaError_t launch_simt(const KvAttn &a, int unit_bound, int rows_max, cudaStream_t st) {
     using P = SimtPlan<InT, D, R>;
@@ -303,8 +360,12 @@ cudaError_t launch_simt_d(const KvAttn &a, int d, int unit_bound, int rows_max, 
 }
 
 template <typename InT, int D>
-cudaError_t launch_join(const KvAttn &a, int unit_bound, cudaStream_t st) {
+cudaError_t launch_join(const KvAttn &a, int unit_bound, int few, cudaStream_t st) {
     const int per_unit = a.tok_stride * a.Hq;
+    if (few) {
+        const cudaError_t e = gdn_launch_pdl(kv_join_few_kernel<InT, D>, dim3((unsigned)unit_bound, (unsigned)per_unit), 256, 0, st, a);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
     const dim3 grid((unsigned)unit_bound, (unsigned)std::min((per_unit + 7) / 8, 64));
     const cudaError_t e = gdn_launch_pdl(kv_join_kernel<InT, D>, grid, 256, 0, st, a);
     return e != cudaSuccess ? e : cudaGetLastError();
@@ -316,10 +377,10 @@ cudaError_t gdn_launch_kv_attn_simt(const gdn::KvAttn &a, int d, int unit_bound,
     return gdn::launch_simt_d<float>(a, d, unit_bound, rows_max, few, st);
 }
 
-cudaError_t gdn_launch_kv_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, cudaStream_t st) {
+cudaError_t gdn_launch_kv_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int few, cudaStream_t st) {
     using namespace gdn;
     using bf = __nv_bfloat16;
-    if (d == 64) return bf16 ? launch_join<bf, 64>(a, unit_bound, st) : launch_join<float, 64>(a, unit_bound, st);
-    if (d == 128) return bf16 ? launch_join<bf, 128>(a, unit_bound, st) : launch_join<float, 128>(a, unit_bound, st);
-    return bf16 ? launch_join<bf, 256>(a, unit_bound, st) : launch_join<float, 256>(a, unit_bound, st);
+    if (d == 64) return bf16 ? launch_join<bf, 64>(a, unit_bound, few, st) : launch_join<float, 64>(a, unit_bound, few, st);
+    if (d == 128) return bf16 ? launch_join<bf, 128>(a, unit_bound, few, st) : launch_join<float, 128>(a, unit_bound, few, st);
+    return bf16 ? launch_join<bf, 256>(a, unit_bound, few, st) : launch_join<float, 256>(a, unit_bound, few, st);
 }
