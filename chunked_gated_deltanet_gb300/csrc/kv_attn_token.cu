@@ -8,10 +8,12 @@
 // CTA (unit, kv head, every Z-th segment), 4 warps, every fourth block each. A warp reads its keys and values from global
 // memory straight into the fragments of the products, without shared memory: the order of the reduction index of a
 // product is free as long as both operands share it, so
-//   S = q K^T     m16n8k16, A = q (rows), B = 8 keys; lane (g, t) = (lane / 4, lane % 4) reads 16 bytes of key 8 a + g at
-//                 columns 64 j + 16 t: four k-steps of four columns each; q's fragments lie in shared memory;
-//   O += P V      A = P in the score fragments' own layout; lane (g, t) reads d / 8 bytes at column g d / 8 of the four keys
-//                 that its weights belong to: byte i of them is n-tile i, so O's column n of n-tile i is n d / 8 + i.
+//   S^T = K q^T    m16n8k16, A = 16 keys, B = 8 rows; lane (g, t) = (lane / 4, lane % 4) reads 16 bytes of keys g and g + 8
+//                  at columns 64 j + 16 t: four k-steps of four columns each; q's fragments lie in shared memory;
+//   O^T += V^T P^T A = V^T, B = P^T: the scores' fragments, transposed 8 x 8 at a time (movmatrix); lane (g, t) reads d / 8
+//                  bytes at column g d / 8 of the four keys that its weights belong to, and bytes 2 i, 2 i + 1 of them are
+//                  m-tile i: rows g and g + 8 of it are columns g d / 8 + 2 i, + 1.
+// With the rows as the narrow side (8 or 16) no accumulator and no product is spent on rows that are not there.
 // Units of UK keys are loaded one ahead, across blocks and segments too. The four warps' results are added in order in shared memory
 // and leave as the segment's partial result (or the result, where there is one segment only).
 // Bound: HBM.
@@ -31,17 +33,24 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], c
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+// The 8 x 8 matrix of 16-bit elements whose row g is lanes 4 g .. 4 g + 3's pairs, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+
 template <int D, int R>
 struct TokenPlan {
     static constexpr int UK = D == 256 ? 16 : 32;   // keys of a unit: 16 or 32 registers of loads each for keys and values
-    static constexpr int NA = UK / 8;               // key n-tiles
+    static constexpr int NA = UK / 16;              // key m-tiles
     static constexpr int J = D / 64;                // 16-byte chunks of a key row per lane
     static constexpr int W = D / 32;                // 32-bit words of a value row per lane
-    static constexpr int NO = D / 8;                // output n-tiles
-    static constexpr int RF = R / 8;                // row halves of a fragment in use
+    static constexpr int NO = D / 8;                // output columns of a lane
+    static constexpr int NT = R / 8;                // row n-tiles
     static constexpr int NU = kKvBlock / UK;        // units of a block
     static constexpr size_t kSo = 0, kMl = kTokenWarps * R * D * sizeof(float), kQf = kMl + kTokenWarps * R * 8,
-                            kQr = kQf + 4 * J * 32 * 2 * RF * 4, kBytes = kQr + R * 8;
+                            kQr = kQf + 4 * J * 32 * 2 * NT * 4, kBytes = kQr + R * 8;
     // CTAs on an SM: as many as the accumulators and loads leave registers for
     static constexpr int kCtas = D * R <= 1024 ? 3 : 2;
 };
@@ -61,11 +70,51 @@ __device__ __forceinline__ void ld_words(uint32_t (&w)[N], const void *p) {
     }
 }
 
+// Scores of 16 N keys -> weights: exponents c s + add (+ lmax for the maximum only), the running maximum and sum (of the
+// lane's keys; added over the lanes at the end), O rescaled.
+template <int N, int NT, int NO>
+__device__ __forceinline__ void token_softmax(float (&s)[N][NT][4], const float (&c)[NT][2], const float (&add)[NT][2], float lmax,
+                                              float ivs, float (&m)[NT][2], float (&l)[NT][2], float (&o)[NO / 2][NT][4]) {
+#pragma unroll
+    for (int f = 0; f < NT; ++f) {
+        float corr[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < N; ++x) top = fmaxf(top, fmaxf(s[x][f][y], s[x][f][2 + y]));
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            if (top > -INFINITY) top = fmaf(top, c[f][y], add[f][y] + lmax);
+            const float mn = fmaxf(m[f][y], top), base = mn == -INFINITY ? 0.f : mn;
+            corr[y] = ex2(m[f][y] - base);
+            m[f][y] = mn;
+            const float off = add[f][y] - base;
+            float sum = 0.f;
+#pragma unroll
+            for (int x = 0; x < N; ++x)
+#pragma unroll
+                for (int k = y; k < 4; k += 2) {
+                    const float p = ex2(fmaf(s[x][f][k], c[f][y], off));
+                    s[x][f][k] = p;
+                    sum += p;
+                }
+            l[f][y] = fmaf(sum, ivs, l[f][y] * corr[y]);
+        }
+        if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+            for (int i = 0; i < NO / 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[i][f][k] *= corr[k & 1];
+        }
+    }
+}
+
 template <int D, int R>
 __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_attn_token_kernel(const KvAttn a) {
     using P = TokenPlan<D, R>;
     using bf = __nv_bfloat16;
-    constexpr int UK = P::UK, NA = P::NA, J = P::J, W = P::W, NO = P::NO, RF = P::RF, NU = P::NU;
+    constexpr int UK = P::UK, NA = P::NA, J = P::J, W = P::W, NO = P::NO, NT = P::NT, NU = P::NU;
     grid_dep_wait();
     grid_dep_launch();
     const int ui = a.unit0 + blockIdx.x, h = blockIdx.y;
@@ -93,18 +142,18 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
         if (lane == 0) atomicOr(a.err, kErrKvBounds);
         return 0;   // in bounds; the result is reported as invalid
     };
-    uint32_t kb[NA][J][4], vb[UK / 16][4][W];
+    uint32_t kb[NA][2][J][4], vb[NA][4][W];
     auto load_k = [&](int page, int n) {
         const int8_t *src = a.c.k + ((int64_t)page * a.Hkv + h) * (kKvBlock * D) + (n * UK + g) * D + 16 * tq;
 #pragma unroll
-        for (int x = 0; x < NA; ++x)
+        for (int x = 0; x < 2 * NA; ++x)
 #pragma unroll
-            for (int j = 0; j < J; ++j) ld_words(kb[x][j], src + 8 * x * D + 64 * j);
+            for (int j = 0; j < J; ++j) ld_words(kb[x / 2][x % 2][j], src + 8 * x * D + 64 * j);
     };
     auto load_v = [&](int page, int n) {
         const int8_t *src = a.c.v + ((int64_t)page * a.Hkv + h) * (kKvBlock * D) + (n * UK + 2 * tq) * D + g * NO;
 #pragma unroll
-        for (int x = 0; x < UK / 16; ++x)
+        for (int x = 0; x < NA; ++x)
 #pragma unroll
             for (int y = 0; y < 4; ++y) ld_words(vb[x][y], src + (16 * x + (y & 1) + 8 * (y >> 1)) * D);
     };
@@ -113,12 +162,12 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
         load_k(page, 0);
         load_v(page, 0);
     }
-    // q's fragments, by warp 0: per k-step the lane's columns 0, 1 and 2, 3 of rows g (and g + 8), scaled rows in fp16
+    // q's fragments, by warp 0: per k-step the lane's columns 0, 1 and 2, 3 of rows g (and g + 8), scaled, in fp16
     const bf *q = static_cast<const bf *>(a.q);
     auto q_row = [&](int r) { return q + ((int64_t)(u.row + r / a.G) * a.Hq + h * a.G + r % a.G) * D + 16 * tq; };
     if (warp == 0) {
 #pragma unroll
-        for (int f = 0; f < RF; ++f) {
+        for (int f = 0; f < NT; ++f) {
             const int r = g + 8 * f;
             uint4 w[J][2];
             float top = 0.f, sum = 0.f, back;
@@ -157,74 +206,24 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
 #pragma unroll
                     for (int k = 0; k < 8; ++k) x[k] *= up;
                     const uint4 y = f8_to_h8(x);
-                    uint32_t *dst = sqf + ((4 * j + 2 * i) * 32 + lane) * 2 * RF + f;
+                    uint32_t *dst = sqf + ((4 * j + 2 * i) * 32 + lane) * 2 * NT + 2 * f;
                     dst[0] = y.x;
-                    dst[RF] = y.y;
-                    dst[64 * RF] = y.z;
-                    dst[64 * RF + RF] = y.w;
+                    dst[1] = y.y;
+                    dst[64 * NT] = y.z;
+                    dst[64 * NT + 1] = y.w;
                 }
         }
     }
     __syncthreads();
-    float2 qr[RF];
+    float2 qr[NT][2];   // of the lane's rows, 8 f + 2 tq + y
 #pragma unroll
-    for (int f = 0; f < RF; ++f) qr[f] = sqr[g + 8 * f];
+    for (int f = 0; f < NT; ++f)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) qr[f][y] = sqr[8 * f + 2 * tq + y];
 
-    float dead[2] = {0.f, 0.f};
-    // One product on fragments whose rows 8..15 may be absent (R = 8): their accumulators stay zero and are shared.
-    auto mma_rows = [&](float *acc, const uint32_t *x, const uint32_t (&b)[2], bool half) {
-        float d4[4] = {acc[0], acc[1], RF == 2 ? acc[2] : dead[0], RF == 2 ? acc[3] : dead[1]};
-        const uint32_t a4[4] = {x[0], RF == 2 ? x[1] : 0u, x[RF], RF == 2 ? x[3] : 0u};
-        if (half) mma_f16(d4, a4, b);
-        else mma_bf16(d4, a4, b);
-        acc[0] = d4[0];
-        acc[1] = d4[1];
-        if (RF == 2) {
-            acc[2] = d4[2];
-            acc[3] = d4[3];
-        }
-    };
-    float o[NO][2 * RF], m[RF], l[RF];
-    // Scores -> weights: exponents c s + add (+ lvs for the maximum only), the running maximum and sum, O rescaled; s holds
-    // the weights after.
-    auto softmax = [&](float (&s)[NA][2 * RF], const float (&c)[RF], const float (&add)[RF], float lmax, float ivs) {
-#pragma unroll
-        for (int f = 0; f < RF; ++f) {
-            float top = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < NA; ++x) top = fmaxf(top, fmaxf(s[x][2 * f], s[x][2 * f + 1]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            if (top > -INFINITY) top = fmaf(top, c[f], add[f] + lmax);
-            const float mn = fmaxf(m[f], top), base = mn == -INFINITY ? 0.f : mn;
-            const float corr = ex2(m[f] - base);
-            m[f] = mn;
-            const float off = add[f] - base;
-            float sum = 0.f;
-#pragma unroll
-            for (int x = 0; x < NA; ++x)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const float p = ex2(fmaf(s[x][2 * f + y], c[f], off));
-                    s[x][2 * f + y] = p;
-                    sum += p;
-                }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            l[f] = fmaf(sum, ivs, l[f] * corr);
-            if (corr != 1.f) {
-#pragma unroll
-                for (int i = 0; i < NO; ++i) {
-                    o[i][2 * f] *= corr;
-                    o[i][2 * f + 1] *= corr;
-                }
-            }
-        }
-    };
-
-    // the rows' own block, at the end of the last segment
+    float o[NO / 2][NT][4], m[NT][2], l[NT][2];   // o: columns g NO + 2 i (+ 1 in [2], [3]) of the lane's two rows
+    // the rows' own block, at the end of the last segment: as it came, 16 keys at a time
     auto own_block = [&] {
-        // the rows' own block as it came: 16 keys at a time
         bool odd_value = false;
         const bf *tail = static_cast<const bf *>(a.c.tail);
         auto raw_row = [&](int kv, int off) -> const bf * {
@@ -234,64 +233,63 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
             return nullptr;
         };
         const float lraw = kv_log2_vscale(a, table, u.block - 1, h, 9);
-        float c[RF], add[RF];
+        float c[NT][2], add[NT][2];
 #pragma unroll
-        for (int f = 0; f < RF; ++f) {
-            c[f] = a.scale_log2;
-            add[f] = 0.f;
-        }
+        for (int f = 0; f < NT; ++f)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                c[f][y] = a.scale_log2;
+                add[f][y] = 0.f;
+            }
         const int n_key = u.first + u.count;
 #pragma unroll 1
         for (int k0 = 0; k0 < n_key; k0 += 16) {
-            float s[NA][2 * RF];
+            float s[1][NT][4];
 #pragma unroll
-            for (int x = 0; x < NA; ++x)
+            for (int f = 0; f < NT; ++f)
 #pragma unroll
-                for (int f = 0; f < 2 * RF; ++f) s[x][f] = x < 2 ? 0.f : -INFINITY;
+                for (int k = 0; k < 4; ++k) s[0][f][k] = 0.f;
             const bf *key[2] = {raw_row(0, k0 + g), raw_row(0, k0 + 8 + g)};
 #pragma unroll 1
             for (int j = 0; j < J; ++j) {
-                uint32_t w[2][8], qw[RF][8];
+                uint32_t w[2][8], qw[NT][8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     w[0][i] = w[1][i] = 0;
 #pragma unroll
-                    for (int f = 0; f < RF; ++f) qw[f][i] = 0;
+                    for (int f = 0; f < NT; ++f) qw[f][i] = 0;
                 }
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                     if (key[x]) ld_words(w[x], key[x] + 64 * j + 16 * tq);
 #pragma unroll
-                for (int f = 0; f < RF; ++f)
+                for (int f = 0; f < NT; ++f)
                     if (g + 8 * f < n_row) ld_words(qw[f], q_row(g + 8 * f) + 64 * j);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    uint32_t qa[2 * RF];
+                    const uint32_t ka[4] = {w[0][2 * k], w[1][2 * k], w[0][2 * k + 1], w[1][2 * k + 1]};
 #pragma unroll
-                    for (int f = 0; f < RF; ++f) {
-                        qa[f] = qw[f][2 * k];
-                        qa[RF + f] = qw[f][2 * k + 1];
-                    }
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t b[2] = {w[x][2 * k], w[x][2 * k + 1]};
-                        mma_rows(s[x], qa, b, false);
+                    for (int f = 0; f < NT; ++f) {
+                        const uint32_t b[2] = {qw[f][2 * k], qw[f][2 * k + 1]};
+                        mma_bf16(s[0][f], ka, b);
                     }
                 }
             }
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int f = 0; f < NT; ++f)
 #pragma unroll
-                for (int f = 0; f < RF; ++f)
+                for (int k = 0; k < 4; ++k)
+                    if (k0 + g + 8 * (k >> 1) > u.first + (8 * f + 2 * tq + (k & 1)) / a.G) s[0][f][k] = -INFINITY;
+            token_softmax<1, NT, NO>(s, c, add, lraw, 1.f, m, l, o);
+            uint32_t ph[NT][2], pl[NT][2];   // weights of keys g and g + 8, rows 2 tq, 2 tq + 1; transposed
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        if (k0 + 8 * x + 2 * tq + y > u.first + (g + 8 * f) / a.G) s[x][2 * f + y] = -INFINITY;
-            softmax(s, c, add, lraw, 1.f);
-            uint32_t ph[2 * RF], pl[2 * RF];
+            for (int f = 0; f < NT; ++f)
 #pragma unroll
-            for (int f = 0; f < RF; ++f)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) split_bf16x2(s[x][2 * f], s[x][2 * f + 1], ph[x * RF + f], pl[x * RF + f]);
+                for (int x = 0; x < 2; ++x) {
+                    split_bf16x2(s[0][f][2 * x], s[0][f][2 * x + 1], ph[f][x], pl[f][x]);
+                    ph[f][x] = transpose8(ph[f][x]);
+                    pl[f][x] = transpose8(pl[f][x]);
+                }
             const bf *val[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) val[y] = raw_row(1, k0 + 2 * tq + (y & 1) + 8 * (y >> 1));
@@ -308,47 +306,54 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                     v[y][0] = x.x; v[y][1] = x.y; v[y][2] = x.z; v[y][3] = x.w;
                 }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t sel = k & 1 ? 0x7632 : 0x5410;
-                    const uint32_t b[2] = {__byte_perm(v[0][k / 2], v[1][k / 2], sel), __byte_perm(v[2][k / 2], v[3][k / 2], sel)};
-                    mma_rows(o[8 * i + k], ph, b, false);
-                    mma_rows(o[8 * i + k], pl, b, false);
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t va[4] = {__byte_perm(v[0][k], v[1][k], 0x5410), __byte_perm(v[0][k], v[1][k], 0x7632),
+                                            __byte_perm(v[2][k], v[3][k], 0x5410), __byte_perm(v[2][k], v[3][k], 0x7632)};
+#pragma unroll
+                    for (int f = 0; f < NT; ++f) {
+                        mma_bf16(o[4 * i + k][f], va, ph[f]);
+                        mma_bf16(o[4 * i + k][f], va, pl[f]);
+                    }
                 }
             }
         }
         if (__any_sync(0xffffffffu, odd_value)) {
 #pragma unroll
-            for (int f = 0; f < RF; ++f) {
-                const int r = g + 8 * f, n_see = r < n_row ? u.first + r / a.G + 1 : 0;
+            for (int f = 0; f < NT; ++f)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int r = 8 * f + 2 * tq + y, n_see = r < n_row ? u.first + r / a.G + 1 : 0;
 #pragma unroll 1
-                for (int k = 0; k < n_see; ++k) {
-                    const bf *src = raw_row(1, k) + 2 * tq * NO;
+                    for (int k = 0; k < n_see; ++k) {
+                        const bf *src = raw_row(1, k) + g * NO;
 #pragma unroll
-                    for (int i = 0; i < NO; ++i)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const float x = to_f(src[y * NO + i]);
-                            if (!(fabsf(x) <= 3.4e38f)) o[i][2 * f + y] += x;
+                        for (int i = 0; i < NO; ++i) {
+                            const float x = to_f(src[i]);
+                            if (!(fabsf(x) <= 3.4e38f)) o[i / 2][f][2 * (i & 1) + y] += x;
                         }
+                    }
                 }
-            }
         }
     };
+    // the warps' results of a segment, added in order (a warp without a block of it has none)
     auto merge = [&](int seg) {
-        // the warps' results, added in order (those of blocks past the rows' own hold no key)
         const int n_warp = min(kTokenWarps, u.block - seg * a.seg_blocks + 1);
         if (warp < n_warp) {
 #pragma unroll
-            for (int f = 0; f < RF; ++f) {
-                float *dst = so + (warp * R + g + 8 * f) * D + 2 * tq * NO;
+            for (int f = 0; f < NT; ++f)
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                for (int y = 0; y < 2; ++y) {
+                    const int r = 8 * f + 2 * tq + y;
+                    float *dst = so + (warp * R + r) * D + g * NO;
 #pragma unroll
-                    for (int i = 0; i < NO; i += 4)
-                        *reinterpret_cast<float4 *>(dst + y * NO + i) =
-                            make_float4(o[i][2 * f + y], o[i + 1][2 * f + y], o[i + 2][2 * f + y], o[i + 3][2 * f + y]);
-                if (tq == 0) sml[warp * R + g + 8 * f] = make_float2(m[f], l[f]);
-            }
+                    for (int i = 0; i < NO / 2; i += 2)
+                        *reinterpret_cast<float4 *>(dst + 2 * i) =
+                            make_float4(o[i][f][y], o[i][f][2 + y], o[i + 1][f][y], o[i + 1][f][2 + y]);
+                    float sum = l[f][y];
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+                    if (g == 0) sml[warp * R + r] = make_float2(m[f][y], sum);
+                }
         }
         __syncthreads();
         for (int e = t; e < n_row * (D / 4); e += 32 * kTokenWarps) {
@@ -380,15 +385,16 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
         }
         __syncthreads();   // read before the next segment's results
     };
+
     for (int seg = blockIdx.z;;) {
 #pragma unroll
-        for (int i = 0; i < NO; ++i)
+        for (int f = 0; f < NT; ++f) {
+            m[f][0] = m[f][1] = -INFINITY;
+            l[f][0] = l[f][1] = 0.f;
 #pragma unroll
-            for (int f = 0; f < 2 * RF; ++f) o[i][f] = 0.f;
+            for (int i = 0; i < NO / 2; ++i)
 #pragma unroll
-        for (int f = 0; f < RF; ++f) {
-            m[f] = -INFINITY;
-            l[f] = 0.f;
+                for (int k = 0; k < 4; ++k) o[i][f][k] = 0.f;
         }
         const int seg_end = (seg + 1) * a.seg_blocks, next_seg = seg + gridDim.z;
 #pragma unroll 1
@@ -397,50 +403,52 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
             const int64_t ph = (int64_t)page * a.Hkv + h;
             const float ks = a.scale_log2 * a.c.k_scale[ph], vs = a.c.v_scale[ph];
             const float lvs = vs != 0.f ? log2f(vs) : kv_log2_vscale(a, table, blk - 1, h, 8), ivs = ex2(-lvs);
-            float c[RF], add[RF];
+            float c[NT][2], add[NT][2];
 #pragma unroll
-            for (int f = 0; f < RF; ++f) {
-                c[f] = ks * qr[f].x;
-                add[f] = lvs - c[f] * qr[f].y;
-            }
+            for (int f = 0; f < NT; ++f)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    c[f][y] = ks * qr[f][y].x;
+                    add[f][y] = lvs - c[f][y] * qr[f][y].y;
+                }
 #pragma unroll 1
             for (int n = 0; n < NU; ++n) {
-                float s[NA][2 * RF];
+                float s[NA][NT][4];
 #pragma unroll
                 for (int x = 0; x < NA; ++x)
 #pragma unroll
-                    for (int f = 0; f < 2 * RF; ++f) s[x][f] = 0.f;
+                    for (int f = 0; f < NT; ++f)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) s[x][f][k] = 0.f;
 #pragma unroll
                 for (int j = 0; j < J; ++j)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        uint32_t qa[2 * RF];
-                        const uint32_t *src = sqf + ((4 * j + k) * 32 + lane) * 2 * RF;
-                        if (RF == 2) {
-                            const uint4 y = *reinterpret_cast<const uint4 *>(src);
-                            qa[0] = y.x; qa[1] = y.y; qa[2 * RF - 2] = y.z; qa[2 * RF - 1] = y.w;
-                        } else {
-                            const uint2 y = *reinterpret_cast<const uint2 *>(src);
-                            qa[0] = y.x; qa[1] = y.y;
+                        uint32_t b[NT][2];
+                        const uint32_t *src = sqf + ((4 * j + k) * 32 + lane) * 2 * NT;
+#pragma unroll
+                        for (int f = 0; f < NT; ++f) {
+                            b[f][0] = src[2 * f];
+                            b[f][1] = src[2 * f + 1];
                         }
 #pragma unroll
                         for (int x = 0; x < NA; ++x) {
-                            const uint2 b2 = i8_to_f16x4<false>(kb[x][j][k]);
-                            const uint32_t b[2] = {b2.x, b2.y};
-                            mma_rows(s[x], qa, b, true);
+                            const uint2 lo = i8_to_f16x4<false>(kb[x][0][j][k]), hi = i8_to_f16x4<false>(kb[x][1][j][k]);
+                            const uint32_t ka[4] = {lo.x, hi.x, lo.y, hi.y};
+#pragma unroll
+                            for (int f = 0; f < NT; ++f) mma_f16(s[x][f], ka, b[f]);
                         }
                     }
                 const int pn = n + 1 < NU ? page : next;
                 if (pn >= 0) load_k(pn, (n + 1) % NU);
-                softmax(s, c, add, 0.f, ivs);
+                token_softmax<NA, NT, NO>(s, c, add, 0.f, ivs, m, l, o);
 #pragma unroll
-                for (int x = 0; x < UK / 16; ++x) {
-                    uint32_t pa[2 * RF];   // rows g (g + 8) of the first and of the second 8 keys
+                for (int x = 0; x < NA; ++x) {
+                    uint32_t pb[NT][2];
 #pragma unroll
-                    for (int f = 0; f < RF; ++f) {
-                        pa[f] = f2_to_h2(s[2 * x][2 * f], s[2 * x][2 * f + 1]);
-                        pa[RF + f] = f2_to_h2(s[2 * x + 1][2 * f], s[2 * x + 1][2 * f + 1]);
-                    }
+                    for (int f = 0; f < NT; ++f)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) pb[f][y] = transpose8(f2_to_h2(s[x][f][2 * y], s[x][f][2 * y + 1]));
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
                         const uint32_t off = 0x64806480u;
@@ -458,9 +466,10 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                             }
                         }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t b[2] = {e[0][i], e[1][i]};
-                            mma_rows(o[4 * w + i], pa, b, true);
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t va[4] = {e[0][2 * i], e[0][2 * i + 1], e[1][2 * i], e[1][2 * i + 1]};
+#pragma unroll
+                            for (int f = 0; f < NT; ++f) mma_f16(o[2 * w + i][f], va, pb[f]);
                         }
                     }
                 }
