@@ -258,3 +258,35 @@ def test_wait_timeout_is_reported_and_context_survives(cuda_device, d):
     assert status == gdn.GDN_ERR_TIMEOUT
     assert gdn.gdn_device_status() == gdn.GDN_OK
     m.step([1], [200])
+
+
+def test_many_sessions_share_the_gpu(cuda_device):
+    """So many (session, head) chains of tokens that a CTA takes several segments of one: the bits of a few sessions alone."""
+    n, heads, d = 40, (64, 64), 64
+    m, one = (Model(heads, d, BF, n_pages=40 * 75, n_slots=n, max_blocks=80, seed=2) for _ in range(2))
+    lens = [4700 if i % 3 == 0 else 64 * i + 5 for i in range(n)]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    mk = lambda k, h: torch.randn((k, h, d), generator=g, device="cuda").to(torch.bfloat16)   # noqa: E731
+
+    def run(model, slots, new, q, k, v, max_len):
+        plan = gdn.KvPlan.new(sum(new), len(slots))
+        gdn.gdn_kv_plan(model.desc, model.cache, model.i32(slots), model.i32(new), plan)
+        gdn.gdn_kv_append(model.desc, model.cache, plan, k, v)
+        out = torch.full((sum(new), heads[0], d), 7.0, dtype=torch.bfloat16, device="cuda")
+        if q is not None:
+            ws = gdn.kv_attention_workspace(model.desc, sum(new), len(slots), max_len)
+            gdn.gdn_kv_attention(model.desc, model.cache, plan, q, k, v, out, ws, max(new), max_len)
+        assert gdn.gdn_kv_status(plan) == gdn.GDN_OK and gdn.gdn_device_status() == gdn.GDN_OK
+        return out
+
+    k, v = mk(sum(lens), 64), mk(sum(lens), 64)
+    run(m, list(range(n)), lens, None, k, v, 5000)
+    row = 0
+    for i in (0, 1, 39):
+        row = sum(lens[:i])
+        run(one, [i], [lens[i]], None, k[row:row + lens[i]].contiguous(), v[row:row + lens[i]].contiguous(), 5000)
+    q, k, v = mk(n, 64), mk(n, 64), mk(n, 64)
+    out = run(m, list(range(n)), [1] * n, q, k, v, 5000)
+    assert torch.isfinite(out).all()
+    for i in (0, 1, 39):
+        assert torch.equal(run(one, [i], [1], *(t[i:i + 1].contiguous() for t in (q, k, v)), 5000)[0], out[i])
