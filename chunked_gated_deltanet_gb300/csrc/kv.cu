@@ -3,7 +3,6 @@
 #include "kv.cuh"
 
 #include <algorithm>
-#include <cfloat>
 
 namespace gdn {
 
@@ -56,8 +55,10 @@ struct PlanReq {
 // requests' new tokens, one unit per touched block, one page popped from the free stack per block that completes.
 // Sums go in request order, so pages are handed out in unit order. A batch that does not fit (pages, table, unit
 // map, a bad slot or count) leaves the cache as it was, with no unit and the reason in counts[1].
-// Bound: latency (about 1 KB in and out per 16 requests); one CTA keeps the free stack's update in place and
-// race-free without a second launch.
+// Bound: latency (about 1 KB in and out per 16 requests). One CTA, or a cluster of kPlanCluster where the map has room for
+// more units than a CTA has threads: every CTA sums over the requests by itself and expands its share of the units, and the
+// cluster's barrier stands between the last read of the cache's state and its update in place.
+constexpr int kPlanCluster = 8;
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvCache c, const int32_t *slots, const int32_t *n_new,
                                                                 int n, int32_t *rows, int32_t *units, int32_t *counts,
                                                                 int max_units, int32_t *state_out, int32_t *n_free_out) {
@@ -107,29 +108,33 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvCache c, 
         if (total.pages > n_free || n_free > c.n_pages) atomicOr(&bad_all, 1u);
         if (total.units > max_units || total.rows > INT32_MAX) atomicOr(&bad_all, 4u);
     }
-    __syncthreads();   // every read of the state and of the free stack's height is done
+    __syncthreads();   // every read of the state and of the free stack's height is done, in the cluster's CTAs too
+    if (gridDim.x > 1) {
+        asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+    }
     const unsigned status = bad_all;
+    const bool first = blockIdx.x == 0;   // writes what there is once
 #pragma unroll
     for (int j = 0; j < kPlanPer; ++j) {
         const int i = t * per + j;
         if (j < per && i < n) {
             if (status == 0) {
-                rows[i] = (int)at.rows;
+                if (first) rows[i] = (int)at.rows;
                 const int end = ctx[j] + cnt[j];
                 const int fb = ctx[j] / kKvBlock, eb = end / kKvBlock;
                 req[i] = {ctx[j], cnt[j], slot[j], buf[j], at.units, at.pages, (int)at.rows, 0};
                 // the open block moves to the other tail buffer when it is a new block, so that the rows of the
                 // block that closes in this call stay readable after its append
-                reinterpret_cast<int2 *>(state_out)[slot[j]] = make_int2(end, eb != fb ? buf[j] ^ 1 : buf[j]);
+                if (first) reinterpret_cast<int2 *>(state_out)[slot[j]] = make_int2(end, eb != fb ? buf[j] ^ 1 : buf[j]);
                 at.rows += cnt[j];
                 if (cnt[j] > 0) at.units += (end + kKvBlock - 1) / kKvBlock - fb;
                 at.pages += eb - fb;
-            } else {
+            } else if (first) {
                 rows[i] = 0;
             }
         }
     }
-    if (t == 0) {
+    if (t == 0 && first) {
         rows[n] = status == 0 ? (int)total.rows : 0;
         counts[0] = status == 0 ? total.units : 0;
         counts[1] = (int)status;
@@ -138,7 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvCache c, 
     if (status != 0) return;
     __syncthreads();
     // one thread per unit; its request is the last one whose first unit is not after it
-    for (int u = t; u < total.units; u += kPlanThreads) {
+    for (int u = blockIdx.x * kPlanThreads + t; u < total.units; u += gridDim.x * kPlanThreads) {
         int lo = 0, hi = n - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -165,27 +170,32 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvCache c, 
 
 // ---- append ----
 
-// x / scale rounded to nearest even, as an IEEE division and rint would give: the product with the reciprocal is
-// within 1e-4 of the quotient for |x / scale| <= 127, so only quotients that near a tie need the division.
-__device__ __forceinline__ int kv_quant(float x, float scale, float inv) {
-    float y = x * inv;
-    float q = rintf(y);
-    if (!(fabsf(fabsf(y - q) - 0.5f) > 1e-3f)) {
-        y = x / scale;
-        q = rintf(y);
-    }
+// x / scale rounded to nearest even as an IEEE division and rint give it, saturated, a NaN 0: every value of a block with
+// values that are not finite, and the values of a vector whose quotient is near a tie.
+__device__ __forceinline__ int kv_quant(float x, float scale) {
+    const float q = rintf(x / scale);
     return q == q ? (int)fminf(fmaxf(q, -127.f), 127.f) : 0;   // 0 / 0 of an all-zero block, or a NaN: 0
 }
 
 template <typename T> struct Vec16;   // 16 bytes of T as floats
 template <> struct Vec16<float> {
     static constexpr int N = 4;
+    static constexpr uint32_t kInf = 0x7F800000u;
     static __device__ __forceinline__ void get(const uint4 &u, float (&f)[4]) {
         f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
     }
+    // largest magnitude as bits (order-preserving for magnitudes; infinities and NaNs on top)
+    static __device__ __forceinline__ uint32_t top(uint32_t m, const uint4 &u) {
+        m = max(m, u.x & 0x7FFFFFFFu);
+        m = max(m, u.y & 0x7FFFFFFFu);
+        m = max(m, u.z & 0x7FFFFFFFu);
+        return max(m, u.w & 0x7FFFFFFFu);
+    }
+    static __device__ __forceinline__ uint32_t bits(uint32_t m) { return m; }
 };
 template <> struct Vec16<__nv_bfloat16> {
     static constexpr int N = 8;
+    static constexpr uint32_t kInf = 0x7F800000u;
     static __device__ __forceinline__ void get(const uint4 &u, float (&f)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -194,6 +204,13 @@ template <> struct Vec16<__nv_bfloat16> {
             f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
+    static __device__ __forceinline__ uint32_t top(uint32_t m, const uint4 &u) {   // two 16-bit magnitudes
+        m = __vmaxu2(m, u.x & 0x7FFF7FFFu);
+        m = __vmaxu2(m, u.y & 0x7FFF7FFFu);
+        m = __vmaxu2(m, u.z & 0x7FFF7FFFu);
+        return __vmaxu2(m, u.w & 0x7FFF7FFFu);
+    }
+    static __device__ __forceinline__ uint32_t bits(uint32_t m) { return max(m << 16, m & 0xFFFF0000u); }
 };
 
 // CTA (unit, kv head, k or v). A block that closes: its 64 rows (tail rows before `first`, then new ones) go through
@@ -206,7 +223,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvCache c, const i
     grid_dep_launch();
     if ((int)blockIdx.x >= counts[0]) return;
     constexpr int VN = Vec16<InT>::N, VPR = D / VN, NV = kKvBlock * VPR / 256;   // vectors per row, per thread
-    __shared__ float red[8];
+    __shared__ uint32_t red[8];
     const KvUnit u = kv_load_unit(units, blockIdx.x);
     if (!kv_unit_ok(u, c, n_rows)) {
         if (threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) atomicOr(err, kErrKvBounds);
@@ -235,39 +252,61 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvCache c, const i
         }
         return;
     }
-    float m = 0.f;
+    uint32_t mb = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float f[VN];
-        Vec16<InT>::get(w[i], f);
-#pragma unroll
-        for (int j = 0; j < VN; ++j) {
-            const float a = fabsf(f[j]);
-            m = fmaxf(m, a <= FLT_MAX ? a : 0.f);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((t & 31) == 0) red[t >> 5] = m;
+    for (int i = 0; i < NV; ++i) mb = Vec16<InT>::top(mb, w[i]);
+    mb = __reduce_max_sync(0xffffffffu, Vec16<InT>::bits(mb));
+    if ((t & 31) == 0) red[t >> 5] = mb;
     __syncthreads();
-    m = red[0];
+    mb = red[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i]);
-    const float scale = m / 127.f, inv = 1.f / scale;
+    for (int i = 1; i < 8; ++i) mb = max(mb, red[i]);
+    const bool finite = mb < Vec16<InT>::kInf;
+    if (!finite) {   // the scale comes from the finite values
+        mb = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[VN];
+            Vec16<InT>::get(w[i], f);
+#pragma unroll
+            for (int j = 0; j < VN; ++j) {
+                const uint32_t b = __float_as_uint(f[j]) & 0x7FFFFFFFu;
+                if (b < Vec16<InT>::kInf) mb = max(mb, b);
+            }
+        }
+        mb = __reduce_max_sync(0xffffffffu, mb);
+        __syncthreads();
+        if ((t & 31) == 0) red[t >> 5] = mb;
+        __syncthreads();
+        mb = red[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) mb = max(mb, red[i]);
+    }
+    const float scale = __uint_as_float(mb) / 127.f, inv = 1.f / scale;
     const int64_t ph = (int64_t)u.page * Hkv + h;
     int8_t *page = (kv ? c.v : c.k) + ph * kKvBlock * D;
     if (t == 0) (kv ? c.v_scale : c.k_scale)[ph] = scale;
+    // The quotient as the product with the reciprocal, off by less than 1e-4 for |x / scale| <= 127, rounded by adding and
+    // taking away 1.5 * 2^23, whose sum holds the integer in its low bits. Where that is near a tie the vector is divided.
+    const float magic = 12582912.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        float f[VN];
+        float f[VN], d = 0.f;
+        uint32_t q[VN], b[VN / 4];
         Vec16<InT>::get(w[i], f);
-        uint32_t b[VN / 4];
 #pragma unroll
-        for (int j = 0; j < VN / 4; ++j) {
-            b[j] = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) b[j] |= (uint32_t)(kv_quant(f[4 * j + k], scale, inv) & 0xff) << (8 * k);
+        for (int j = 0; j < VN; ++j) {
+            const float y = f[j] * inv, z = y + magic;
+            d = fmaxf(d, fabsf(y - (z - magic)));
+            q[j] = __float_as_uint(z);
         }
+        if (!finite || !(d < 0.499f) || !(inv <= 3.4e38f)) {   // also a scale without a finite reciprocal
+#pragma unroll
+            for (int j = 0; j < VN; ++j) q[j] = (uint32_t)kv_quant(f[j], scale);
+        }
+#pragma unroll
+        for (int j = 0; j < VN / 4; ++j)
+            b[j] = __byte_perm(__byte_perm(q[4 * j], q[4 * j + 1], 0x0040), __byte_perm(q[4 * j + 2], q[4 * j + 3], 0x0040), 0x5410);
         const int e = t + 256 * i, r = e / VPR, col = (e % VPR) * VN;
         if (VN == 8) *reinterpret_cast<uint2 *>(page + r * D + col) = make_uint2(b[0], b[VN / 4 - 1]);
         else *reinterpret_cast<uint32_t *>(page + r * D + col) = b[0];
@@ -374,8 +413,20 @@ cudaError_t gdn_launch_kv_plan(const gdn::KvCache &c, const int32_t *slots, cons
                                  (int)(kKvMaxRequests * sizeof(PlanReq)));
         if (e != cudaSuccess) return e;
     }
-    e = gdn_launch_pdl(kv_plan_kernel, 1, kPlanThreads, smem, st, c, slots, n_new, n, rows, units, counts, max_units,
-                       state_out, n_free_out);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(max_units > kPlanThreads ? kPlanCluster : 1);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cfg.gridDim.x;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kv_plan_kernel, c, slots, n_new, n, rows, units, counts, max_units, state_out, n_free_out);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -63,15 +63,15 @@ gdn::KvCache device_cache(const gdn_kv_cache *c) {
 // Units of a batch: a request of n tokens touches at most (n + 62) / 64 + 1 blocks, and at most n.
 int64_t max_units(int64_t tokens, int32_t requests) { return std::min<int64_t>(tokens, tokens / kKvBlock + 2LL * requests); }
 
-// Key segments of a row's attention, cut at absolute positions. Few rows: 512 keys for one or two key/value heads, so that
-// one token's long context fills the GPU, up to 4,096 for more heads, which fill it with longer segments (a rule on the
-// heads alone: a row's segments do not depend on the batch); fp32, which computes more per key, 512. Many rows: 4,096 keys, where the partial results are a small
-// share of the work.
-int seg_blocks_few(const gdn_attn_desc *d) {
-    if (d->in_dtype == GDN_FP32 || d->n_kv_heads < 4) return 8;
-    return d->n_kv_heads < 8 ? 16 : d->n_kv_heads < 16 ? 32 : 64;
+// Key segments of a row's attention, in blocks, cut at absolute positions. Few rows: 512 keys for up to three key/value
+// heads, so that one token's long context fills the GPU, up to 4,096 for more heads, which fill it with longer ones. Many
+// rows: 4,096 keys, where the partial results are a small share of the work; in fp32 512, where 64 rows of one head take
+// about 3 us a block. A rule on the description alone: a row's segments do not depend on the batch.
+int seg_blocks(const gdn_attn_desc *d, bool few) {
+    if (d->in_dtype == GDN_FP32) return 8;
+    if (!few || d->n_kv_heads >= 16) return 64;
+    return d->n_kv_heads < 4 ? 8 : d->n_kv_heads < 8 ? 16 : 32;
 }
-constexpr int kSegBlocksMany = 64;
 constexpr int kFewRows = 16;   // rows (new tokens of a block x query heads per key/value head) of the few-row form
 
 struct Form {
@@ -86,7 +86,7 @@ Form form_of(const gdn_attn_desc *d, int64_t max_new, int64_t max_len) {
     f.tok_stride = (int)std::min<int64_t>(max_new, kKvBlock);
     f.rows_max = f.tok_stride * G;
     f.few = max_new * G <= kFewRows;
-    f.seg_blocks = f.few ? seg_blocks_few(d) : kSegBlocksMany;
+    f.seg_blocks = seg_blocks(d, f.few);
     const int64_t blocks = std::max<int64_t>((max_len + kKvBlock - 1) / kKvBlock, 1);
     f.n_seg = (blocks + f.seg_blocks - 1) / f.seg_blocks;
     f.unit_bytes = f.n_seg == 1 ? 0 : (size_t)f.n_seg * f.tok_stride * d->n_q_heads * (d->head_dim * sizeof(float) + sizeof(float2));

@@ -13,6 +13,26 @@
 
 namespace gdn {
 
+// 16 int8 as floats: a byte b ^ 0x80 under 0x4B0000 reads 2^23 + 128 + b.
+__device__ __forceinline__ void i8_to_f(const uint4 &u, float (&f)[16]) {
+    const uint32_t w[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[4 * i] = __uint_as_float(__byte_perm(w[i], 0x4B000000u, 0x7440)) - 8388736.f;
+        f[4 * i + 1] = __uint_as_float(__byte_perm(w[i], 0x4B000000u, 0x7441)) - 8388736.f;
+        f[4 * i + 2] = __uint_as_float(__byte_perm(w[i], 0x4B000000u, 0x7442)) - 8388736.f;
+        f[4 * i + 3] = __uint_as_float(__byte_perm(w[i], 0x4B000000u, 0x7443)) - 8388736.f;
+    }
+}
+// 16 floats of a row that may not be there
+__device__ __forceinline__ void ld_own16(const float *row, int col, float (&f)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        const float4 x = row ? *reinterpret_cast<const float4 *>(row + col + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        f[i] = x.x; f[i + 1] = x.y; f[i + 2] = x.z; f[i + 3] = x.w;
+    }
+}
+
 template <typename T> __device__ __forceinline__ T from_f(float x);
 template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
@@ -23,47 +43,42 @@ __device__ __forceinline__ void load_page(float *dst, const int8_t *src) {
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
         const int e = threadIdx.x + 256 * i, r = e / (D / 16), c = (e % (D / 16)) * 16;
-        const uint4 w = *reinterpret_cast<const uint4 *>(src + r * D + c);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        float f[16];
+        i8_to_f(*reinterpret_cast<const uint4 *>(src + r * D + c), f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float4 f;
-            f.x = (float)(int8_t)(x[j] & 0xff);
-            f.y = (float)(int8_t)((x[j] >> 8) & 0xff);
-            f.z = (float)(int8_t)((x[j] >> 16) & 0xff);
-            f.w = (float)(int8_t)(x[j] >> 24);
-            *reinterpret_cast<float4 *>(dst + r * LD + c + 4 * j) = f;
-        }
+        for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4 *>(dst + r * LD + c + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
     }
 }
 
-// The open block's rows as they came: offsets below u.first from the tail, the unit's own from the new rows, none after.
-template <typename InT, int D, int LD>
-__device__ __forceinline__ void load_raw(float *dst, const KvUnit &u, const InT *tail, const InT *x, int Hkv, int h) {
+// Row `off` of the rows' own block as it came: below u.first from the tail, the unit's own from the new rows, none after.
+__device__ __forceinline__ const float *own_row(const KvAttn &a, const KvUnit &u, int kv, int h, int off, int D) {
+    if (off < u.first) return static_cast<const float *>(a.c.tail) + kv_tail_offset(u.slot, u.src, kv, h, a.Hkv, D) + (int64_t)off * D;
+    if (off < u.first + u.count)
+        return static_cast<const float *>(kv ? a.v_new : a.k_new) + ((int64_t)(u.row + off - u.first) * a.Hkv + h) * D;
+    return nullptr;
+}
+
+template <int D, int LD>
+__device__ __forceinline__ void load_own(float *dst, const KvAttn &a, const KvUnit &u, int kv, int h) {
     for (int e = threadIdx.x; e < kKvBlock * D / 4; e += 256) {
-        const int r = e / (D / 4), c = (e % (D / 4)) * 4, o = r - u.first;
-        const InT *s = o < 0 ? tail + r * D + c : (o < u.count ? x + ((int64_t)(u.row + o) * Hkv + h) * D + c : nullptr);
-        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (s) f = make_float4(to_f(s[0]), to_f(s[1]), to_f(s[2]), to_f(s[3]));
-        *reinterpret_cast<float4 *>(dst + r * LD + c) = f;
+        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+        const float *s = own_row(a, u, kv, h, r, D);
+        *reinterpret_cast<float4 *>(dst + r * LD + c) = s ? *reinterpret_cast<const float4 *>(s + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
-// CTA (unit x row tile, kv head, segment), 256 threads, R rows. R = 64: thread (ty, tx) holds 4 rows, 4 keys of the
-// scores and D / 16 columns of the output. R = 8 (few rows): a warp per row, 2 keys and D / 32 columns per lane.
-template <typename InT, int D, int R>
+// Many rows: CTA (unit x tile of 64 rows, kv head, segment), 256 threads; thread (ty, tx) holds 4 rows, 4 keys of the scores
+// and D / 16 columns of the output. Bound: fp32 FMA issue and the shared-memory reads beside it (a 64 x 64 x d step).
+template <int D>
 struct SimtPlan {
-    static constexpr int LD = D + 4, PLD = kKvBlock + 4;   // 16-byte rows that start 4 banks apart
+    static constexpr int R = 64, LD = D + 4, PLD = kKvBlock + 4;   // 16-byte rows that start 4 banks apart
     static constexpr size_t kBytes = (size_t)(R * LD + kKvBlock * LD + R * PLD) * sizeof(float);
-    static constexpr int RT = R == 64 ? 4 : 1;             // rows per thread
-    static constexpr int KT = R == 64 ? 4 : 2;             // keys per thread
-    static constexpr int CT = R == 64 ? D / 16 : D / 32;   // output columns per thread
 };
 
-template <typename InT, int D, int R>
+template <int D>
 __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int row_tiles) {
-    using P = SimtPlan<InT, D, R>;
-    constexpr int LD = P::LD, PLD = P::PLD, RT = P::RT, KT = P::KT, CT = P::CT;
+    using P = SimtPlan<D>;
+    constexpr int R = P::R, LD = P::LD, PLD = P::PLD, CT = D / 16;
     grid_dep_wait();
     grid_dep_launch();
     const int ui = a.unit0 + blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles, h = blockIdx.y, seg = blockIdx.z;
@@ -79,32 +94,27 @@ __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int r
 
     extern __shared__ __align__(16) unsigned char simt_smem[];
     float *Q = reinterpret_cast<float *>(simt_smem), *KV = Q + R * LD, *Pm = KV + kKvBlock * LD;
-    const int t = threadIdx.x;
-    const InT *q = static_cast<const InT *>(a.q);
+    const int t = threadIdx.x, ty = t >> 4, tx = t & 15;
+    const float *q = static_cast<const float *>(a.q);
     for (int e = t; e < R * D / 4; e += 256) {
         const int r = e / (D / 4), c = (e % (D / 4)) * 4;
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r0 + r < n_row) {
-            const InT *s = q + ((int64_t)(u.row + (r0 + r) / a.G) * a.Hq + h * a.G + (r0 + r) % a.G) * D + c;
-            f = make_float4(to_f(s[0]), to_f(s[1]), to_f(s[2]), to_f(s[3]));
-        }
+        if (r0 + r < n_row)
+            f = *reinterpret_cast<const float4 *>(q + ((int64_t)(u.row + (r0 + r) / a.G) * a.Hq + h * a.G + (r0 + r) % a.G) * D + c);
         *reinterpret_cast<float4 *>(Q + r * LD + c) = f;
     }
-    const int ty = R == 64 ? t >> 4 : t >> 5, tx = R == 64 ? t & 15 : t & 31;
-    constexpr int TX = R == 64 ? 16 : 32;
-    float o[RT][CT], m[RT], l[RT];
-    int limit[RT];   // the last offset of its own block that a row sees
+    float o[4][CT], m[4], l[4];
+    int limit[4];   // the last offset of its own block that a row sees
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
+    for (int i = 0; i < 4; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
-        limit[i] = u.first + (r0 + ty * RT + i) / a.G;
+        limit[i] = u.first + (r0 + ty * 4 + i) / a.G;
 #pragma unroll
         for (int j = 0; j < CT; ++j) o[i][j] = 0.f;
     }
     const int b0 = seg * a.seg_blocks, b1 = min(u.block, b0 + a.seg_blocks);
     const int n_blk = b1 - b0 + (seg == last_seg ? 1 : 0);
-    const int64_t Hkv = a.Hkv;
     for (int i = 0; i < n_blk; ++i) {
         const bool raw = b0 + i == u.block;
         int64_t ph = 0;
@@ -115,31 +125,30 @@ __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int r
                 if (t == 0) atomicOr(a.err, kErrKvBounds);
                 continue;   // the same page number in every thread
             }
-            ph = (int64_t)page * Hkv + h;
+            ph = (int64_t)page * a.Hkv + h;
             ks = a.c.k_scale[ph];
             vs = a.c.v_scale[ph];
         }
-        const InT *tail = static_cast<const InT *>(a.c.tail) + kv_tail_offset(u.slot, u.src, 0, h, a.Hkv, D);
         __syncthreads();   // the block before is done with KV and Pm (the first time: Q is written)
-        if (raw) load_raw<InT, D, LD>(KV, u, tail, static_cast<const InT *>(a.k_new), a.Hkv, h);
+        if (raw) load_own<D, LD>(KV, a, u, 0, h);
         else load_page<D, LD>(KV, a.c.k + ph * kKvBlock * D);
         __syncthreads();
-        float s[RT][KT];
+        float s[4][4];
 #pragma unroll
-        for (int x = 0; x < RT; ++x)
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int y = 0; y < KT; ++y) s[x][y] = 0.f;
+            for (int y = 0; y < 4; ++y) s[x][y] = 0.f;
 #pragma unroll 4
         for (int c = 0; c < D; c += 4) {
-            float4 qf[RT], kf[KT];
+            float4 qf[4], kf[4];
 #pragma unroll
-            for (int x = 0; x < RT; ++x) qf[x] = *reinterpret_cast<const float4 *>(Q + (ty * RT + x) * LD + c);
+            for (int x = 0; x < 4; ++x) qf[x] = *reinterpret_cast<const float4 *>(Q + (ty * 4 + x) * LD + c);
 #pragma unroll
-            for (int y = 0; y < KT; ++y) kf[y] = *reinterpret_cast<const float4 *>(KV + (tx + TX * y) * LD + c);
+            for (int y = 0; y < 4; ++y) kf[y] = *reinterpret_cast<const float4 *>(KV + (tx + 16 * y) * LD + c);
 #pragma unroll
-            for (int x = 0; x < RT; ++x)
+            for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int y = 0; y < KT; ++y) {
+                for (int y = 0; y < 4; ++y) {
                     s[x][y] = fmaf(qf[x].x, kf[y].x, s[x][y]);
                     s[x][y] = fmaf(qf[x].y, kf[y].y, s[x][y]);
                     s[x][y] = fmaf(qf[x].z, kf[y].z, s[x][y]);
@@ -148,60 +157,52 @@ __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int r
         }
         const float c = a.scale_log2 * ks;
 #pragma unroll
-        for (int x = 0; x < RT; ++x) {
+        for (int x = 0; x < 4; ++x) {
             float mb = -INFINITY;
 #pragma unroll
-            for (int y = 0; y < KT; ++y) {
-                s[x][y] = raw && tx + TX * y > limit[x] ? -INFINITY : s[x][y] * c;
+            for (int y = 0; y < 4; ++y) {
+                s[x][y] = raw && tx + 16 * y > limit[x] ? -INFINITY : s[x][y] * c;
                 mb = fmaxf(mb, s[x][y]);
             }
 #pragma unroll
-            for (int w = TX / 2; w > 0; w >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
+            for (int w = 8; w > 0; w >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
             const float mn = fmaxf(m[x], mb), base = mn == -INFINITY ? 0.f : mn;
             const float corr = exp2f(m[x] - base);
             float sum = 0.f;
 #pragma unroll
-            for (int y = 0; y < KT; ++y) {
+            for (int y = 0; y < 4; ++y) {
                 const float p = exp2f(s[x][y] - base);
                 sum += p;
-                Pm[(ty * RT + x) * PLD + tx + TX * y] = p * vs;
+                Pm[(ty * 4 + x) * PLD + tx + 16 * y] = p * vs;
             }
 #pragma unroll
-            for (int w = TX / 2; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
             m[x] = mn;
             l[x] = l[x] * corr + sum;
 #pragma unroll
             for (int j = 0; j < CT; ++j) o[x][j] *= corr;
         }
         __syncthreads();   // K is read, P is written
-        if (raw) load_raw<InT, D, LD>(KV, u, tail + (int64_t)a.Hkv * kKvBlock * D, static_cast<const InT *>(a.v_new), a.Hkv, h);
+        if (raw) load_own<D, LD>(KV, a, u, 1, h);
         else load_page<D, LD>(KV, a.c.v + ph * kKvBlock * D);
         __syncthreads();
         // a key that the mask took has weight zero; it adds nothing whatever its value (a NaN or an infinity after
         // the row's position does not reach the row)
 #pragma unroll 2
         for (int k = 0; k < kKvBlock; k += 4) {
-            float4 pf[RT];
+            float4 pf[4];
 #pragma unroll
-            for (int x = 0; x < RT; ++x) pf[x] = *reinterpret_cast<const float4 *>(Pm + (ty * RT + x) * PLD + k);
+            for (int x = 0; x < 4; ++x) pf[x] = *reinterpret_cast<const float4 *>(Pm + (ty * 4 + x) * PLD + k);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
                 float v[CT];
-                if constexpr (R == 64) {
 #pragma unroll
-                    for (int j = 0; j < CT / 4; ++j) {
-                        const float4 f = *reinterpret_cast<const float4 *>(KV + (k + kk) * LD + 4 * tx + 64 * j);
-                        v[4 * j] = f.x; v[4 * j + 1] = f.y; v[4 * j + 2] = f.z; v[4 * j + 3] = f.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < CT / 2; ++j) {
-                        const float2 f = *reinterpret_cast<const float2 *>(KV + (k + kk) * LD + 2 * tx + 64 * j);
-                        v[2 * j] = f.x; v[2 * j + 1] = f.y;
-                    }
+                for (int j = 0; j < CT / 4; ++j) {
+                    const float4 f = *reinterpret_cast<const float4 *>(KV + (k + kk) * LD + 4 * tx + 64 * j);
+                    v[4 * j] = f.x; v[4 * j + 1] = f.y; v[4 * j + 2] = f.z; v[4 * j + 3] = f.w;
                 }
 #pragma unroll
-                for (int x = 0; x < RT; ++x) {
+                for (int x = 0; x < 4; ++x) {
                     const float p = kk == 0 ? pf[x].x : kk == 1 ? pf[x].y : kk == 2 ? pf[x].z : pf[x].w;
                     if (raw && p == 0.f) continue;
 #pragma unroll
@@ -210,24 +211,180 @@ __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int r
             }
         }
     }
-    // one segment: the result; several: the partial one (column j of a thread: 4 tx + 64 (j / 4) + j % 4, or the pairs)
-    constexpr int W = R == 64 ? 4 : 2;
+    // one segment: the result; several: the partial one (columns 4 tx + 64 j ..)
 #pragma unroll
-    for (int x = 0; x < RT; ++x) {
-        const int r = r0 + ty * RT + x;
+    for (int x = 0; x < 4; ++x) {
+        const int r = r0 + ty * 4 + x;
         if (r >= n_row) continue;
         const int head = h * a.G + r % a.G;
+        const float inv = last_seg > 0 ? 1.f : l[x] > 0.f ? 1.f / l[x] : (l[x] == 0.f ? 0.f : l[x]);   // no key: zero; NaN stays
+        float *dst;
         if (last_seg == 0) {
-            const float inv = l[x] > 0.f ? 1.f / l[x] : (l[x] == 0.f ? 0.f : l[x]);   // no key: zero; NaN stays
-            InT *dst = static_cast<InT *>(a.out) + ((int64_t)(u.row + r / a.G) * a.Hq + head) * D;
-#pragma unroll
-            for (int j = 0; j < CT; ++j) dst[W * tx + 64 * (j / W) + j % W] = from_f<InT>(o[x][j] * inv);
+            dst = static_cast<float *>(a.out) + ((int64_t)(u.row + r / a.G) * a.Hq + head) * D;
         } else {
             const int64_t pr = kv_part_row(a, ui, seg, r / a.G, head);
-            float *dst = a.part_o + pr * D;
-#pragma unroll
-            for (int j = 0; j < CT; ++j) dst[W * tx + 64 * (j / W) + j % W] = o[x][j];
+            dst = a.part_o + pr * D;
             if (tx == 0) a.part_ml[pr] = make_float2(m[x], l[x]);
+        }
+#pragma unroll
+        for (int j = 0; j < CT; j += 4)
+            *reinterpret_cast<float4 *>(dst + 4 * tx + 16 * j) = make_float4(o[x][j] * inv, o[x][j + 1] * inv, o[x][j + 2] * inv, o[x][j + 3] * inv);
+    }
+}
+
+// Few rows (a single token's heads): CTA (unit x tile of RT rows, kv head, segment), 4 warps, every fourth block each.
+//   scores   lane (g, t) = (lane / 4, lane % 4): 16 values of key 8 i + g at columns 16 t + 64 j, times RT rows' q from
+//            shared memory, added over t;
+//   output   lane (r, c): 16 columns 16 c of the keys = r modulo the rows a warp reads at once, added over r at the end.
+// The warps' results are added in order. Bound: the latency of a few dependent reads, then HBM.
+template <int D, int RT>
+__global__ void __launch_bounds__(128) kv_attn_few_simt_kernel(const KvAttn a, int row_tiles) {
+    constexpr int J = D / 64, LPR = D / 16, KPR = 32 / LPR;   // 16-column chunks of a lane; lanes of a value row, rows at once
+    grid_dep_wait();
+    grid_dep_launch();
+    const int ui = a.unit0 + blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * RT, h = blockIdx.y, seg = blockIdx.z;
+    const KvUnit u = kv_load_unit(a.units, ui);   // inside the map whatever the count
+    if (ui >= a.counts[0]) return;
+    const int last_seg = u.block / a.seg_blocks, n_row = u.count * a.G;
+    if (!kv_unit_ok(u, a.c, a.n_rows) || u.count > a.max_new || last_seg >= a.n_seg) {
+        if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
+        return;
+    }
+    if (r0 >= n_row || seg > last_seg) return;
+    __shared__ __align__(16) float sq[RT][D], sp[4][RT][kKvBlock], so[4][RT][D], sm[4][RT], sl[4][RT];
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = lane >> 2, tq = lane & 3, vr = lane / LPR, vc = lane % LPR;
+    for (int e = t; e < RT * D / 4; e += 128) {
+        const int r = r0 + e / (D / 4), c = e % (D / 4) * 4;
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < n_row)
+            f = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + ((int64_t)(u.row + r / a.G) * a.Hq + h * a.G + r % a.G) * D + c);
+        *reinterpret_cast<float4 *>(&sq[e / (D / 4)][c]) = f;
+    }
+    __syncthreads();
+    float o[RT][16], m[RT], l[RT];
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+        m[x] = -INFINITY;
+        l[x] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[x][j] = 0.f;
+    }
+    const int b0 = seg * a.seg_blocks, b1 = min(u.block + 1, b0 + a.seg_blocks);
+    for (int b = b0 + warp; b < b1; b += 4) {
+        const bool raw = b == u.block;
+        int64_t ph = 0;
+        float c = a.scale_log2, vs = 1.f;
+        if (!raw) {
+            int page = a.c.table[(int64_t)u.slot * a.c.max_blocks + b];
+            if ((unsigned)page >= (unsigned)a.c.n_pages) {
+                if (lane == 0) atomicOr(a.err, kErrKvBounds);
+                page = 0;   // in bounds; the result is reported as invalid
+            }
+            ph = (int64_t)page * a.Hkv + h;
+            c *= a.c.k_scale[ph];
+            vs = a.c.v_scale[ph];
+        }
+        const int8_t *kp = a.c.k + ph * (kKvBlock * D) + g * D + 16 * tq, *vp = a.c.v + ph * (kKvBlock * D) + vr * D + 16 * vc;
+        float s[RT][8];   // keys 8 i + g
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int x = 0; x < RT; ++x) s[x][i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                float f[16];
+                if (!raw) i8_to_f(__ldg(reinterpret_cast<const uint4 *>(kp + 8 * i * D + 64 * j)), f);
+                else ld_own16(own_row(a, u, 0, h, 8 * i + g, D), 64 * j + 16 * tq, f);
+#pragma unroll
+                for (int x = 0; x < RT; ++x)
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        const float4 qf = *reinterpret_cast<const float4 *>(&sq[x][64 * j + 16 * tq + k]);
+                        s[x][i] = fmaf(qf.x, f[k], s[x][i]);
+                        s[x][i] = fmaf(qf.y, f[k + 1], s[x][i]);
+                        s[x][i] = fmaf(qf.z, f[k + 2], s[x][i]);
+                        s[x][i] = fmaf(qf.w, f[k + 3], s[x][i]);
+                    }
+            }
+        }
+        __syncwarp();   // the block before is done with sp
+#pragma unroll
+        for (int x = 0; x < RT; ++x) {
+            const int limit = raw ? u.first + (r0 + x) / a.G : kKvBlock;
+            float mb = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s[x][i] += __shfl_xor_sync(0xffffffffu, s[x][i], 1);
+                s[x][i] += __shfl_xor_sync(0xffffffffu, s[x][i], 2);
+                s[x][i] = 8 * i + g > limit ? -INFINITY : s[x][i] * c;
+                mb = fmaxf(mb, s[x][i]);
+            }
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
+            const float mn = fmaxf(m[x], mb), base = mn == -INFINITY ? 0.f : mn;
+            const float corr = exp2f(m[x] - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p = exp2f(s[x][i] - base);
+                sum += p;
+                if (tq == 0) sp[warp][x][8 * i + g] = p * vs;
+            }
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            m[x] = mn;
+            l[x] = l[x] * corr + sum;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[x][j] *= corr;
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int k = 0; k < kKvBlock; k += KPR) {
+            float f[16];
+            if (!raw) i8_to_f(__ldg(reinterpret_cast<const uint4 *>(vp + k * D)), f);
+            else ld_own16(own_row(a, u, 1, h, k + vr, D), 16 * vc, f);
+#pragma unroll
+            for (int x = 0; x < RT; ++x) {
+                const float p = sp[warp][x][k + vr];
+                if (raw && p == 0.f) continue;   // masked: nothing, whatever the value
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[x][j] = fmaf(p, f[j], o[x][j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+#pragma unroll
+            for (int w = LPR; w < 32; w <<= 1) o[x][j] += __shfl_xor_sync(0xffffffffu, o[x][j], w);
+            if (vr == 0) so[warp][x][16 * vc + j] = o[x][j];
+        }
+        if (lane == 0) {
+            sm[warp][x] = m[x];
+            sl[warp][x] = l[x];
+        }
+    }
+    __syncthreads();
+    for (int e = t; e < RT * D; e += 128) {
+        const int x = e / D, col = e % D, r = r0 + x;
+        if (r >= n_row) break;
+        const float M = fmaxf(fmaxf(sm[0][x], sm[1][x]), fmaxf(sm[2][x], sm[3][x])), base = M == -INFINITY ? 0.f : M;
+        float y = 0.f, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float f = exp2f(sm[w][x] - base);
+            y = fmaf(f, so[w][x][col], y);
+            L = fmaf(f, sl[w][x], L);
+        }
+        const int head = h * a.G + r % a.G;
+        if (last_seg == 0) {
+            const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+            static_cast<float *>(a.out)[((int64_t)(u.row + r / a.G) * a.Hq + head) * D + col] = y * inv;
+        } else {
+            const int64_t pr = kv_part_row(a, ui, seg, r / a.G, head);
+            a.part_o[pr * D + col] = y;
+            if (col == 0) a.part_ml[pr] = make_float2(M, L);
         }
     }
 }
@@ -337,26 +494,25 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(const KvAttn a) {
     static_cast<InT *>(a.out)[((int64_t)u.row * a.Hq + r) * D + t] = from_f<InT>(x * inv);
 }
 
-template <typename InT, int D, int R>
-cudaError_t launch_simt(const KvAttn &a, int unit_bound, int rows_max, cudaStream_t st) {
-    using P = SimtPlan<InT, D, R>;
-    if (P::kBytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kv_attn_simt_kernel<InT, D, R>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::kBytes);
+template <int D>
+cudaError_t launch_simt(const KvAttn &a, int unit_bound, int rows_max, int few, cudaStream_t st) {
+    cudaError_t e;
+    if (few) {
+        // rows per CTA: what there is, up to 4 (16 columns each in registers)
+        const int rt = rows_max == 1 ? 1 : rows_max == 2 ? 2 : 4, row_tiles = (rows_max + rt - 1) / rt;
+        const dim3 grid((unsigned)((int64_t)unit_bound * row_tiles), (unsigned)a.Hkv, (unsigned)a.n_seg);
+        e = rt == 1 ? gdn_launch_pdl(kv_attn_few_simt_kernel<D, 1>, grid, 128, 0, st, a, row_tiles)
+            : rt == 2 ? gdn_launch_pdl(kv_attn_few_simt_kernel<D, 2>, grid, 128, 0, st, a, row_tiles)
+                      : gdn_launch_pdl(kv_attn_few_simt_kernel<D, 4>, grid, 128, 0, st, a, row_tiles);
+    } else {
+        using P = SimtPlan<D>;
+        e = cudaFuncSetAttribute(kv_attn_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::kBytes);
         if (e != cudaSuccess) return e;
+        const int row_tiles = (rows_max + P::R - 1) / P::R;
+        const dim3 grid((unsigned)((int64_t)unit_bound * row_tiles), (unsigned)a.Hkv, (unsigned)a.n_seg);
+        e = gdn_launch_pdl(kv_attn_simt_kernel<D>, grid, 256, P::kBytes, st, a, row_tiles);
     }
-    const int row_tiles = (rows_max + R - 1) / R;
-    const dim3 grid((unsigned)((int64_t)unit_bound * row_tiles), (unsigned)a.Hkv, (unsigned)a.n_seg);
-    const cudaError_t e = gdn_launch_pdl(kv_attn_simt_kernel<InT, D, R>, grid, 256, P::kBytes, st, a, row_tiles);
     return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-template <typename InT>
-cudaError_t launch_simt_d(const KvAttn &a, int d, int unit_bound, int rows_max, int few, cudaStream_t st) {
-    // few rows: tiles of 8 (a warp each), so that a single token's heads do not leave most of a 64-row tile idle
-    if (d == 64) return few ? launch_simt<InT, 64, 8>(a, unit_bound, rows_max, st) : launch_simt<InT, 64, 64>(a, unit_bound, rows_max, st);
-    if (d == 128) return few ? launch_simt<InT, 128, 8>(a, unit_bound, rows_max, st) : launch_simt<InT, 128, 64>(a, unit_bound, rows_max, st);
-    return few ? launch_simt<InT, 256, 8>(a, unit_bound, rows_max, st) : launch_simt<InT, 256, 64>(a, unit_bound, rows_max, st);
 }
 
 template <typename InT, int D>
@@ -374,7 +530,9 @@ cudaError_t launch_join(const KvAttn &a, int unit_bound, int few, cudaStream_t s
 }  // namespace gdn
 
 cudaError_t gdn_launch_kv_attn_simt(const gdn::KvAttn &a, int d, int unit_bound, int rows_max, int few, cudaStream_t st) {
-    return gdn::launch_simt_d<float>(a, d, unit_bound, rows_max, few, st);
+    if (d == 64) return gdn::launch_simt<64>(a, unit_bound, rows_max, few, st);
+    if (d == 128) return gdn::launch_simt<128>(a, unit_bound, rows_max, few, st);
+    return gdn::launch_simt<256>(a, unit_bound, rows_max, few, st);
 }
 
 cudaError_t gdn_launch_kv_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int few, cudaStream_t st) {

@@ -170,18 +170,16 @@ def _check(st: int):
         raise GdnError(st, load_library().gdn_last_error().decode())
 
 
-def _ptr(t: Optional[torch.Tensor]):
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     if t is None:
         return None
     if not t.is_contiguous():
         raise ValueError("tensors passed to the library must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+def _stream(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 _TORCH_DT = {GDN_BF16: torch.bfloat16, GDN_FP32: torch.float32}
@@ -464,16 +462,17 @@ def gdn_kv_status(plan: KvPlan, stream=None) -> int:
     return int(load_library().gdn_kv_status(ctypes.byref(plan.c), _stream(stream)))
 
 
-def _check_rows(desc, n_rows: int, dtype, **arrays):
-    for name, (t, heads) in arrays.items():
-        if t.dtype != dtype or tuple(t.shape) != (n_rows, heads, desc.head_dim):
-            raise ValueError(f"{name} must be {dtype} {[n_rows, heads, desc.head_dim]}, got {t.dtype} {list(t.shape)}")
+def _check_rows(name: str, t: torch.Tensor, desc: gdn_attn_desc, n_rows: int, heads: int):
+    if t.shape != (n_rows, heads, desc.head_dim) or t.dtype != _TORCH_DT[desc.in_dtype]:
+        raise ValueError(f"{name} must be {_TORCH_DT[desc.in_dtype]} {[n_rows, heads, desc.head_dim]}, got {t.dtype} "
+                         f"{list(t.shape)}")
 
 
 def gdn_kv_append(desc, cache: KvCache, plan: KvPlan, k: torch.Tensor, v: torch.Tensor, stream=None):
     """k, v: [n_rows][Hkv][d] in the plan's row order."""
     n, Hkv = k.shape[0], desc.n_kv_heads
-    _check_rows(desc, n, _TORCH_DT[desc.in_dtype], k=(k, Hkv), v=(v, Hkv))
+    _check_rows("k", k, desc, n, Hkv)
+    _check_rows("v", v, desc, n, Hkv)
     _check(load_library().gdn_kv_append(ctypes.byref(desc), ctypes.byref(cache.c), ctypes.byref(plan.c), _ptr(k),
                                         _ptr(v), n, _stream(stream)))
 
@@ -495,7 +494,10 @@ def gdn_kv_attention(desc, cache: KvCache, plan: KvPlan, q: torch.Tensor, k: tor
                      out: torch.Tensor, ws: Optional[torch.Tensor], max_new: int, max_len: int, stream=None):
     """q, out: [n_rows][Hq][d]; k, v: the arrays given to gdn_kv_append; max_new, max_len: bounds over the batch."""
     n, Hq, Hkv = q.shape[0], desc.n_q_heads, desc.n_kv_heads
-    _check_rows(desc, n, _TORCH_DT[desc.in_dtype], q=(q, Hq), k=(k, Hkv), v=(v, Hkv), out=(out, Hq))
+    _check_rows("q", q, desc, n, Hq)
+    _check_rows("k", k, desc, n, Hkv)
+    _check_rows("v", v, desc, n, Hkv)
+    _check_rows("out", out, desc, n, Hq)
     _check(load_library().gdn_kv_attention(ctypes.byref(desc), ctypes.byref(cache.c), ctypes.byref(plan.c), _ptr(q),
                                            _ptr(k), _ptr(v), _ptr(out), n, max_new, max_len, _ptr(ws),
                                            ws.numel() if ws is not None else 0, _stream(stream)))
