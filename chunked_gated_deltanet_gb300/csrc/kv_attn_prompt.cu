@@ -106,26 +106,34 @@ template <int D>
 struct PromptPlan {
     static constexpr int NQ = D == 256 ? 1 : 2;              // MMA tiles of 128 rows
     static constexpr int R = 128 * NQ;
-    static constexpr int NS = D == 256 ? 2 : 4;              // key and value slots of 64 keys each
+    static constexpr int NS = D == 256 ? 3 : 4;              // key and value slots of 64 keys each
+    // One tile leaves TMEM columns for its queries: they are the A operand from there, which spares the shared-memory pipe
+    // two thirds of S's reads and the queries' place.
+    static constexpr bool kQT = NQ == 1;
     static constexpr int CW = D == 256 ? 8 : 4;              // warps that convert keys, and as many that convert values
     // First thread of the roles. The issuing warps come first: a scheduler that prefers older warps then lets their few
     // instructions through.
     static constexpr int kSoft0 = 128, kKeys0 = kSoft0 + 128 * NQ, kVals0 = kKeys0 + 32 * CW, NT = kVals0 + 32 * CW;
     static constexpr uint32_t kTile = 128 * D * 2;           // bytes of a 128-row query tile
     static constexpr uint32_t kBlk = 64 * D * 2;             // bytes of a slot
-    static constexpr uint32_t kQ = 0, kK = NQ * kTile, kV = kK + NS * kBlk, kInfo = kV + NS * kBlk;
+    // queries, key slots, value slots; with the queries in TMEM they pass through the third key and value slots
+    static constexpr uint32_t kQ = kQT ? 4 * kBlk : 0, kK = kQT ? 0 : NQ * kTile, kV = kK + (kQT ? 2 : NS) * kBlk,
+                              kInfo = kQT ? 6 * kBlk : kV + NS * kBlk;
+    __host__ __device__ static constexpr uint32_t key_slot(uint32_t i) { return kK + (kQT && i == 2 ? 4 : i) * kBlk; }
+    __host__ __device__ static constexpr uint32_t val_slot(uint32_t i) { return kV + (kQT && i == 2 ? 3 : i) * kBlk; }
     static constexpr int kMaxBlocks = 64 + 4;                // 8-bit blocks of a segment and raw blocks of a span
     static constexpr uint32_t kRow = kInfo + kMaxBlocks * 16;        // float2 [R]: what takes Q's scaling out, 1152 sum(Q)
     static constexpr uint32_t kRawK = kRow + R * 8;                  // float [4][64]: the scalings of the raw blocks' keys
     static constexpr uint32_t kBar = kRawK + 4 * 64 * 4;
     // barriers: key and value slots full and free, scores and weights of (tile, buffer), a tile's product before its last,
-    // all products, the queries and the blocks' scales
+    // all products, the queries and the blocks' scales, the
+    // queries in TMEM
     static constexpr int bKFull = 0, bKFree = NS, bVFull = 2 * NS, bVFree = 3 * NS, bS = 4 * NS, bP = bS + 2 * NQ,
-                         bPV = bP + 2 * NQ, bDrain = bPV + NQ, bReady = bDrain + 1, kNBar = bReady + 1;
+                         bPV = bP + 2 * NQ, bDrain = bPV + NQ, bReady = bDrain + 1, bQ = bReady + 1, kNBar = bQ + 1;
     static constexpr uint32_t kSlot = kBar + (kNBar + 1) / 2 * 16;
     static constexpr uint32_t kBad = kSlot + 16;             // per raw block of the span: it has a value that is not finite
     static constexpr uint32_t kBytes = kBad + 16;
-    static constexpr uint32_t kO = 256;                      // TMEM columns: scores [0, 256), outputs from here
+    static constexpr uint32_t kO = 256;                      // TMEM columns: scores [0, 128 NQ), queries from 128, outputs from here
     static constexpr uint32_t kTmemCols = 512;
     static constexpr int kVec = D / 64;                      // 64-column groups
     static constexpr int kLoads = 8 * kVec / CW;             // 16-byte loads of a key or value thread per block
@@ -210,6 +218,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         for (int i = 0; i < P::NQ; ++i) mbar_init(&bar64[P::bPV + i], 1);
         mbar_init(&bar64[P::bDrain], nt);
         mbar_init(&bar64[P::bReady], P::NT / 32);
+        mbar_init(&bar64[P::bQ], 4);
         mbar_init_fence();
         for (int i = 0; i < 4; ++i) bad_v[i] = 0;
     }
@@ -268,7 +277,28 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 if (c == 0) row_q[r] = make_float2(back, 1152.f * up * sum);
             }
         }
-        fence_proxy_async();
+        if constexpr (P::kQT) {   // each softmax thread its row, from the slots into TMEM
+            kv_named_barrier(3, P::kKeys0);
+            if (t >= P::kSoft0) {
+                const int r = t - P::kSoft0;
+                const unsigned char *src = sm + P::kQ + (r >> 3) * (D * 16) + (r & 7) * 16;
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(src + (4 * k + i) * 128);
+                        w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+                    }
+                    tmem_st16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 + 16 * k, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(bar(P::bQ));
+            }
+        } else {
+            fence_proxy_async();
+        }
         warp_arrive(bar(P::bReady));
         alive = warp_wait(bar(P::bReady), 0, limit);
     }
@@ -281,15 +311,19 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             constexpr uint32_t idS = umma_idesc_f16(128, 64, 0, 0), idO8 = umma_idesc_f16(128, D, 0, 1),
                                idOraw = umma_idesc_bf16(128, D, 0, 1);
             const bool elected = elect_one();
+            if constexpr (P::kQT) alive = warp_wait(bar(P::bQ), 0, limit) && alive;
             const uint64_t dq = umma_smem_desc(sm + P::kQ + tile * P::kTile, 128, D * 16),
-                           dk0 = umma_smem_desc(sm + P::kK, 128, D * 16), dv0 = umma_smem_desc(sm + P::kV, D * 16, 128);
+                           dk0 = umma_smem_desc(sm, 128, D * 16), dv0 = umma_smem_desc(sm, D * 16, 128);
             const uint32_t s0_tm = tmem + 128 * tile, o_tm = tmem + P::kO + tile * D;
             auto issue_s = [&](int n) {
                 const int slot = n % NS, b = n & 1;
-                const uint64_t dk = dk0 + slot * (P::kBlk >> 4);
+                const uint64_t dk = dk0 + (P::key_slot(slot) >> 4);
                 if (elected) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) umma_bf16(s0_tm + 64 * b, dq + 16 * k, dk + 16 * k, idS, k > 0);
+                    for (int k = 0; k < D / 16; ++k) {
+                        if constexpr (P::kQT) umma_bf16_ts(s0_tm + 64 * b, tmem + 128 + 8 * k, dk + 16 * k, idS, k > 0);
+                        else umma_bf16(s0_tm + 64 * b, dq + 16 * k, dk + 16 * k, idS, k > 0);
+                    }
                     bar_commit(bar(P::bS + 2 * tile + b));
                     bar_commit(bar(P::bKFree + slot));
                 }
@@ -309,7 +343,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                                                       bar(P::bP + 2 * tile + b), (n >> 1) & 1, limit));
                 if (!alive) break;
                 tc_fence_after();
-                const uint64_t dv = dv0 + slot * (P::kBlk >> 4);
+                const uint64_t dv = dv0 + (P::val_slot(slot) >> 4);
                 const uint32_t p_tm = s0_tm + 64 * b, idO = n < n8 ? idO8 : idOraw;
                 if (elected) {
 #pragma unroll
@@ -366,7 +400,6 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         const int8_t *pool = (is_v ? a.c.v : a.c.k) + (int64_t)h * (kKvBlock * D) + kr * D + ch * 16;
         const int64_t stride = (int64_t)a.Hkv * (kKvBlock * D);
         const uint32_t full = bar(is_v ? P::bVFull : P::bKFull), free = bar(is_v ? P::bVFree : P::bKFree);
-        unsigned char *slots = sm + (is_v ? P::kV : P::kK) + kr * 16 + ch * 256;
         // load i of this warp: 8 keys x 64 columns, key group (cw + CW i) / kVec, column group (cw + CW i) % kVec
         uint4 w[P::kLoads];
         auto load = [&](int n) {
@@ -445,7 +478,11 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 alive = false;
                 break;
             }
-            unsigned char *dst = slots + slot * P::kBlk;
+            if (P::kQT && n == 2 && !warp_wait(bar(P::bQ), 0, limit)) {   // the queries leave the third slots
+                alive = false;
+                break;
+            }
+            unsigned char *dst = sm + (is_v ? P::val_slot(slot) : P::key_slot(slot)) + kr * 16 + ch * 256;
             if (n < n8) {
                 if (is_v) store(std::true_type{}, dst);
                 else store(std::false_type{}, dst);
@@ -582,9 +619,9 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 a.part_ml[pr] = make_float2(m, l);
             }
             const bool fix = live && seg == last_seg && bad_v[min(max(blk - blo, 0), 3)] != 0;
-            // The warp's 32 rows pass through shared memory (Q's, which every product has read), 128 bytes of a row at a time
+            // The warp's 32 rows pass through shared memory (the operands', which every product has read), 128 bytes of a row at a time
             // with the 16-byte chunks of row i at chunk ^ (i % 8), so that the stores to global memory are of whole rows.
-            unsigned char *stage = sm + P::kQ + (warp - P::kSoft0 / 32) * (32 * 128);
+            unsigned char *stage = sm + (warp - P::kSoft0 / 32) * (32 * 128);
             const int64_t dst_row = one ? (int64_t)(u.row + tok) * a.Hq + head : pr;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {

@@ -179,7 +179,9 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is None:   # the current stream's handle without a Stream object around it (3 us of a short call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 _TORCH_DT = {GDN_BF16: torch.bfloat16, GDN_FP32: torch.float32}
