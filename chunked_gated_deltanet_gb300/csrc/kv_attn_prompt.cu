@@ -115,7 +115,11 @@ struct PromptPlan {
     // instructions through.
     static constexpr int kSoft0 = 128, kKeys0 = kSoft0 + 128 * NQ, kVals0 = kKeys0 + 32 * CW, NT = kVals0 + 32 * CW;
     static constexpr uint32_t kTile = 128 * D * 2;           // bytes of a 128-row query tile
-    static constexpr uint32_t kBlk = 64 * D * 2;             // bytes of a slot
+    // A slot's core matrices (8 keys x 16 bytes) lie 144 bytes apart along d and kGroup apart along the keys. With 128 the
+    // lanes that write without bank conflicts are 8 keys of one column, whose 16-byte reads of 8 pages' rows take 32 passes
+    // of the load pipe; with 144 they are 2 keys of 4 columns, and take 8.
+    static constexpr uint32_t kCore = 144, kGroup = D / 8 * kCore;
+    static constexpr uint32_t kBlk = 8 * kGroup;             // bytes of a slot
     // queries, key slots, value slots; with the queries in TMEM they pass through the third key and value slots
     static constexpr uint32_t kQ = kQT ? 4 * kBlk : 0, kK = kQT ? 0 : NQ * kTile, kV = kK + (kQT ? 2 : NS) * kBlk,
                               kInfo = kQT ? 6 * kBlk : kV + NS * kBlk;
@@ -313,7 +317,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             const bool elected = elect_one();
             if constexpr (P::kQT) alive = warp_wait(bar(P::bQ), 0, limit) && alive;
             const uint64_t dq = umma_smem_desc(sm + P::kQ + tile * P::kTile, 128, D * 16),
-                           dk0 = umma_smem_desc(sm, 128, D * 16), dv0 = umma_smem_desc(sm, D * 16, 128);
+                           dk0 = umma_smem_desc(sm, P::kCore, P::kGroup), dv0 = umma_smem_desc(sm, P::kGroup, P::kCore);
             const uint32_t s0_tm = tmem + 128 * tile, o_tm = tmem + P::kO + tile * D;
             auto issue_s = [&](int n) {
                 const int slot = n % NS, b = n & 1;
@@ -321,8 +325,8 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 if (elected) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        if constexpr (P::kQT) umma_bf16_ts(s0_tm + 64 * b, tmem + 128 + 8 * k, dk + 16 * k, idS, k > 0);
-                        else umma_bf16(s0_tm + 64 * b, dq + 16 * k, dk + 16 * k, idS, k > 0);
+                        if constexpr (P::kQT) umma_bf16_ts(s0_tm + 64 * b, tmem + 128 + 8 * k, dk + 2 * P::kCore / 16 * k, idS, k > 0);
+                        else umma_bf16(s0_tm + 64 * b, dq + 16 * k, dk + 2 * P::kCore / 16 * k, idS, k > 0);
                     }
                     bar_commit(bar(P::bS + 2 * tile + b));
                     bar_commit(bar(P::bKFree + slot));
@@ -348,11 +352,11 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 if (elected) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        umma_bf16_ts(o_tm, p_tm + 8 * k, dv + (uint64_t)(2 * D * k), idO, n > 0 || k > 0);
+                        umma_bf16_ts(o_tm, p_tm + 8 * k, dv + 2 * P::kGroup / 16 * k, idO, n > 0 || k > 0);
                     if (n >= n8) {   // the low parts of the raw block's weights
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            umma_bf16_ts(o_tm, p_tm + 32 + 8 * k, dv + (uint64_t)(2 * D * k), idO, 1);
+                            umma_bf16_ts(o_tm, p_tm + 32 + 8 * k, dv + 2 * P::kGroup / 16 * k, idO, 1);
                     }
                 }
                 if (more) issue_s(n + 2);
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         }
         kv_named_barrier(2, 64 * P::CW);
         warp_arrive(bar(P::bReady));
-        const int cw = warp % P::CW, kr = lane & 7, ch = lane >> 3;   // warp of the role; key of 8 and 16-byte chunk of 64
+        const int cw = warp % P::CW, kr = lane >> 2, ch = lane & 3;   // warp of the role; key of 8 and 16-byte chunk of 64
         const bf *tail = static_cast<const bf *>(a.c.tail);
         const int8_t *pool = (is_v ? a.c.v : a.c.k) + (int64_t)h * (kKvBlock * D) + kr * D + ch * 16;
         const int64_t stride = (int64_t)a.Hkv * (kKvBlock * D);
@@ -417,9 +421,9 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             for (int i = 0; i < P::kLoads; ++i) {
                 const int j = cw + P::CW * i;
                 const uint2 x0 = i8_to_f16x4<V>(w[i].x), x1 = i8_to_f16x4<V>(w[i].y), x2 = i8_to_f16x4<V>(w[i].z), x3 = i8_to_f16x4<V>(w[i].w);
-                unsigned char *o = dst + j / P::kVec * (D * 16) + j % P::kVec * 1024;
+                unsigned char *o = dst + j / P::kVec * P::kGroup + j % P::kVec * (8 * P::kCore);
                 *reinterpret_cast<uint4 *>(o) = make_uint4(x0.x, x0.y, x1.x, x1.y);
-                *reinterpret_cast<uint4 *>(o + 128) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                *reinterpret_cast<uint4 *>(o + P::kCore) = make_uint4(x2.x, x2.y, x3.x, x3.y);
             }
         };
         // a raw block: the tail's rows, then the new ones, zero past the last
@@ -457,12 +461,12 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                                 }
                                 y[k] = f8_to_h8(f);
                             }
-                            if (pass == 1) *reinterpret_cast<uint4 *>(dst + kg * (D * 16) + dg * 1024 + k * 128) = y[k];
+                            if (pass == 1) *reinterpret_cast<uint4 *>(dst + kg * P::kGroup + dg * (8 * P::kCore) + k * P::kCore) = y[k];
                         }
                     }
                     if (pass == 0) {
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                         float back;
                         up = pow2_to_2_15(top, back);
                         if (ch == 0) raw_k[(block - blo) * 64 + off] = back;
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 alive = false;
                 break;
             }
-            unsigned char *dst = sm + (is_v ? P::val_slot(slot) : P::key_slot(slot)) + kr * 16 + ch * 256;
+            unsigned char *dst = sm + (is_v ? P::val_slot(slot) : P::key_slot(slot)) + kr * 16 + ch * (2 * P::kCore);
             if (n < n8) {
                 if (is_v) store(std::true_type{}, dst);
                 else store(std::false_type{}, dst);
