@@ -57,7 +57,7 @@ struct TokenPlan {
 
 // N 32-bit words from global memory (N = 2 or a multiple of 4)
 template <int N>
-__device__ __forceinline__ void ld_words(uint32_t (&w)[N], const void *p) {
+__device__ __forceinline__ void ld_words(uint32_t *w, const void *p) {
     if constexpr (N == 2) {
         const uint2 x = __ldg(static_cast<const uint2 *>(p));
         w[0] = x.x; w[1] = x.y;
@@ -115,6 +115,8 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
     using P = TokenPlan<D, R>;
     using bf = __nv_bfloat16;
     constexpr int UK = P::UK, NA = P::NA, J = P::J, W = P::W, NO = P::NO, NT = P::NT, NU = P::NU;
+    constexpr int VB = NO < 16 ? NO : 16;   // bytes of a value row that a lane reads at once
+    auto col = [](int g, int i) { return i / VB * (8 * VB) + g * VB + i % VB; };   // column i of lane group g
     grid_dep_wait();
     grid_dep_launch();
     const int ui = a.unit0 + blockIdx.x, h = blockIdx.y;
@@ -148,14 +150,16 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
 #pragma unroll
         for (int x = 0; x < 2 * NA; ++x)
 #pragma unroll
-            for (int j = 0; j < J; ++j) ld_words(kb[x / 2][x % 2][j], src + 8 * x * D + 64 * j);
+            for (int j = 0; j < J; ++j) ld_words<4>(kb[x / 2][x % 2][j], src + 8 * x * D + 64 * j);
     };
     auto load_v = [&](int page, int n) {
-        const int8_t *src = a.c.v + ((int64_t)page * a.Hkv + h) * (kKvBlock * D) + (n * UK + 2 * tq) * D + g * NO;
+        const int8_t *src = a.c.v + ((int64_t)page * a.Hkv + h) * (kKvBlock * D) + (n * UK + 2 * tq) * D + g * VB;
 #pragma unroll
         for (int x = 0; x < NA; ++x)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) ld_words(vb[x][y], src + (16 * x + (y & 1) + 8 * (y >> 1)) * D);
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int i = 0; i < W; i += VB / 4) ld_words<VB / 4>(&vb[x][y][i], src + (16 * x + (y & 1) + 8 * (y >> 1)) * D + 8 * 4 * i);
     };
     int blk = blockIdx.z * a.seg_blocks + warp, page = page_of(blk);
     if (page >= 0) {
@@ -261,10 +265,10 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                 }
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                    if (key[x]) ld_words(w[x], key[x] + 64 * j + 16 * tq);
+                    if (key[x]) ld_words<8>(w[x], key[x] + 64 * j + 16 * tq);
 #pragma unroll
                 for (int f = 0; f < NT; ++f)
-                    if (g + 8 * f < n_row) ld_words(qw[f], q_row(g + 8 * f) + 64 * j);
+                    if (g + 8 * f < n_row) ld_words<8>(qw[f], q_row(g + 8 * f) + 64 * j);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t ka[4] = {w[0][2 * k], w[1][2 * k], w[0][2 * k + 1], w[1][2 * k + 1]};
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     uint4 x = make_uint4(0, 0, 0, 0);
-                    if (val[y]) x = __ldg(reinterpret_cast<const uint4 *>(val[y] + g * NO + 8 * i));
+                    if (val[y]) x = __ldg(reinterpret_cast<const uint4 *>(val[y] + col(g, 8 * i)));
                     // a value that is not finite would reach rows that do not see it (0 * inf): left out here, and
                     // added by the rows that do at the end
                     odd_value |= drop_not_finite(x);
@@ -325,10 +329,10 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                     const int r = 8 * f + 2 * tq + y, n_see = r < n_row ? u.first + r / a.G + 1 : 0;
 #pragma unroll 1
                     for (int k = 0; k < n_see; ++k) {
-                        const bf *src = raw_row(1, k) + g * NO;
+                        const bf *src = raw_row(1, k);
 #pragma unroll
                         for (int i = 0; i < NO; ++i) {
-                            const float x = to_f(src[i]);
+                            const float x = to_f(src[col(g, i)]);
                             if (!(fabsf(x) <= 3.4e38f)) o[i / 2][f][2 * (i & 1) + y] += x;
                         }
                     }
@@ -344,10 +348,10 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int r = 8 * f + 2 * tq + y;
-                    float *dst = so + (warp * R + r) * D + g * NO;
+                    float *dst = so + (warp * R + r) * D;
 #pragma unroll
                     for (int i = 0; i < NO / 2; i += 2)
-                        *reinterpret_cast<float4 *>(dst + 2 * i) =
+                        *reinterpret_cast<float4 *>(dst + col(g, 2 * i)) =
                             make_float4(o[i][f][y], o[i][f][2 + y], o[i + 1][f][y], o[i + 1][f][2 + y]);
                     float sum = l[f][y];
 #pragma unroll
