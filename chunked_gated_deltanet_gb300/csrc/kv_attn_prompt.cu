@@ -238,48 +238,51 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     bool alive = true;
 
     if (t < P::kKeys0) {
-        // ---- the queries, by the issuing and the softmax warps while the first blocks are fetched: a warp takes 32 / (d / 8)
-        // rows at a time, a lane 8 columns; into K-major core matrices (8 rows x 16 bytes) ----
-        constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = P::kKeys0 / 32 * RPW, IT = 4;   // IT loads in flight
-        const int c = lane % LPR;
+        // ---- the queries, by the issuing and the softmax warps while the first blocks are fetched: a warp takes 8 rows at a
+        // time and 4 lanes a row, each every fourth piece of 8 columns. So two rows and two sectors go to a quarter warp's load,
+        // and the 32 stores of a piece fill four K-major core matrices (8 rows x 16 bytes) side by side, free of conflicts ----
+        constexpr int NP = D / 32, STEP = P::kKeys0 / 32 * 8;
+        const int c = lane & 3;
 #pragma unroll 1
-        for (int rb = warp * RPW + lane / LPR; rb - lane / LPR < nt * 128; rb += IT * STEP) {
-            uint4 qw[IT];
+        for (int rb = warp * 8; rb < nt * 128; rb += STEP) {
+            const int r = rb + (lane >> 2), rr = r0 + r;
+            uint4 w[NP];
+            if (r < rows_here) {
+                const int tok = rr / a.G;
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const bf *>(a.q) +
+                                                                   ((int64_t)(u.row + tok) * a.Hq + h * a.G + (rr - tok * a.G)) * D) + c;
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int r = rb + i * STEP, rr = r0 + r;
-                qw[i] = make_uint4(0, 0, 0, 0);
-                if (r < rows_here)
-                    qw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const bf *>(a.q) +
-                                                                  ((int64_t)(u.row + rr / a.G) * a.Hq + h * a.G + rr % a.G) * D + c * 8));
+                for (int i = 0; i < NP; ++i) w[i] = __ldg(src + 4 * i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) w[i] = make_uint4(0, 0, 0, 0);
             }
-#pragma unroll 1
-            for (int i = 0; i < IT; ++i) {
-                const int r = rb + i * STEP;
-                uint4 w = qw[0];
+            float f[8], top = 0.f, sum = 0.f;
 #pragma unroll
-                for (int k = 0; k + 1 < IT; ++k) qw[k] = qw[k + 1];
-                float f[8], top = 0.f, sum = 0.f;
-                b8_to_f(w, f);
+            for (int i = 0; i < NP; ++i) {
+                b8_to_f(w[i], f);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     top = fmaxf(top, fabsf(f[k]));
                     sum += f[k];
                 }
+            }
 #pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) {
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                }
-                float back;
-                const float up = pow2_to_2_15(top, back);
+            for (int o = 2; o > 0; o >>= 1) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            }
+            float back;
+            const float up = pow2_to_2_15(top, back);
+            unsigned char *dst = sm + P::kQ + (r >> 7) * P::kTile + ((r & 127) >> 3) * (D * 16) + c * 128 + (r & 7) * 16;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                b8_to_f(w[i], f);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) f[k] *= up;
-                w = f8_to_h8(f);
-                if (r >= nt * 128) continue;
-                *reinterpret_cast<uint4 *>(sm + P::kQ + (r >> 7) * P::kTile + ((r & 127) >> 3) * (D * 16) + c * 128 + (r & 7) * 16) = w;
-                if (c == 0) row_q[r] = make_float2(back, 1152.f * up * sum);
+                *reinterpret_cast<uint4 *>(dst + 512 * i) = f8_to_h8(f);
             }
+            if (c == 0) row_q[r] = make_float2(back, 1152.f * up * sum);
         }
         if constexpr (P::kQT) {   // each softmax thread its row, from the slots into TMEM
             kv_named_barrier(3, P::kKeys0);
