@@ -55,6 +55,16 @@ __host__ __device__ __forceinline__ int64_t kv_tail_offset(int slot, int buf, in
     return ((((int64_t)slot * 2 + buf) * 2 + kv) * Hkv + h) * kKvBlock * d;
 }
 
+// Growing segments of the many-row bf16 form, in blocks: 32 below block 64, 64 below 128, 128 below 512, then 256. A segment
+// costs its CTA about 12 blocks' time besides its own (queries in, outputs out) and the join a row of partial results, so
+// long contexts want long ones, and short contexts short ones, to have CTAs for all SMs. Cut at absolute positions.
+constexpr int kKvMaxSegBlocks = 256;
+constexpr int kv_prompt_rows(int d) { return d == 256 ? 128 : 256; }   // rows of a CTA of that form
+__host__ __device__ constexpr int kv_grown_seg(int block) {
+    return block < 64 ? block / 32 : block < 128 ? 2 : block < 512 ? 2 + block / 128 : 4 + block / 256;
+}
+__host__ __device__ constexpr int kv_grown_start(int seg) { return seg < 3 ? 32 * seg : seg < 6 ? 128 * (seg - 2) : 256 * (seg - 4); }
+
 // Attention launch. Rows of a unit for kv head h: r = t * G + g, token t of the unit and query head h * G + g.
 struct KvAttn {
     const void *q, *k_new, *v_new;  // [n_rows][Hq][d], [n_rows][Hkv][d]
@@ -69,12 +79,16 @@ struct KvAttn {
     int64_t part_rows;              // units of the launch * tok_stride * Hq
     int unit0;                      // first unit of the launch (a call whose partials do not fit is several)
     int tok_stride;                 // most tokens of a unit: min(64, max_new)
-    int seg_blocks, n_seg;          // keys [s * seg_blocks, (s + 1) * seg_blocks) * 64 belong to segment s
+    int seg_blocks, n_seg;          // segment s: blocks [s * seg_blocks, (s + 1) * seg_blocks), or by kv_grown_start with seg_blocks 0
     int max_new;                    // the caller's bound on a request's new tokens
     long long wait_limit;           // polls before a bounded wait gives up
     int skip_first_copy;            // test hook: 3 = the prompt kernel never announces its first key tile
     unsigned int *err;
 };
+
+// Segment of a block, and a segment's first block.
+__device__ __forceinline__ int kv_seg_of(const KvAttn &a, int block) { return a.seg_blocks ? block / a.seg_blocks : kv_grown_seg(block); }
+__device__ __forceinline__ int kv_seg_start(const KvAttn &a, int seg) { return a.seg_blocks ? seg * a.seg_blocks : kv_grown_start(seg); }
 
 // Row of the partial results: (unit, token of the unit, query head) of a segment.
 __device__ __forceinline__ int64_t kv_part_row(const KvAttn &a, int unit, int seg, int tok, int head) {

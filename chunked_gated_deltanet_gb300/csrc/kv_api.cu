@@ -5,6 +5,7 @@
 #include "kv.cuh"
 
 #include <algorithm>
+#include <array>
 #include <cmath>
 
 using namespace gdn_host;
@@ -64,13 +65,22 @@ gdn::KvCache device_cache(const gdn_kv_cache *c) {
 int64_t max_units(int64_t tokens, int32_t requests) { return std::min<int64_t>(tokens, tokens / kKvBlock + 2LL * requests); }
 
 // Key segments of a row's attention, in blocks, cut at absolute positions. Few rows: 512 keys for up to three key/value
-// heads, so that one token's long context fills the GPU, up to 4,096 for more heads, which fill it with longer ones. Many
-// rows: 4,096 keys, where the partial results are a small share of the work; in fp32 512, where 64 rows of one head take
-// about 3 us a block. A rule on the description alone: a row's segments do not depend on the batch.
-int seg_blocks(const gdn_attn_desc *d, bool few) {
+// heads, so that one token's long context fills the GPU, up to 4,096 for more heads, which fill it with longer ones. fp32:
+// 512, where 64 rows of one head take about 3 us a block. Many rows in bf16: by the CTAs of one request and segment. Up to
+// 31, short segments fill the SMs; up to 159, growing ones (0, kv_grown_start's); more fill them alone. Against 64
+// blocks throughout (us): 165 x 12 rows of 6 sessions over 18,107 keys 60 -> 37, 290 x 16 rows over 41,802 240 -> 220,
+// 4,000 x 16 over 37,802 1,164 -> 1,075; and 180 x 16 rows of 16 sessions over 12,000, which fill the GPU together,
+// 193 -> 198. A rule on the description and max_new: a row's segments do not depend on the batch.
+int many_ctas(const gdn_attn_desc *d, int64_t max_new) {
+    const int rows = gdn::kv_prompt_rows(d->head_dim), G = d->n_q_heads / d->n_kv_heads;
+    return (int)std::min<int64_t>((max_new * G + rows - 1) / rows * d->n_kv_heads, INT32_MAX);
+}
+constexpr int kManySteps[] = {8, 32, 160}, kManySegs[] = {32, 48, 0, 128};
+int seg_blocks(const gdn_attn_desc *d, bool few, int64_t max_new) {
     if (d->in_dtype == GDN_FP32) return 8;
-    if (!few || d->n_kv_heads >= 16) return 64;
-    return d->n_kv_heads < 4 ? 8 : d->n_kv_heads < 8 ? 16 : 32;
+    if (few) return d->n_kv_heads < 4 ? 8 : d->n_kv_heads < 8 ? 16 : d->n_kv_heads < 16 ? 32 : 64;
+    const int n = many_ctas(d, max_new);
+    return kManySegs[n < kManySteps[0] ? 0 : n < kManySteps[1] ? 1 : n < kManySteps[2] ? 2 : 3];
 }
 constexpr int kFewRows = 16;   // rows (new tokens of a block x query heads per key/value head) of the few-row form
 
@@ -86,11 +96,19 @@ Form form_of(const gdn_attn_desc *d, int64_t max_new, int64_t max_len) {
     f.tok_stride = (int)std::min<int64_t>(max_new, kKvBlock);
     f.rows_max = f.tok_stride * G;
     f.few = max_new * G <= kFewRows;
-    f.seg_blocks = seg_blocks(d, f.few);
+    f.seg_blocks = seg_blocks(d, f.few, max_new);
     const int64_t blocks = std::max<int64_t>((max_len + kKvBlock - 1) / kKvBlock, 1);
-    f.n_seg = (blocks + f.seg_blocks - 1) / f.seg_blocks;
+    f.n_seg = f.seg_blocks ? (blocks + f.seg_blocks - 1) / f.seg_blocks : gdn::kv_grown_seg((int)blocks - 1) + 1;
     f.unit_bytes = f.n_seg == 1 ? 0 : (size_t)f.n_seg * f.tok_stride * d->n_q_heads * (d->head_dim * sizeof(float) + sizeof(float2));
     return f;
+}
+// The largest max_new of each of these forms, none above `most`: a form's partial results are the largest there.
+std::array<int64_t, 5> form_tops(const gdn_attn_desc *d, int64_t most) {
+    const int G = d->n_q_heads / d->n_kv_heads, rows = gdn::kv_prompt_rows(d->head_dim);
+    std::array<int64_t, 5> tops = {kFewRows / G, most};
+    for (int i = 0; i < 3; ++i) tops[2 + i] = (int64_t)((kManySteps[i] - 1) / d->n_kv_heads) * rows / G;
+    for (int64_t &n : tops) n = std::min(std::max<int64_t>(n, 1), most);
+    return tops;
 }
 constexpr size_t kWsTarget = size_t(2) << 30;   // a call's partial results beyond this go in several launches
 constexpr size_t kWsSlack = 512;                // alignment of the two parts
@@ -166,19 +184,20 @@ GDN_API gdn_status gdn_kv_append(const gdn_attn_desc *d, const gdn_kv_cache *c, 
 
 GDN_API size_t gdn_kv_attention_workspace_min(const gdn_attn_desc *d, int64_t max_len) {
     if (check_attn(d) != GDN_OK || max_len < 0 || max_len > INT32_MAX) return 0;
-    const int64_t few = std::max(1, kFewRows / (d->n_q_heads / d->n_kv_heads));
-    return kWsSlack + std::max(form_of(d, few, max_len).unit_bytes, form_of(d, kKvBlock + kFewRows, max_len).unit_bytes);
+    size_t need = 0;
+    for (const int64_t max_new : form_tops(d, INT32_MAX)) need = std::max(need, form_of(d, max_new, max_len).unit_bytes);
+    return kWsSlack + need;
 }
 
 GDN_API size_t gdn_kv_attention_workspace(const gdn_attn_desc *d, int64_t max_tokens, int32_t max_requests, int64_t max_len) {
     if (check_attn(d) != GDN_OK || max_tokens < 0 || max_tokens > INT32_MAX || max_requests < 1 || max_len < 0 ||
         max_len > INT32_MAX)
         return 0;
-    const size_t units = (size_t)max_units(max_tokens, max_requests);
-    const int64_t few = std::max(1, kFewRows / (d->n_q_heads / d->n_kv_heads));
     size_t need = 0;
-    for (const int64_t max_new : {std::min<int64_t>(few, std::max<int64_t>(max_tokens, 1)), std::max<int64_t>(max_tokens, 1)})
+    for (const int64_t max_new : form_tops(d, std::max<int64_t>(max_tokens, 1))) {
+        const size_t units = (size_t)max_units(std::min<int64_t>(max_tokens, max_new * max_requests), max_requests);
         need = std::max(need, std::min(units * form_of(d, max_new, max_len).unit_bytes, kWsTarget));
+    }
     return std::max(kWsSlack + need, gdn_kv_attention_workspace_min(d, max_len));
 }
 

@@ -125,7 +125,7 @@ struct PromptPlan {
                               kInfo = kQT ? 6 * kBlk : kV + NS * kBlk;
     __host__ __device__ static constexpr uint32_t key_slot(uint32_t i) { return kK + (kQT && i == 2 ? 4 : i) * kBlk; }
     __host__ __device__ static constexpr uint32_t val_slot(uint32_t i) { return kV + (kQT && i == 2 ? 3 : i) * kBlk; }
-    static constexpr int kMaxBlocks = 64 + 4;                // 8-bit blocks of a segment and raw blocks of a span
+    static constexpr int kMaxBlocks = kKvMaxSegBlocks + 4;                // 8-bit blocks of a segment and raw blocks of a span
     static constexpr uint32_t kRow = kInfo + kMaxBlocks * 16;        // float2 [R]: what takes Q's scaling out, 1152 sum(Q)
     static constexpr uint32_t kRawK = kRow + R * 8;                  // float [4][64]: the scalings of the raw blocks' keys
     static constexpr uint32_t kBar = kRawK + 4 * 64 * 4;
@@ -144,7 +144,7 @@ struct PromptPlan {
     // Registers: an SM partition's 512 per lane hold 5 of the 20 warps (two tiles) at 96, or 6 of the 24 (one tile) at 80.
     // Then the issuing, key and value warps go down to 64 and the softmax warps up to 144: per partition
     // 64 + 2 x 144 + 2 x 64 = 480 of 480 (two tiles), 64 + 144 + 4 x 64 = 464 of 480 (one tile).
-    static_assert(kBytes <= 227 * 1024, "shared memory");
+    static_assert(kBytes <= 227 * 1024 && R == kv_prompt_rows(D), "shared memory, rows of a CTA");
 };
 
 // A block of the pass: its page, c = scale log2(e) k_scale, log2 of the value scale in the exponent that m is the maximum
@@ -164,11 +164,13 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     grid_dep_wait();
     grid_dep_launch();
     // later units (longer contexts) first: a causal launch then ends on its short ones
-    const int ui = a.unit0 + n_units - 1 - (int)(blockIdx.x / row_tiles), rt = blockIdx.x % row_tiles, h = blockIdx.y, seg = blockIdx.z;
+    const int ui = a.unit0 + n_units - 1 - (int)(blockIdx.x / row_tiles), rt = blockIdx.x % row_tiles, h = blockIdx.y;
+    // and of growing segments the longer ones
+    const int seg = a.seg_blocks ? (int)blockIdx.z : a.n_seg - 1 - (int)blockIdx.z;
     const KvUnit u = kv_load_unit(a.units, ui);   // inside the map whatever the count
     const int unit1 = min(a.unit0 + n_units, a.counts[0]);
     if (ui >= unit1) return;
-    bool ok = kv_unit_ok(u, a.c, a.n_rows) && u.count <= a.max_new && u.block / a.seg_blocks < a.n_seg;
+    bool ok = kv_unit_ok(u, a.c, a.n_rows) && u.count <= a.max_new && kv_seg_of(a, u.block) < a.n_seg;
     // the span's first unit works for all of it
     if (ok && ui > a.unit0 && u.block % span != 0) {
         const KvUnit w = kv_load_unit(a.units, ui - 1);
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
         return;
     }
-    const int last_seg = u.block / a.seg_blocks;   // a span lies in one segment: span divides seg_blocks
+    const int last_seg = kv_seg_of(a, u.block);   // a span lies in one segment: span divides their starts
     const int n_row = n_tok * a.G, r0 = rt * P::R;
     if (r0 >= n_row || seg > last_seg) return;
 
@@ -204,8 +206,8 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     const int nt = rows_here > 128 ? 2 : 1;        // MMA tiles in use
     // blocks of this tile's rows, and the blocks of the pass: 8-bit [c0, c0 + n8), then raw from blo
     const int blo = (pos0 + r0 / a.G) / kKvBlock, bhi = (pos0 + (r0 + rows_here - 1) / a.G) / kKvBlock;
-    const int c0 = seg * a.seg_blocks;
-    const int n8 = min(bhi - c0, a.seg_blocks);
+    const int c0 = kv_seg_start(a, seg);
+    const int n8 = min(bhi, kv_seg_start(a, seg + 1)) - c0;
     const int nb = n8 + (seg == last_seg ? bhi - blo + 1 : 0);
 
     if (t == 0) {

@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttn a) {
     const int ui = a.unit0 + blockIdx.x;
     if (ui >= a.counts[0]) return;
     const KvUnit u = kv_load_unit(a.units, ui);
-    const int n_seg = u.block / a.seg_blocks + 1;
+    const int n_seg = kv_seg_of(a, u.block) + 1;
     if (!kv_unit_ok(u, a.c, a.n_rows) || u.count > a.max_new || n_seg > a.n_seg || n_seg == 1) return;
     constexpr int W = D == 64 ? 2 : 4, N = D / (32 * W);
     const int lane = threadIdx.x & 31;

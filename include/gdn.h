@@ -418,10 +418,12 @@ size_t gdn_kv_attention_workspace_min(const gdn_attn_desc *desc, int64_t max_len
  * size the launches; a unit outside them is left out and reported by
  * gdn_device_status). Rows of out that belong to no unit are untouched.
  * Softmax, sums and outputs are accumulated in fp32. With bf16 inputs the
- * weights enter the second product rounded to bf16; fp32 inputs run in fp32
- * throughout. Deterministic; a row's bits depend on the session and on whether
- * the call is of the few-row form (max_new * Hq / Hkv <= 16), not on the rest
- * of the batch. */
+ * weights of complete blocks enter the second product in fp16, scaled so that
+ * the largest stay in its range and unrounded in the sum; those of the row's
+ * own block as the sum of two bf16 numbers. fp32 inputs run in fp32
+ * throughout. Deterministic; a row's bits depend on the session, the
+ * description and min(max_new, n_rows), which choose the form and how its keys
+ * are cut into segments, not on the other requests. */
 gdn_status gdn_kv_attention(const gdn_attn_desc *desc, const gdn_kv_cache *cache, const gdn_kv_map *map,
                             const void *q, const void *k, const void *v, void *out, int64_t n_rows, int32_t max_new,
                             int64_t max_len, void *workspace, size_t workspace_bytes, gdn_stream_t stream);

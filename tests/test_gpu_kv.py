@@ -85,6 +85,43 @@ def test_a_row_does_not_depend_on_the_batch(cuda_device, dtype):
         assert torch.equal(alone, both[n2:])
 
 
+def test_segments_of_every_length(cuda_device):
+    """33,000 keys and as many rows as make each rule of the segments hold (32 blocks, 48, growing to 256, 128), through a
+    workspace of the smallest size; the first and last rows of each call."""
+    m = Model((16, 2), 64, BF, n_pages=580, n_slots=1, max_blocks=580, seed=12)
+    m.ws_bytes = gdn.gdn_kv_attention_workspace_min(m.desc, 580 * B)
+    m.step([0], [33000], check=False, max_len=580 * B)
+    for n in (40, 200, 700, 3000):
+        start = len(m.slots[0].k)
+        q, k, v = m.draw(n, 16, 3.0), m.draw(n, 2), m.draw(n, 2)
+        out = m.step([0], [n], check=False, data=(q, k, v), max_len=580 * B).double().cpu().numpy()
+        for a in (0, n - 2):
+            ref, bound = m.attention(0, start + a, q[a:a + 2].double().numpy())
+            assert (np.abs(out[a:a + 2] - ref) <= bound).all(), (n, a)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_a_long_context_does_not_depend_on_the_batch(cuda_device, d):
+    """As above past one segment: with the same max_new, the bits of a session alone."""
+    g = torch.Generator().manual_seed(6)
+    mk = lambda n, h: torch.randn((n, h, d), generator=g).to(torch.bfloat16)   # noqa: E731
+    a, b = (Model((8, 2), d, BF, n_pages=140, max_blocks=70) for _ in range(2))
+    for new in (3500, 20, 1):
+        mine, other = [mk(new, h) for h in (8, 2, 2)], [mk(new, h) for h in (8, 2, 2)]
+        alone = a.step([2], [new], check=False, data=mine)
+        both = b.step([4, 2], [new, new], check=False, data=[torch.cat([y, x]) for x, y in zip(mine, other)])
+        assert torch.equal(alone, both[new:])
+
+
+@pytest.mark.parametrize("heads,d,new", [((3, 1), 256, 105), ((4, 2), 64, 169), ((8, 2), 128, 1), ((32, 8), 128, 30)])
+def test_the_workspace_takes_one_launch(cuda_device, heads, d, new):
+    """The workspace of a batch's tokens, requests and longest context holds its partial results, whatever max_new."""
+    m = Model(heads, d, BF, max_blocks=600)
+    gdn.gdn_timing_begin(100)
+    m.step([0, 3, 4], [new] * 3, check=False, max_len=38000)
+    assert gdn.gdn_timing_end()["kv_attention"][1] == 1
+
+
 @pytest.mark.parametrize("few", [True, False], ids=["token", "prompt"])
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
 def test_unused_memory_is_not_read_into_results(cuda_device, dtype, few):
