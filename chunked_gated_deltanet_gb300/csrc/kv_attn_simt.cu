@@ -269,12 +269,14 @@ __global__ void __launch_bounds__(128) kv_attn_few_simt_kernel(const KvAttn a, i
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[x][j] = 0.f;
     }
-    const int b0 = seg * a.seg_blocks, b1 = min(u.block + 1, b0 + a.seg_blocks);
-    for (int b = b0 + warp; b < b1; b += 4) {
-        const bool raw = b == u.block;
+    // complete blocks, then 16 keys a warp of the rows' own, the first by the warp whose turn it is (one warp for all of them
+    // would be the longest part of a short context)
+    const int own0 = 16 * ((warp - u.block) & 3);
+    auto block_step = [&](auto raw_c, int b) {
+        constexpr bool raw = decltype(raw_c)::value;
         int64_t ph = 0;
         float c = a.scale_log2, vs = 1.f;
-        if (!raw) {
+        if constexpr (!raw) {
             int page = a.c.table[(int64_t)u.slot * a.c.max_blocks + b];
             if ((unsigned)page >= (unsigned)a.c.n_pages) {
                 if (lane == 0) atomicOr(a.err, kErrKvBounds);
@@ -290,10 +292,11 @@ __global__ void __launch_bounds__(128) kv_attn_few_simt_kernel(const KvAttn a, i
         for (int i = 0; i < 8; ++i) {
 #pragma unroll
             for (int x = 0; x < RT; ++x) s[x][i] = 0.f;
+            if (raw && 16 * (i / 2) != own0) continue;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 float f[16];
-                if (!raw) i8_to_f(__ldg(reinterpret_cast<const uint4 *>(kp + 8 * i * D + 64 * j)), f);
+                if constexpr (!raw) i8_to_f(__ldg(reinterpret_cast<const uint4 *>(kp + 8 * i * D + 64 * j)), f);
                 else ld_own16(own_row(a, u, 0, h, 8 * i + g, D), 64 * j + 16 * tq, f);
 #pragma unroll
                 for (int x = 0; x < RT; ++x)
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(128) kv_attn_few_simt_kernel(const KvAttn a, i
             for (int i = 0; i < 8; ++i) {
                 s[x][i] += __shfl_xor_sync(0xffffffffu, s[x][i], 1);
                 s[x][i] += __shfl_xor_sync(0xffffffffu, s[x][i], 2);
-                s[x][i] = 8 * i + g > limit ? -INFINITY : s[x][i] * c;
+                s[x][i] = 8 * i + g > limit || (raw && 16 * (i / 2) != own0) ? -INFINITY : s[x][i] * c;
                 mb = fmaxf(mb, s[x][i]);
             }
 #pragma unroll
@@ -338,10 +341,11 @@ __global__ void __launch_bounds__(128) kv_attn_few_simt_kernel(const KvAttn a, i
             for (int j = 0; j < 16; ++j) o[x][j] *= corr;
         }
         __syncwarp();
+        const int k1 = raw ? own0 + 16 : kKvBlock;
 #pragma unroll 4
-        for (int k = 0; k < kKvBlock; k += KPR) {
+        for (int k = raw ? own0 : 0; k < k1; k += KPR) {
             float f[16];
-            if (!raw) i8_to_f(__ldg(reinterpret_cast<const uint4 *>(vp + k * D)), f);
+            if constexpr (!raw) i8_to_f(__ldg(reinterpret_cast<const uint4 *>(vp + k * D)), f);
             else ld_own16(own_row(a, u, 1, h, k + vr, D), 16 * vc, f);
 #pragma unroll
             for (int x = 0; x < RT; ++x) {
@@ -351,7 +355,10 @@ __global__ void __launch_bounds__(128) kv_attn_few_simt_kernel(const KvAttn a, i
                 for (int j = 0; j < 16; ++j) o[x][j] = fmaf(p, f[j], o[x][j]);
             }
         }
-    }
+    };
+    const int b0 = seg * a.seg_blocks, b1 = min(u.block, b0 + a.seg_blocks);
+    for (int b = b0 + warp; b < b1; b += 4) block_step(std::false_type{}, b);
+    if (seg == last_seg && own0 < u.first + u.count) block_step(std::true_type{}, u.block);
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
 #pragma unroll

@@ -226,7 +226,10 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
         for (int y = 0; y < 2; ++y) qr[f][y] = sqr[8 * f + 2 * tq + y];
 
     float o[NO / 2][NT][4], m[NT][2], l[NT][2];   // o: columns g NO + 2 i (+ 1 in [2], [3]) of the lane's two rows
-    // the rows' own block, at the end of the last segment: as it came, 16 keys at a time
+    // the rows' own block, at the end of the last segment: as it came, 16 keys a warp, the first by the warp whose turn it is
+    // (one warp for all of them would be the longest part of a short context)
+    const int own0 = 16 * ((warp - u.block) & 3);
+    static_assert(kTokenWarps == 4, "16 keys each");
     auto own_block = [&] {
         bool odd_value = false;
         const bf *tail = static_cast<const bf *>(a.c.tail);
@@ -245,79 +248,76 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                 c[f][y] = a.scale_log2;
                 add[f][y] = 0.f;
             }
-        const int n_key = u.first + u.count;
+        const int k0 = own0;
+        float s[1][NT][4];
+#pragma unroll
+        for (int f = 0; f < NT; ++f)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[0][f][k] = 0.f;
+        const bf *key[2] = {raw_row(0, k0 + g), raw_row(0, k0 + 8 + g)};
 #pragma unroll 1
-        for (int k0 = 0; k0 < n_key; k0 += 16) {
-            float s[1][NT][4];
+        for (int j = 0; j < J; ++j) {
+            uint32_t w[2][8], qw[NT][8];
 #pragma unroll
-            for (int f = 0; f < NT; ++f)
+            for (int i = 0; i < 8; ++i) {
+                w[0][i] = w[1][i] = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) s[0][f][k] = 0.f;
-            const bf *key[2] = {raw_row(0, k0 + g), raw_row(0, k0 + 8 + g)};
-#pragma unroll 1
-            for (int j = 0; j < J; ++j) {
-                uint32_t w[2][8], qw[NT][8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    w[0][i] = w[1][i] = 0;
-#pragma unroll
-                    for (int f = 0; f < NT; ++f) qw[f][i] = 0;
-                }
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (key[x]) ld_words<8>(w[x], key[x] + 64 * j + 16 * tq);
-#pragma unroll
-                for (int f = 0; f < NT; ++f)
-                    if (g + 8 * f < n_row) ld_words<8>(qw[f], q_row(g + 8 * f) + 64 * j);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t ka[4] = {w[0][2 * k], w[1][2 * k], w[0][2 * k + 1], w[1][2 * k + 1]};
-#pragma unroll
-                    for (int f = 0; f < NT; ++f) {
-                        const uint32_t b[2] = {qw[f][2 * k], qw[f][2 * k + 1]};
-                        mma_bf16(s[0][f], ka, b);
-                    }
-                }
+                for (int f = 0; f < NT; ++f) qw[f][i] = 0;
             }
 #pragma unroll
-            for (int f = 0; f < NT; ++f)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k0 + g + 8 * (k >> 1) > u.first + (8 * f + 2 * tq + (k & 1)) / a.G) s[0][f][k] = -INFINITY;
-            token_softmax<1, NT, NO>(s, c, add, lraw, 1.f, m, l, o);
-            uint32_t ph[NT][2], pl[NT][2];   // weights of keys g and g + 8, rows 2 tq, 2 tq + 1; transposed
+            for (int x = 0; x < 2; ++x)
+                if (key[x]) ld_words<8>(w[x], key[x] + 64 * j + 16 * tq);
 #pragma unroll
             for (int f = 0; f < NT; ++f)
+                if (g + 8 * f < n_row) ld_words<8>(qw[f], q_row(g + 8 * f) + 64 * j);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    split_bf16x2(s[0][f][2 * x], s[0][f][2 * x + 1], ph[f][x], pl[f][x]);
-                    ph[f][x] = transpose8(ph[f][x]);
-                    pl[f][x] = transpose8(pl[f][x]);
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t ka[4] = {w[0][2 * k], w[1][2 * k], w[0][2 * k + 1], w[1][2 * k + 1]};
+#pragma unroll
+                for (int f = 0; f < NT; ++f) {
+                    const uint32_t b[2] = {qw[f][2 * k], qw[f][2 * k + 1]};
+                    mma_bf16(s[0][f], ka, b);
                 }
-            const bf *val[4];
+            }
+        }
 #pragma unroll
-            for (int y = 0; y < 4; ++y) val[y] = raw_row(1, k0 + 2 * tq + (y & 1) + 8 * (y >> 1));
+        for (int f = 0; f < NT; ++f)
 #pragma unroll
-            for (int i = 0; i < NO / 8; ++i) {   // eight columns of the four keys
-                uint32_t v[4][4];
+            for (int k = 0; k < 4; ++k)
+                if (k0 + g + 8 * (k >> 1) > u.first + (8 * f + 2 * tq + (k & 1)) / a.G) s[0][f][k] = -INFINITY;
+        token_softmax<1, NT, NO>(s, c, add, lraw, 1.f, m, l, o);
+        uint32_t ph[NT][2], pl[NT][2];   // weights of keys g and g + 8, rows 2 tq, 2 tq + 1; transposed
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (val[y]) x = __ldg(reinterpret_cast<const uint4 *>(val[y] + col(g, 8 * i)));
-                    // a value that is not finite would reach rows that do not see it (0 * inf): left out here, and
-                    // added by the rows that do at the end
-                    odd_value |= drop_not_finite(x);
-                    v[y][0] = x.x; v[y][1] = x.y; v[y][2] = x.z; v[y][3] = x.w;
-                }
+        for (int f = 0; f < NT; ++f)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t va[4] = {__byte_perm(v[0][k], v[1][k], 0x5410), __byte_perm(v[0][k], v[1][k], 0x7632),
-                                            __byte_perm(v[2][k], v[3][k], 0x5410), __byte_perm(v[2][k], v[3][k], 0x7632)};
+            for (int x = 0; x < 2; ++x) {
+                split_bf16x2(s[0][f][2 * x], s[0][f][2 * x + 1], ph[f][x], pl[f][x]);
+                ph[f][x] = transpose8(ph[f][x]);
+                pl[f][x] = transpose8(pl[f][x]);
+            }
+        const bf *val[4];
 #pragma unroll
-                    for (int f = 0; f < NT; ++f) {
-                        mma_bf16(o[4 * i + k][f], va, ph[f]);
-                        mma_bf16(o[4 * i + k][f], va, pl[f]);
-                    }
+        for (int y = 0; y < 4; ++y) val[y] = raw_row(1, k0 + 2 * tq + (y & 1) + 8 * (y >> 1));
+#pragma unroll
+        for (int i = 0; i < NO / 8; ++i) {   // eight columns of the four keys
+            uint32_t v[4][4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (val[y]) x = __ldg(reinterpret_cast<const uint4 *>(val[y] + col(g, 8 * i)));
+                // a value that is not finite would reach rows that do not see it (0 * inf): left out here, and
+                // added by the rows that do at the end
+                odd_value |= drop_not_finite(x);
+                v[y][0] = x.x; v[y][1] = x.y; v[y][2] = x.z; v[y][3] = x.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t va[4] = {__byte_perm(v[0][k], v[1][k], 0x5410), __byte_perm(v[0][k], v[1][k], 0x7632),
+                                        __byte_perm(v[2][k], v[3][k], 0x5410), __byte_perm(v[2][k], v[3][k], 0x7632)};
+#pragma unroll
+                for (int f = 0; f < NT; ++f) {
+                    mma_bf16(o[4 * i + k][f], va, ph[f]);
+                    mma_bf16(o[4 * i + k][f], va, pl[f]);
                 }
             }
         }
@@ -326,9 +326,9 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
             for (int f = 0; f < NT; ++f)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const int r = 8 * f + 2 * tq + y, n_see = r < n_row ? u.first + r / a.G + 1 : 0;
+                    const int r = 8 * f + 2 * tq + y, n_see = r < n_row ? min(k0 + 16, u.first + r / a.G + 1) : 0;
 #pragma unroll 1
-                    for (int k = 0; k < n_see; ++k) {
+                    for (int k = k0; k < n_see; ++k) {
                         const bf *src = raw_row(1, k);
 #pragma unroll
                         for (int i = 0; i < NO; ++i) {
@@ -339,35 +339,32 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                 }
         }
     };
-    // the warps' results of a segment, added in order (a warp without a block of it has none)
+    // the warps' results of a segment, added in order (a warp without a key of it has none: weight 0)
     auto merge = [&](int seg) {
-        const int n_warp = min(kTokenWarps, u.block - seg * a.seg_blocks + 1);
-        if (warp < n_warp) {
 #pragma unroll
-            for (int f = 0; f < NT; ++f)
+        for (int f = 0; f < NT; ++f)
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int r = 8 * f + 2 * tq + y;
-                    float *dst = so + (warp * R + r) * D;
+            for (int y = 0; y < 2; ++y) {
+                const int r = 8 * f + 2 * tq + y;
+                float *dst = so + (warp * R + r) * D;
 #pragma unroll
-                    for (int i = 0; i < NO / 2; i += 2)
-                        *reinterpret_cast<float4 *>(dst + col(g, 2 * i)) =
-                            make_float4(o[i][f][y], o[i][f][2 + y], o[i + 1][f][y], o[i + 1][f][2 + y]);
-                    float sum = l[f][y];
+                for (int i = 0; i < NO / 2; i += 2)
+                    *reinterpret_cast<float4 *>(dst + col(g, 2 * i)) =
+                        make_float4(o[i][f][y], o[i][f][2 + y], o[i + 1][f][y], o[i + 1][f][2 + y]);
+                float sum = l[f][y];
 #pragma unroll
-                    for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-                    if (g == 0) sml[warp * R + r] = make_float2(m[f][y], sum);
-                }
-        }
+                for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+                if (g == 0) sml[warp * R + r] = make_float2(m[f][y], sum);
+            }
         __syncthreads();
         for (int e = t; e < n_row * (D / 4); e += 32 * kTokenWarps) {
             const int r = e / (D / 4), col = (e % (D / 4)) * 4;
             float M = -INFINITY;
-            for (int w = 0; w < n_warp; ++w) M = fmaxf(M, sml[w * R + r].x);
+            for (int w = 0; w < kTokenWarps; ++w) M = fmaxf(M, sml[w * R + r].x);
             const float base = M == -INFINITY ? 0.f : M;
             float L = 0.f;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = 0; w < n_warp; ++w) {
+            for (int w = 0; w < kTokenWarps; ++w) {
                 const float2 ml = sml[w * R + r];
                 const float f = ex2(ml.x - base);
                 const float4 y = *reinterpret_cast<const float4 *>(so + (w * R + r) * D + col);
@@ -483,7 +480,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
         }
         // nothing is loaded ahead past the last segment (told apart here, so that no register is kept for it)
         if (seg == last_seg) {
-            if (blk == u.block) own_block();
+            if (own0 < u.first + u.count) own_block();
             merge(seg);
             return;
         }

@@ -85,6 +85,31 @@ def test_a_row_does_not_depend_on_the_batch(cuda_device, dtype):
         assert torch.equal(alone, both[n2:])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_values_that_are_not_finite_in_every_part_of_the_block(cuda_device, dtype):
+    """Few rows: infinities and NaN among the own block's values reach the rows that see them, once each, and no other."""
+    m = Model((4, 2), 128, dtype)
+    n = 63
+    q, k, v = m.draw(n, 4), m.draw(n, 2), m.draw(n, 2)
+    clean = v.clone()
+    for key, col, x in ((3, 5, "inf"), (20, 5, "inf"), (37, 5, "inf"), (50, 9, "-inf"), (21, 7, "nan"), (60, 70, "inf"), (62, 100, "inf")):
+        v[key, 0, col], clean[key, 0, col] = float(x), 0.0
+    m.step([1], [61], check=False, data=(q[:61], k[:61], clean[:61]))
+    m.step([0], [61], check=False, data=(q[:61], k[:61], v[:61]))
+    out = m.step([0], [2], check=False, data=(q[61:], k[61:], v[61:])).double().cpu().numpy()
+    m.slots[1].k += [x.float().numpy() for x in k[61:]]
+    m.slots[1].v += [x.float().numpy() for x in clean[61:]]
+    ref, bound = m.attention(1, 61, q[61:].double().numpy())
+    for row in range(2):
+        want = {5: np.inf, 9: -np.inf, 7: np.nan, 70: np.inf, **({100: np.inf} if row else {})}
+        for h in range(4):
+            for c in range(128):
+                if h < 2 and c in want:
+                    assert np.array_equal(out[row, h, c], want[c], equal_nan=True), (row, h, c)
+                else:
+                    assert abs(out[row, h, c] - ref[row, h, c]) <= bound[row, h, c], (row, h, c)
+
+
 def test_segments_of_every_length(cuda_device):
     """33,000 keys and as many rows as make each rule of the segments hold (32 blocks, 48, growing to 256, 128), through a
     workspace of the smallest size; the first and last rows of each call."""
