@@ -14,20 +14,6 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// 4 int8 -> 4 bf16, exact: with a byte b under the upper byte 0x43 a bf16 reads 128 + (b & 127) once bit 7 (which is the
-// exponent's lowest) is cleared, and 128 or 256 from bit 7 alone; their difference is the signed value.
-__device__ __forceinline__ uint2 i8_to_bf16x4(uint32_t x) {
-    uint2 o;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t w = __byte_perm(x, 0x43434343u, i == 0 ? 0x4140 : 0x4342);
-        const uint32_t a = w & 0xFF7FFF7Fu, b = w & 0xFF80FF80u;
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
-        (i == 0 ? o.x : o.y) = *reinterpret_cast<const uint32_t *>(&d);
-    }
-    return o;
-}
-
 // 4 int8 -> 4 fp16, exact: 0x6400 | (b ^ 0x80) reads 1152 + b. Centred: b; otherwise 1152 + b.
 template <bool kCentred = true>
 __device__ __forceinline__ uint2 i8_to_f16x4(uint32_t x) {

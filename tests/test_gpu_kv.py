@@ -352,3 +352,15 @@ def test_many_sessions_share_the_gpu(cuda_device):
     assert torch.isfinite(out).all()
     for i in (0, 1, 39):
         assert torch.equal(run(one, [i], [1], *(t[i:i + 1].contiguous() for t in (q, k, v)), 5000)[0], out[i])
+
+
+def test_the_example_serves_a_conversation(cuda_device):
+    """The hybrid block of examples/: prompt turns, a fork and graph replays equal to eager steps."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "examples", "hybrid_session.py")
+    spec = importlib.util.spec_from_file_location("hybrid_session", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    diff, _ = example.run(turn=192, branches=3, steps=70, device=cuda_device)
+    assert diff == 0.0
