@@ -60,6 +60,7 @@ __host__ __device__ __forceinline__ int64_t kv_tail_offset(int slot, int buf, in
 // long contexts want long ones, and short contexts short ones, to have CTAs for all SMs. Cut at absolute positions.
 constexpr int kKvMaxSegBlocks = 256;
 constexpr int kv_prompt_rows(int d) { return d == 256 ? 128 : 256; }   // rows of a CTA of that form
+constexpr int kKvSimtRows = 64;                                        // and of its fp32 form
 __host__ __device__ constexpr int kv_grown_seg(int block) {
     return block < 64 ? block / 32 : block < 128 ? 2 : block < 512 ? 2 + block / 128 : 4 + block / 256;
 }

@@ -64,23 +64,24 @@ gdn::KvCache device_cache(const gdn_kv_cache *c) {
 // Units of a batch: a request of n tokens touches at most (n + 62) / 64 + 1 blocks, and at most n.
 int64_t max_units(int64_t tokens, int32_t requests) { return std::min<int64_t>(tokens, tokens / kKvBlock + 2LL * requests); }
 
-// Key segments of a row's attention, in blocks, cut at absolute positions. Few rows: 512 keys for up to three key/value
-// heads, so that one token's long context fills the GPU, up to 4,096 for more heads, which fill it with longer ones. fp32:
-// 512, where 64 rows of one head take about 3 us a block. Many rows in bf16: by the CTAs of one request and segment. Up to
-// 31, short segments fill the SMs; up to 159, growing ones (0, kv_grown_start's); more fill them alone. Against 64
-// blocks throughout (us): 165 x 12 rows of 6 sessions over 18,107 keys 60 -> 37, 290 x 16 rows over 41,802 240 -> 220,
-// 4,000 x 16 over 37,802 1,164 -> 1,075; and 180 x 16 rows of 16 sessions over 12,000, which fill the GPU together,
-// 193 -> 198. A rule on the description and max_new: a row's segments do not depend on the batch.
-int many_ctas(const gdn_attn_desc *d, int64_t max_new) {
-    const int rows = gdn::kv_prompt_rows(d->head_dim), G = d->n_q_heads / d->n_kv_heads;
-    return (int)std::min<int64_t>((max_new * G + rows - 1) / rows * d->n_kv_heads, INT32_MAX);
-}
-constexpr int kManySteps[] = {8, 32, 160}, kManySegs[] = {32, 48, 0, 128};
+// Key segments of a row's attention, in blocks, cut at absolute positions. Few rows: 512 keys for fp32 and for up to three
+// key/value heads, so that one token's long context fills the GPU, up to 4,096 for more heads, which fill it with longer
+// ones. Many rows: by the CTAs of one request and segment. Up to 31, short segments fill the SMs; up to 159, growing ones
+// (0, kv_grown_start's); more fill them alone. Against 64 blocks throughout (us): 165 x 12 rows of 6 sessions over 18,107
+// keys 60 -> 37, 290 x 16 rows over 41,802 240 -> 220, 4,000 x 16 over 37,802 1,164 -> 1,075; and 180 x 16 rows of 16
+// sessions over 12,000, which fill the GPU together, 193 -> 198. In fp32, where 64 rows of one head take about 3 us a block:
+// 256 keys up to 159 CTAs, then 512 (against 512 throughout: a prompt of 2,048 x 2 rows 77 -> 47, 2 of 644 x 8 over 2,825
+// even; 2 of 2,099 x 32, which fill the SMs, lose 5 % with 256).
+// A rule on the description and max_new: a row's segments do not depend on the batch.
+int many_rows(const gdn_attn_desc *d) { return d->in_dtype == GDN_FP32 ? gdn::kKvSimtRows : gdn::kv_prompt_rows(d->head_dim); }
+constexpr int kManySteps[] = {8, 32, 160}, kManySegs[] = {32, 48, 0, 128}, kManySegsFp32[] = {4, 4, 4, 8};
 int seg_blocks(const gdn_attn_desc *d, bool few, int64_t max_new) {
-    if (d->in_dtype == GDN_FP32) return 8;
-    if (few) return d->n_kv_heads < 4 ? 8 : d->n_kv_heads < 8 ? 16 : d->n_kv_heads < 16 ? 32 : 64;
-    const int n = many_ctas(d, max_new);
-    return kManySegs[n < kManySteps[0] ? 0 : n < kManySteps[1] ? 1 : n < kManySteps[2] ? 2 : 3];
+    const bool fp32 = d->in_dtype == GDN_FP32;
+    if (few) return fp32 || d->n_kv_heads < 4 ? 8 : d->n_kv_heads < 8 ? 16 : d->n_kv_heads < 16 ? 32 : 64;
+    const int rows = many_rows(d), G = d->n_q_heads / d->n_kv_heads;   // rows of a CTA
+    const int64_t ctas = (max_new * G + rows - 1) / rows * d->n_kv_heads;
+    const int i = ctas < kManySteps[0] ? 0 : ctas < kManySteps[1] ? 1 : ctas < kManySteps[2] ? 2 : 3;
+    return fp32 ? kManySegsFp32[i] : kManySegs[i];
 }
 constexpr int kFewRows = 16;   // rows (new tokens of a block x query heads per key/value head) of the few-row form
 
@@ -104,7 +105,7 @@ Form form_of(const gdn_attn_desc *d, int64_t max_new, int64_t max_len) {
 }
 // The largest max_new of each of these forms, none above `most`: a form's partial results are the largest there.
 std::array<int64_t, 5> form_tops(const gdn_attn_desc *d, int64_t most) {
-    const int G = d->n_q_heads / d->n_kv_heads, rows = gdn::kv_prompt_rows(d->head_dim);
+    const int G = d->n_q_heads / d->n_kv_heads, rows = many_rows(d);
     std::array<int64_t, 5> tops = {kFewRows / G, most};
     for (int i = 0; i < 3; ++i) tops[2 + i] = (int64_t)((kManySteps[i] - 1) / d->n_kv_heads) * rows / G;
     for (int64_t &n : tops) n = std::min(std::max<int64_t>(n, 1), most);

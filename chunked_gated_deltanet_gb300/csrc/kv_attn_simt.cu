@@ -71,7 +71,7 @@ __device__ __forceinline__ void load_own(float *dst, const KvAttn &a, const KvUn
 // and D / 16 columns of the output. Bound: fp32 FMA issue and the shared-memory reads beside it (a 64 x 64 x d step).
 template <int D>
 struct SimtPlan {
-    static constexpr int R = 64, LD = D + 4, PLD = kKvBlock + 4;   // 16-byte rows that start 4 banks apart
+    static constexpr int R = kKvSimtRows, LD = D + 4, PLD = kKvBlock + 4;   // 16-byte rows that start 4 banks apart
     static constexpr size_t kBytes = (size_t)(R * LD + kKvBlock * LD + R * PLD) * sizeof(float);
 };
 
