@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttn a) {
 
 // The same for the few-row form, whose rows have many segments: a CTA per (token, query head), warp w taking segments
 // w, w + 8, ... and the eight sums added in order.
-template <typename InT, int D>
+template <typename InT, int D, int B>
 __global__ void __launch_bounds__(256) kv_join_few_kernel(const KvAttn a) {
     grid_dep_wait();
     grid_dep_launch();
@@ -462,7 +462,29 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(const KvAttn a) {
     __shared__ float so[8][D], sl[8];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int64_t stride = a.part_rows, pr = kv_part_row(a, ui, 0, 0, 0) + r;
+    // B of the warp's segments at a time, the first before the maximum is known: one latency for all of them
+    float2 ml[B];
+    float v[B][N][W];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int s = s0 + 8 * i;
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (s < n_seg) ml[i] = a.part_ml[s * stride + pr];
+            const float *src = a.part_o + (s * stride + pr) * D;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+#pragma unroll
+                for (int k = 0; k < W; ++k) v[i][j][k] = 0.f;
+                if (s >= n_seg) continue;
+                if constexpr (W == 4) *reinterpret_cast<float4 *>(v[i][j]) = *reinterpret_cast<const float4 *>(src + W * (lane + 32 * j));
+                else *reinterpret_cast<float2 *>(v[i][j]) = *reinterpret_cast<const float2 *>(src + W * (lane + 32 * j));
+            }
+        }
+    };
+    load(warp);
     float M = -INFINITY;
+#pragma unroll 4
     for (int s = lane; s < n_seg; s += 32) M = fmaxf(M, a.part_ml[s * stride + pr].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -472,19 +494,17 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(const KvAttn a) {
     for (int j = 0; j < N; ++j)
 #pragma unroll
         for (int k = 0; k < W; ++k) o[j][k] = 0.f;
-#pragma unroll 4
-    for (int s = warp; s < n_seg; s += 8) {
-        const float2 ml = a.part_ml[s * stride + pr];
-        const float f = exp2f(ml.x - base);
-        l = fmaf(f, ml.y, l);
-        const float *src = a.part_o + (s * stride + pr) * D;
+#pragma unroll 1
+    for (int s0 = warp; s0 < n_seg; s0 += 8 * B) {
+        if (s0 != warp) load(s0);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            float v[W];
-            if constexpr (W == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(src + W * (lane + 32 * j));
-            else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src + W * (lane + 32 * j));
+        for (int i = 0; i < B; ++i) {
+            const float f = exp2f(ml[i].x - base);   // 0 for a segment that is not there
+            l = fmaf(f, ml[i].y, l);
 #pragma unroll
-            for (int k = 0; k < W; ++k) o[j][k] = fmaf(f, v[k], o[j][k]);
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int k = 0; k < W; ++k) o[j][k] = fmaf(f, v[i][j][k], o[j][k]);
         }
     }
 #pragma unroll
@@ -529,7 +549,11 @@ template <typename InT, int D>
 cudaError_t launch_join(const KvAttn &a, int unit_bound, int few, cudaStream_t st) {
     const int per_unit = a.tok_stride * a.Hq;
     if (few) {
-        const cudaError_t e = gdn_launch_pdl(kv_join_few_kernel<InT, D>, dim3((unsigned)unit_bound, (unsigned)per_unit), 256, 0, st, a);
+// loads under way against CTAs on an SM, with the attention: 82 segments of 16 rows, d = 256, 23.3 us with eight and
+        // 24.7 with two; 8 segments of 2,048 rows, d = 128, 112.9 and 109.8
+        const dim3 grid((unsigned)unit_bound, (unsigned)per_unit);
+        const cudaError_t e = a.n_seg > 32 ? gdn_launch_pdl(kv_join_few_kernel<InT, D, 8>, grid, 256, 0, st, a)
+                                           : gdn_launch_pdl(kv_join_few_kernel<InT, D, 2>, grid, 256, 0, st, a);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     const dim3 grid((unsigned)unit_bound, (unsigned)std::min((per_unit + 7) / 8, 64));
