@@ -549,7 +549,7 @@ template <typename InT, int D>
 cudaError_t launch_join(const KvAttn &a, int unit_bound, int few, cudaStream_t st) {
     const int per_unit = a.tok_stride * a.Hq;
     if (few) {
-// loads under way against CTAs on an SM, with the attention: 82 segments of 16 rows, d = 256, 23.3 us with eight and
+        // loads under way against CTAs on an SM, with the attention: 82 segments of 16 rows, d = 256, 23.3 us with eight and
         // 24.7 with two; 8 segments of 2,048 rows, d = 128, 112.9 and 109.8
         const dim3 grid((unsigned)unit_bound, (unsigned)per_unit);
         const cudaError_t e = a.n_seg > 32 ? gdn_launch_pdl(kv_join_few_kernel<InT, D, 8>, grid, 256, 0, st, a)

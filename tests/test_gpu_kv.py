@@ -354,6 +354,18 @@ def test_many_sessions_share_the_gpu(cuda_device):
         assert torch.equal(run(one, [i], [1], *(t[i:i + 1].contiguous() for t in (q, k, v)), 5000)[0], out[i])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_pages_past_two_gigabytes(cuda_device, dtype):
+    """A pool of more than 2^31 bytes of keys whose last pages are handed out first: append, prompt and single tokens."""
+    n_pages = 2 ** 31 // (8 * 64 * 256) + 40
+    m = Model((8, 8), 256, dtype, n_pages=n_pages, n_slots=2, max_blocks=16)
+    m.cache.free.copy_(torch.arange(n_pages, dtype=torch.int32, device=cuda_device))
+    m.step([1, 0], [130, 70])
+    m.step([0, 1], [1, 1])
+    m.step([1], [70])
+    assert int(m.cache.table[1, 0]) * 8 * 64 * 256 > 2 ** 31
+
+
 def test_the_example_serves_a_conversation(cuda_device):
     """The hybrid block of examples/: prompt turns, a fork and graph replays equal to eager steps."""
     import importlib.util
