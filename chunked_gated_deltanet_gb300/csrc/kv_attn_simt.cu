@@ -10,6 +10,7 @@
 #include "kv.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gdn {
 
@@ -37,14 +38,19 @@ template <typename T> __device__ __forceinline__ T from_f(float x);
 template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// 64 rows of an 8-bit page as floats into shared memory (row stride LD); page values are exact in fp32.
+// 64 rows of an 8-bit page from global memory, and as floats into shared memory (row stride LD; exact).
+template <int D>
+__device__ __forceinline__ void load_page(uint4 (&w)[D / 64], const int8_t *src) {
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(src) + threadIdx.x + 256 * i);
+}
 template <int D, int LD>
-__device__ __forceinline__ void load_page(float *dst, const int8_t *src) {
+__device__ __forceinline__ void store_page(float *dst, const uint4 (&w)[D / 64]) {
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
         const int e = threadIdx.x + 256 * i, r = e / (D / 16), c = (e % (D / 16)) * 16;
         float f[16];
-        i8_to_f(*reinterpret_cast<const uint4 *>(src + r * D + c), f);
+        i8_to_f(w[i], f);
 #pragma unroll
         for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4 *>(dst + r * LD + c + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
     }
@@ -68,8 +74,9 @@ __device__ __forceinline__ void load_own(float *dst, const KvAttn &a, const KvUn
 }
 
 // Many rows: CTA (unit x tile of 64 rows, kv head, segment), 256 threads; thread (ty, tx) holds 4 rows, 4 keys of the scores
-// and D / 16 columns of the output. Bound: fp32 FMA issue and the shared-memory reads beside it (a 64 x 64 x d step). A
-// prompt of 2,048 tokens, 2 heads of 64: 47 us with the join, 23 TFLOP/s.
+// and D / 16 columns of the output. Bound: the shared-memory reads (eight 16-byte
+// ones beside 64 FMAs of a 4 x 4 tile), which halve the FMA rate. A prompt of 2,048 tokens, 2 heads of 64: 46 us with the
+// join, 23 TFLOP/s.
 template <int D>
 struct SimtPlan {
     static constexpr int R = kKvSimtRows, LD = D + 4, PLD = kKvBlock + 4;   // 16-byte rows that start 4 banks apart
@@ -114,26 +121,9 @@ __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int r
 #pragma unroll
         for (int j = 0; j < CT; ++j) o[i][j] = 0.f;
     }
-    const int b0 = seg * a.seg_blocks, b1 = min(u.block, b0 + a.seg_blocks);
-    const int n_blk = b1 - b0 + (seg == last_seg ? 1 : 0);
-    for (int i = 0; i < n_blk; ++i) {
-        const bool raw = b0 + i == u.block;
-        int64_t ph = 0;
-        float ks = 1.f, vs = 1.f;
-        if (!raw) {
-            const int page = a.c.table[(int64_t)u.slot * a.c.max_blocks + b0 + i];
-            if ((unsigned)page >= (unsigned)a.c.n_pages) {
-                if (t == 0) atomicOr(a.err, kErrKvBounds);
-                continue;   // the same page number in every thread
-            }
-            ph = (int64_t)page * a.Hkv + h;
-            ks = a.c.k_scale[ph];
-            vs = a.c.v_scale[ph];
-        }
-        __syncthreads();   // the block before is done with KV and Pm (the first time: Q is written)
-        if (raw) load_own<D, LD>(KV, a, u, 0, h);
-        else load_page<D, LD>(KV, a.c.k + ph * kKvBlock * D);
-        __syncthreads();
+    // scores of the block in KV and their weights into Pm; then the block's values in KV
+    auto scores = [&](auto raw_c, float ks, float vs) {
+        constexpr bool raw = decltype(raw_c)::value;
         float s[4][4];
 #pragma unroll
         for (int x = 0; x < 4; ++x)
@@ -183,10 +173,9 @@ __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int r
 #pragma unroll
             for (int j = 0; j < CT; ++j) o[x][j] *= corr;
         }
-        __syncthreads();   // K is read, P is written
-        if (raw) load_own<D, LD>(KV, a, u, 1, h);
-        else load_page<D, LD>(KV, a.c.v + ph * kKvBlock * D);
-        __syncthreads();
+    };
+    auto values = [&](auto raw_c) {
+        constexpr bool raw = decltype(raw_c)::value;
         // a key that the mask took has weight zero; it adds nothing whatever its value (a NaN or an infinity after
         // the row's position does not reach the row)
 #pragma unroll 2
@@ -211,6 +200,48 @@ __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int r
                 }
             }
         }
+    };
+    const int b0 = seg * a.seg_blocks, b1 = min(u.block, b0 + a.seg_blocks);
+    const int32_t *table = a.c.table + (int64_t)u.slot * a.c.max_blocks;
+    // the head's part of block b's page, the page in bounds whatever the table holds (the result is reported as invalid then)
+    auto part_of = [&](int b) {
+        int page = table[b];
+        if ((unsigned)page >= (unsigned)a.c.n_pages) {
+            if (t == 0) atomicOr(a.err, kErrKvBounds);
+            page = 0;
+        }
+        return (int64_t)page * a.Hkv + h;
+    };
+    // keys are loaded a block ahead, values while the scores are computed
+    uint4 kw[D / 64], vw[D / 64];
+    int64_t ph = b0 < b1 ? part_of(b0) : 0;
+    if (b0 < b1) load_page<D>(kw, a.c.k + ph * kKvBlock * D);
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        const float ks = a.c.k_scale[ph], vs = a.c.v_scale[ph];
+        __syncthreads();   // the block before is done with KV and Pm (the first time: Q is written)
+        store_page<D, LD>(KV, kw);
+        load_page<D>(vw, a.c.v + ph * kKvBlock * D);
+        __syncthreads();
+        if (b + 1 < b1) {
+            ph = part_of(b + 1);
+            load_page<D>(kw, a.c.k + ph * kKvBlock * D);
+        }
+        scores(std::false_type{}, ks, vs);
+        __syncthreads();   // K is read, P is written
+        store_page<D, LD>(KV, vw);
+        __syncthreads();
+        values(std::false_type{});
+    }
+    if (seg == last_seg) {
+        __syncthreads();
+        load_own<D, LD>(KV, a, u, 0, h);
+        __syncthreads();
+        scores(std::true_type{}, 1.f, 1.f);
+        __syncthreads();
+        load_own<D, LD>(KV, a, u, 1, h);
+        __syncthreads();
+        values(std::true_type{});
     }
     // one segment: the result; several: the partial one (columns 4 tx + 64 j ..)
 #pragma unroll
