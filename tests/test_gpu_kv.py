@@ -110,6 +110,30 @@ def test_values_that_are_not_finite_in_every_part_of_the_block(cuda_device, dtyp
                     assert abs(out[row, h, c] - ref[row, h, c]) <= bound[row, h, c], (row, h, c)
 
 
+@pytest.mark.parametrize("n", [2, 200], ids=["few", "many"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_a_query_that_is_not_finite_keeps_to_its_row(cuda_device, dtype, n):
+    """NaN and infinities in some heads of a token's query: the other rows are as without them, zero and tiny ones too."""
+    m = Model((4, 2), 128, dtype)
+    m.step([1], [150], check=False)
+    q, k, v = m.draw(n, 4), m.draw(n, 2), m.draw(n, 2)
+    q[n - 1, 0, 3], q[0, 3, 0], q[0, 1, 127] = float("nan"), float("inf"), float("-inf")
+    q[0, 0], q[n - 1, 2] = 0.0, q[n - 1, 2] * 2.0 ** -100
+    out = m.step([1], [n], check=False, data=(q, k, v)).double().cpu().numpy()
+    bad = {(n - 1, 0), (0, 3), (0, 1)}
+    for t in (0, n - 1):
+        clean = q[t:t + 1].clone()
+        for row, head in bad:
+            if row == t:
+                clean[0, head] = 0.0
+        ref, bound = m.attention(1, 150 + t, clean.double().numpy())
+        for head in range(4):
+            if (t, head) in bad:
+                assert np.isnan(out[t, head]).all(), (t, head)
+            else:
+                assert (np.abs(out[t, head] - ref[0, head]) <= bound[0, head]).all(), (t, head)
+
+
 def test_segments_of_every_length(cuda_device):
     """33,000 keys and as many rows as make each rule of the segments hold (32 blocks, 48, growing to 256, 128), through a
     workspace of the smallest size; the first and last rows of each call."""
