@@ -385,8 +385,23 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         // loop unrolled by two, measured slower: the roles share one instruction cache) ----
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
         const bool is_v = t >= P::kVals0;
-        // pages and scales of the pass's blocks, which the softmax warps read as well
+        // load i of this warp: 8 keys x 64 columns, key group (cw + CW i) / kVec, column group (cw + CW i) % kVec
+        uint4 w[P::kLoads];
+        auto load_from = [&](const int8_t *src, int cw) {
+#pragma unroll
+            for (int i = 0; i < P::kLoads; ++i) {
+                const int j = cw + P::CW * i;
+                w[i] = __ldg(reinterpret_cast<const uint4 *>(src + j / P::kVec * (8 * D) + j % P::kVec * 64));
+            }
+        };
+        // pages and scales of the pass's blocks, which the softmax warps read as well; with d = 256 the first block's loads
+        // before them (2.5 % of 290 x 16 rows over 41,802 keys; the two-tile form has no registers left for that: 6 % slower)
         const int32_t *table = a.c.table + (int64_t)u.slot * a.c.max_blocks;
+        if (P::kQT && n8 > 0) {
+            int page = table[c0];
+            if ((unsigned)page >= (unsigned)a.c.n_pages) page = 0;
+            load_from((is_v ? a.c.v : a.c.k) + ((int64_t)page * a.Hkv + h) * (kKvBlock * D) + (lane >> 2) * D + (lane & 3) * 16, warp % P::CW);
+        }
         for (int i = t - P::kKeys0; i < nb; i += 64 * P::CW) {
             BlockInfo x = {0, a.scale_log2, 0.f, 1.f};
             if (i < n8) {
@@ -413,17 +428,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         const int8_t *pool = (is_v ? a.c.v : a.c.k) + (int64_t)h * (kKvBlock * D) + kr * D + ch * 16;
         const int64_t stride = (int64_t)a.Hkv * (kKvBlock * D);
         const uint32_t full = bar(is_v ? P::bVFull : P::bKFull), free = bar(is_v ? P::bVFree : P::bKFree);
-        // load i of this warp: 8 keys x 64 columns, key group (cw + CW i) / kVec, column group (cw + CW i) % kVec
-        uint4 w[P::kLoads];
-        auto load = [&](int n) {
-            n = min(n, nb - 1);   // a raw block: page 0, not used
-            const int8_t *src = pool + info[n].page * stride;
-#pragma unroll
-            for (int i = 0; i < P::kLoads; ++i) {
-                const int j = cw + P::CW * i;
-                w[i] = __ldg(reinterpret_cast<const uint4 *>(src + j / P::kVec * (8 * D) + j % P::kVec * 64));
-            }
-        };
+        auto load = [&](int n) { load_from(pool + info[min(n, nb - 1)].page * stride, cw); };   // a raw block: page 0, not used
         auto store = [&](auto vals, unsigned char *dst) {
             constexpr bool V = decltype(vals)::value;
 #pragma unroll
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 }
             }
         };
-        load(0);
+        if (!P::kQT) load(0);
 #pragma unroll 1
         for (int n = 0; n < nb; ++n) {
             const int slot = n % NS;
