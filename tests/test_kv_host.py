@@ -119,3 +119,21 @@ def test_binding_refuses_wrong_arrays():
             gdn.gdn_kv_append(d, cache, plan, k, v)
     with pytest.raises(ValueError):
         gdn.gdn_kv_plan(d, cache, torch.zeros(2, dtype=torch.int64), torch.zeros(2, dtype=torch.int32), plan)
+
+
+@pytest.mark.parametrize("dtype", [gdn.GDN_BF16, gdn.GDN_FP32])
+@pytest.mark.parametrize("heads,d", [((1, 1), 64), ((3, 1), 256), ((16, 2), 256), ((32, 8), 128), ((64, 64), 64), ((40, 1), 128)])
+def test_workspace_sizes_grow_with_every_bound(lib, heads, d, dtype):
+    """More tokens, requests or keys never need less, and the smallest workspace that works is never above the full one."""
+    desc = gdn.make_attn_desc(*heads, d, dtype)
+    tokens, requests, lengths = (1, 2, 17, 300, 5000, 70000), (1, 3, 64), (1, 64, 65, 513, 2049, 8193, 40000, 1000000)
+    size = {(t, r, n): gdn.gdn_kv_attention_workspace(desc, t, r, n) for t in tokens for r in requests for n in lengths}
+    low = [gdn.gdn_kv_attention_workspace_min(desc, n) for n in lengths]
+    assert all(v > 0 for v in size.values()) and low == sorted(low)
+    for axis, values in enumerate((tokens, requests, lengths)):
+        for key, v in size.items():
+            i = values.index(key[axis])
+            if i:
+                assert v >= size[key[:axis] + (values[i - 1],) + key[axis + 1:]], key
+    for (t, r, n), v in size.items():
+        assert v >= low[lengths.index(n)]
