@@ -671,9 +671,9 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                     *reinterpret_cast<float4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
                         make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 __syncwarp();
-#pragma unroll 1
-                for (int i = lane >> 3; i < 32; i += 4) {   // 4 rows of 8 chunks a time
-                    const int k = lane & 7;
+#pragma unroll 8
+                for (int it = 0; it < 8; ++it) {   // 4 rows of 8 chunks a time
+                    const int i = 4 * it + (lane >> 3), k = lane & 7;
                     const float4 x = *reinterpret_cast<const float4 *>(stage + i * 128 + ((k ^ (i & 7)) << 4));
                     const int64_t row = __shfl_sync(0xffffffffu, dst_row, i);
                     if (tr - lane + i >= rows_here) continue;
