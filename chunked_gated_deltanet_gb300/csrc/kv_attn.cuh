@@ -56,16 +56,33 @@ __device__ __forceinline__ bool drop_not_finite(uint4 &u) {
     return any;
 }
 
-// log2 of the value scale of block b of a slot. An all-zero block (any scale serves) counts with the nearest before it
-// that has one, `tries` blocks looked at in all.
-__device__ __forceinline__ float kv_log2_vscale(const KvAttn &a, const int32_t *table, int b, int h, int tries) {
-    for (; tries > 0 && b >= 0; --tries, --b) {
-        const int page = table[b];
-        if ((unsigned)page >= (unsigned)a.c.n_pages) break;
-        const float vs = a.c.v_scale[(int64_t)page * a.Hkv + h];
-        if (vs != 0.f) return log2f(vs);
+// ---- the unit of the summed values ----
+// The bf16 kernels sum 2^{x - m} v over a row's keys with the weights in fp16 and the int8 of a complete block as they
+// are, so its value scale vs has to sit in the weight: 2^{x + log2 vs - lref - m}, where what is summed is in units of
+// 2^lref. fp16 has few exponents, so the unit follows the scales: it moves to a block whose scale is further than
+// 2^kUnitSpan from it, and what was summed moves along. Inside the span (blocks of like values, the usual case) nothing
+// moves. A unit is a power of two, so a move is exact and leaves no trace in rows that do not see the block.
+constexpr float kUnitSpan = 4.f;
+
+// 2^e of a whole e in [-126, 127]
+__device__ __forceinline__ float pow2_of(float e) {
+    return __uint_as_float((uint32_t)(127 + (int)fminf(fmaxf(e, -126.f), 127.f)) << 23);
+}
+// log2 of a block's value scale; +inf of an all-zero block, whose values are at home in any unit
+__device__ __forceinline__ float kv_log2_scale(float vs) { return vs != 0.f ? log2f(vs) : INFINITY; }
+// That over the unit, which moves if it has to; `move` (1 before) becomes the power of two that the sums take along
+__device__ __forceinline__ float kv_unit(float lvs, float &lref, float &move) {
+    float dv = lvs - lref;
+    if (!(fabsf(dv) <= kUnitSpan)) {
+        dv = 0.f;
+        if (lvs != INFINITY) {
+            const float to = rintf(lvs);
+            move = pow2_of(lref - to);
+            lref = to;
+            dv = lvs - to;
+        }
     }
-    return 0.f;
+    return dv;
 }
 
 }  // namespace gdn

@@ -7,11 +7,11 @@
 //                 scores are then off by 1152 times the row's sum of Q, which the softmax's fma subtracts. A key of the
 //                 row's own block, which is read as it came, is scaled by a power of two like a row of Q.
 //   O += P V      128 rows x d, K = 64 keys: P in TMEM as the A operand, V in shared memory. An 8-bit block: V int8 -> fp16
-//                 (exact), P = 2^{c s + log2 vs - m} with the block's value scale vs in the weight and m the running
-//                 maximum of exactly that exponent, so P <= 2^14 whatever the scales, and fp16 rounds it by 2^-11 of its
-//                 size (2^-25 absolute below 2^-14, where a key adds next to nothing). The row's own block: V bf16, P in
+//                 (exact), P = 2^{c s + dv - m} with the block's value scale over the unit of O, 2^dv (kv_attn.cuh), in
+//                 the weight and m the running maximum of exactly that exponent, so P <= 2^14 whatever the scales, and
+//                 fp16 rounds it by 2^-11 of its size (2^-25 absolute below 2^-14). The row's own block: V bf16, P in
 //                 two bf16 products, its upper and lower 8 bits: a row with few keys has nothing to average a rounding
-//                 out. The sum l takes the unrounded weights, 2^{c s - m}.
+//                 out. The sum l takes the unrounded weights without the scale, 2^{c s - m}.
 //
 // CTA: one row tile of R = 256 rows (two MMA tiles of 128; d = 256: one tile) of one kv head, over one segment of keys.
 // Rows are the (token, query head of the group) pairs of a span: consecutive blocks of one request, aligned to `span`
@@ -151,13 +151,12 @@ struct PromptPlan {
     static_assert(kBytes <= 227 * 1024 && R == kv_prompt_rows(D), "shared memory, rows of a CTA");
 };
 
-// A block of the pass: its page, c = scale log2(e) k_scale, log2 of the value scale in the exponent that m is the maximum
-// of, and the factor of its weights in the sum (1 / v_scale). A raw block counts with the value scale of the block before
-// it (so that m compares like with like), but its weights are of the values themselves.
-struct BlockInfo {
+// A block of the pass: its page, c = scale log2(e) k_scale, and log2 of the value scale (kv_log2_scale; not of a raw block).
+struct __align__(16) BlockInfo {
     int page;
-    float c, lvs, ivs;
+    float c, lvs;
 };
+constexpr float kRawSpan = 16.f;   // how far a raw block's values, whose two-part weights have 8-bit exponents, may be from the unit 1
 
 
 template <int D>
@@ -403,7 +402,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             load_from((is_v ? a.c.v : a.c.k) + ((int64_t)page * a.Hkv + h) * (kKvBlock * D) + (lane >> 2) * D + (lane & 3) * 16, warp % P::CW);
         }
         for (int i = t - P::kKeys0; i < nb; i += 64 * P::CW) {
-            BlockInfo x = {0, a.scale_log2, 0.f, 1.f};
+            BlockInfo x = {0, a.scale_log2, 0.f};
             if (i < n8) {
                 x.page = table[c0 + i];
                 const bool in = (unsigned)x.page < (unsigned)a.c.n_pages;
@@ -414,10 +413,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 const int64_t ph = (int64_t)x.page * a.Hkv + h;
                 const float ks = a.c.k_scale[ph], vs = a.c.v_scale[ph];
                 x.c = in ? a.scale_log2 * ks : 0.f;
-                x.lvs = in && vs != 0.f ? log2f(vs) : kv_log2_vscale(a, table, c0 + i - 1, h, 8);
-                x.ivs = ex2(-x.lvs);
-            } else {
-                x.lvs = kv_log2_vscale(a, table, blo + i - n8 - 1, h, 9);
+                x.lvs = in ? kv_log2_scale(vs) : INFINITY;
             }
             info[i] = x;
         }
@@ -521,7 +517,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         const int pos = pos0 + r / a.G, blk = pos / kKvBlock, off = pos % kKvBlock;
         const uint32_t o_tm = tmem + lanes + P::kO + tile * D;
         const float2 rq = row_q[tr];
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, lref = 0.f;
         auto block_step = [&](auto is_raw, int n) {
             constexpr bool raw = decltype(is_raw)::value;
             const int b = 2 * tile + (n & 1);
@@ -558,12 +554,23 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[j + k], s[j + 4 + k]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[60 + k]);
-            const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, c1152 + x.lvs);
-            float f = 1.f;
+            // the block's values over the unit of O; a raw block's are their own, and the weights' power of two is exact
+            float f = 1.f, dv = 0.f, raw_up = 1.f;   // f: what O is rescaled by
+            if (raw) {
+                if (fabsf(lref) > kRawSpan) {
+                    f = pow2_of(lref);
+                    lref = 0.f;
+                }
+                raw_up = pow2_of(-lref);
+            } else {
+                dv = kv_unit(x.lvs, lref, f);
+            }
+            const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, c1152 + dv);
             if (see > 0 && top > m + kSlack) {    // also the row's first keys (m = -inf)
-                f = ex2(m - top);              // 0 then
+                const float g = ex2(m - top);  // 0 then
                 m = top;
-                l *= f;
+                l *= g;
+                f *= g;
             }
             // O is rescaled once the product that is under way on it is done (a row's first keys meet O = 0)
             if (n > 0 && __any_sync(0xffffffffu, f != 1.f)) {
@@ -587,10 +594,10 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 }
                 tmem_wait_st();
             }
-            // the weights (8-bit blocks: times the value scale, which the sum takes out again); none of a block that the
-            // row does not see
+            // the weights (8-bit blocks: times the value scale over the unit, which the sum takes out again); none of a block
+            // that the row does not see
             const uint64_t cc = f2_pack(c, c);
-            const float add = see == 0 ? -INFINITY : c1152 + ((raw ? 0.f : x.lvs) - (m == -INFINITY ? 0.f : m));
+            const float add = see == 0 ? -INFINITY : c1152 + (dv - (m == -INFINITY ? 0.f : m));
             const uint64_t bb = f2_pack(add, add);
             uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -604,7 +611,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                     p0 = ex2(p0);
                     p1 = ex2(p1);
                     sum[k & 1] = f2_add(sum[k & 1], f2_pack(p0, p1));
-                    if (raw) split_bf16x2(p0, p1, w[k], lo[k]);
+                    if (raw) split_bf16x2(p0 * raw_up, p1 * raw_up, w[k], lo[k]);
                     else w[k] = f2_to_h2(p0, p1);
                 }
                 tmem_st16(s_tm + 16 * j, w);
@@ -612,7 +619,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             }
             float s0, s1;
             f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
-            l = fmaf(s0 + s1, x.ivs, l);
+            l = fmaf(s0 + s1, ex2(-dv), l);
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(bar(P::bP + b));
@@ -630,7 +637,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             const bool live = tr < rows_here;
             const int head = h * a.G + r % a.G, tok = r / a.G;
             const bool one = last_seg == 0;
-            const float inv = one ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;   // no key: zero; NaN stays
+            const float inv = (one ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f) * pow2_of(lref);   // no key: zero; NaN stays
             int64_t pr = 0;
             if (live && !one) {
                 pr = kv_part_row(a, ui + blk - u.block, seg, blk == u.block ? tok : off, head);

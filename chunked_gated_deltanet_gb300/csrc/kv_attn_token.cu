@@ -1,7 +1,7 @@
 // Attention of few query rows (single tokens, short continuations) over the paged 8-bit key/value cache, bf16 inputs.
 //
 // The mathematics is that of kv_attn_prompt.cu (keys as 1152 + q in fp16 against rows scaled by a power of two, weights
-// with the value scale in the running exponent in fp16; the row's own block in two bf16 products), on warp-level MMAs: with
+// in fp16 with the value scale over the unit of the warp's O; the row's own block in two bf16 products), on warp-level MMAs: with
 // up to 16 rows the work is reading the cache, 2 d bytes a key and head against 4 d flops a row, and tcgen05's 128 rows
 // would be empty.
 //
@@ -71,11 +71,11 @@ __device__ __forceinline__ void ld_words(uint32_t *w, const void *p) {
     }
 }
 
-// Scores of 16 N keys -> weights: exponents c s + add (+ lmax for the maximum only), the running maximum and sum (of the
-// lane's keys; added over the lanes at the end), O rescaled.
+// Scores of 16 N keys -> weights: exponents c s + add, the running maximum and sum (of the lane's keys, without the value
+// scale, 1 / ivs; added over the lanes at the end), O rescaled.
 template <int N, int NT, int NO>
-__device__ __forceinline__ void token_softmax(float (&s)[N][NT][4], const float (&c)[NT][2], const float (&add)[NT][2], float lmax,
-                                              float ivs, float (&m)[NT][2], float (&l)[NT][2], float (&o)[NO / 2][NT][4]) {
+__device__ __forceinline__ void token_softmax(float (&s)[N][NT][4], const float (&c)[NT][2], const float (&add)[NT][2], float ivs,
+                                              float (&m)[NT][2], float (&l)[NT][2], float (&o)[NO / 2][NT][4]) {
 #pragma unroll
     for (int f = 0; f < NT; ++f) {
         float corr[2];
@@ -86,7 +86,7 @@ __device__ __forceinline__ void token_softmax(float (&s)[N][NT][4], const float 
             for (int x = 0; x < N; ++x) top = fmaxf(top, fmaxf(s[x][f][y], s[x][f][2 + y]));
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-            if (top > -INFINITY) top = fmaf(top, c[f][y], add[f][y] + lmax);
+            if (top > -INFINITY) top = fmaf(top, c[f][y], add[f][y]);
             const float mn = fmaxf(m[f][y], top), base = mn == -INFINITY ? 0.f : mn;
             corr[y] = ex2(m[f][y] - base);
             m[f][y] = mn;
@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
         for (int y = 0; y < 2; ++y) qr[f][y] = sqr[8 * f + 2 * tq + y];
 
     float o[NO / 2][NT][4], m[NT][2], l[NT][2];   // o: columns g NO + 2 i (+ 1 in [2], [3]) of the lane's two rows
+    float lref = 0.f;                             // O is in units of 2^lref
     // the rows' own block, at the end of the last segment: as it came, 16 keys a warp, the first by the warp whose turn it is
     // (one warp for all of them would be the longest part of a short context)
     const int own0 = 16 * ((warp - u.block) & 3);
@@ -240,7 +241,15 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                 return static_cast<const bf *>(kv ? a.v_new : a.k_new) + ((int64_t)(u.row + off - u.first) * a.Hkv + h) * D;
             return nullptr;
         };
-        const float lraw = kv_log2_vscale(a, table, u.block - 1, h, 9);
+        // these values are their own: the unit becomes 1
+        const float move = pow2_of(lref);
+        lref = 0.f;
+#pragma unroll
+        for (int i = 0; i < NO / 2; ++i)
+#pragma unroll
+            for (int f = 0; f < NT; ++f)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[i][f][k] *= move;
         float c[NT][2], add[NT][2];
 #pragma unroll
         for (int f = 0; f < NT; ++f)
@@ -286,7 +295,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (k0 + g + 8 * (k >> 1) > u.first + (8 * f + 2 * tq + (k & 1)) / a.G) s[0][f][k] = -INFINITY;
-        token_softmax<1, NT, NO>(s, c, add, lraw, 1.f, m, l, o);
+        token_softmax<1, NT, NO>(s, c, add, 1.f, m, l, o);
         uint32_t ph[NT][2], pl[NT][2];   // weights of keys g and g + 8, rows 2 tq, 2 tq + 1; transposed
 #pragma unroll
         for (int f = 0; f < NT; ++f)
@@ -342,6 +351,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
     };
     // the warps' results of a segment, added in order (a warp without a key of it has none: weight 0)
     auto merge = [&](int seg) {
+        const float unit = pow2_of(lref);
 #pragma unroll
         for (int f = 0; f < NT; ++f)
 #pragma unroll
@@ -351,7 +361,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
 #pragma unroll
                 for (int i = 0; i < NO / 2; i += 2)
                     *reinterpret_cast<float4 *>(dst + col(g, 2 * i)) =
-                        make_float4(o[i][f][y], o[i][f][2 + y], o[i + 1][f][y], o[i + 1][f][2 + y]);
+                        make_float4(o[i][f][y] * unit, o[i][f][2 + y] * unit, o[i + 1][f][y] * unit, o[i + 1][f][2 + y] * unit);
                 float sum = l[f][y];
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
@@ -389,6 +399,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
     };
 
     for (int seg = blockIdx.z;;) {
+        lref = 0.f;
 #pragma unroll
         for (int f = 0; f < NT; ++f) {
             m[f][0] = m[f][1] = -INFINITY;
@@ -404,14 +415,23 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
             const int next = page_of(blk + kTokenWarps < seg_end ? blk + kTokenWarps : next_seg * a.seg_blocks + warp);
             const int64_t ph = (int64_t)page * a.Hkv + h;
             const float ks = a.scale_log2 * a.c.k_scale[ph], vs = a.c.v_scale[ph];
-            const float lvs = vs != 0.f ? log2f(vs) : kv_log2_vscale(a, table, blk - 1, h, 8), ivs = ex2(-lvs);
+            float move = 1.f;
+            const float dv = kv_unit(kv_log2_scale(vs), lref, move), ivs = ex2(-dv);
+            if (move != 1.f) {
+#pragma unroll
+                for (int i = 0; i < NO / 2; ++i)
+#pragma unroll
+                    for (int f = 0; f < NT; ++f)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[i][f][k] *= move;
+            }
             float c[NT][2], add[NT][2];
 #pragma unroll
             for (int f = 0; f < NT; ++f)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     c[f][y] = ks * qr[f][y].x;
-                    add[f][y] = lvs - c[f][y] * qr[f][y].y;
+                    add[f][y] = dv - c[f][y] * qr[f][y].y;
                 }
 #pragma unroll 1
             for (int n = 0; n < NU; ++n) {
@@ -443,7 +463,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                     }
                 const int pn = n + 1 < NU ? page : next;
                 if (pn >= 0) load_k(pn, (n + 1) % NU);
-                token_softmax<NA, NT, NO>(s, c, add, 0.f, ivs, m, l, o);
+                token_softmax<NA, NT, NO>(s, c, add, ivs, m, l, o);
 #pragma unroll
                 for (int x = 0; x < NA; ++x) {
                     uint32_t pb[NT][2];

@@ -319,9 +319,11 @@ gdn_status gdn_gates(const gdn_layer_desc *desc, const float *a, const float *b,
  * and for values, with one fp32 scale per (page, head): scale = absmax / 127
  * over the block's 64 d elements, q = x / scale rounded to nearest even, value =
  * q * scale (all zero: scale 0). Keys and values are finite, and a block's
- * largest value is 0 or between 2^-90 and 2^90 (the bf16 attention keeps scales
- * in exponents); a NaN is held as 0 and an infinity as 127 times a scale taken
- * from the block's finite elements. The open block at a slot's end is kept in
+ * largest value is 0 or between 2^-90 and 2^90; the largest values of a
+ * session's blocks of one head, the open one among them, are within 2^80 of one
+ * another where they are not 0 (the bf16 attention sums them in fp32 over a unit
+ * that follows them); a NaN is held as 0 and an infinity as 127 times a scale
+ * taken from the block's finite elements. The open block at a slot's end is kept in
  * in_dtype as it came, in the slot's tail. A query at position p reads the
  * blocks before its own (p / 64) from 8 bits and its own block's positions
  * <= p as they came. So the pages' content and every row of the attention

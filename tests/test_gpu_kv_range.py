@@ -1,0 +1,104 @@
+"""Attention over the 8-bit cache where its values, weights or queries are of very unequal size, against the bounds of
+kv_bounds.py."""
+import pytest
+import torch
+
+from chunked_gated_deltanet_gb300 import gdn
+from kv_bounds import Bounded
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = gdn.GDN_BF16, gdn.GDN_FP32
+DTYPES = pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+FORMS = pytest.mark.parametrize("n", [2, 40], ids=["few", "many"])
+DIMS = pytest.mark.parametrize("d", [64, 128, 256])
+
+
+def fill(m, k, v):
+    """The keys and values of slot 0, without a look at the outputs."""
+    q = torch.zeros((k.shape[0], m.hq, m.d), dtype=k.dtype)
+    m.step([0], [k.shape[0]], check=False, data=(q, k, v))
+
+
+@FORMS
+@DIMS
+@pytest.mark.parametrize("zeros", [1, 12], ids=["one zero block", "twelve"])
+def test_small_values_after_blocks_of_zeros(cuda_device, d, n, zeros):
+    """A prefix whose values are all zero has no scale of its own to hold the others to."""
+    m = Bounded((8, 2), d, BF, seed=21)
+    a, b = 64 * zeros, 300
+    v = m.draw(a + b, 2, 1e-6)
+    v[:a] = 0
+    fill(m, m.draw(a + b, 2), v)
+    m.step([0], [n], q_size=2.0, data=(m.draw(n, 8, 2.0), m.draw(n, 2), m.draw(n, 2, 1e-6)))
+    m.check_contents()
+
+
+PATTERNS = {"grows": [0, 0, 1, 1, 1, 1], "falls": [1, 1, 0, 0, 0, 0], "alternates": [0, 1, 0, 1, 1, 0],
+            "one large": [0, 0, 0, 1, 0, 0], "last large": [0, 0, 0, 0, 0, 1], "last small": [1, 1, 1, 1, 1, 0]}
+
+
+@FORMS
+@DTYPES
+@pytest.mark.parametrize("ratio", [12, 20, 30, 80], ids=lambda r: f"2^{r}")
+@pytest.mark.parametrize("pattern", PATTERNS)
+def test_blocks_of_unequal_values(cuda_device, pattern, ratio, dtype, n):
+    """Values of blocks (and of the open block) that are 2^ratio apart, in one column of the large ones only, so that every
+    other column is the small ones' alone."""
+    m = Bounded((4, 2), 128, dtype, seed=22)
+    sizes = PATTERNS[pattern]
+    v = m.draw(320, 2)
+    for b, big in enumerate(sizes[:5]):
+        rows = v[64 * b:64 * b + 64]
+        if big:
+            keep = rows[:, :, 3].clone()
+            rows.zero_()
+            rows[:, :, 3] = keep * 2.0 ** ratio
+    fill(m, m.draw(320, 2), v)
+    own = m.draw(n, 2)
+    if sizes[5]:
+        own[:, :, 3] *= 2.0 ** ratio
+    m.step([0], [n], data=(m.draw(n, 4, 2.0), m.draw(n, 2), own))
+
+
+@FORMS
+@DIMS
+def test_an_own_block_far_from_the_cache(cuda_device, d, n):
+    """Values near the ends of the range: the cache's tiny and the open block's huge, and the other way round."""
+    for cached, own in ((1e-12, 1e12), (1e12, 1e-12)):
+        m = Bounded((8, 2), d, BF, seed=23)
+        fill(m, m.draw(200, 2), m.draw(200, 2, cached))
+        m.step([0], [n], data=(m.draw(n, 8, 2.0), m.draw(n, 2), m.draw(n, 2, own)))
+
+
+@DTYPES
+@pytest.mark.parametrize("heads", [(4, 4), (8, 1), (16, 1)], ids=lambda h: f"{h[0]}q{h[1]}kv")
+@DIMS
+def test_ordinary_rows_keep_the_stated_bounds(cuda_device, d, heads, dtype):
+    """Sharp and flat rows, prompts and single tokens, within the bounds of the arithmetic that the library states."""
+    m = Bounded(heads, d, dtype, seed=26)
+    m.step([0, 1], [200, 45], q_size=3.0)
+    m.step([0, 1], [1, 30], q_size=1.0)
+    m.step([1, 0], [1, 1], q_size=4.0)
+
+
+@pytest.mark.parametrize("heads", [(2, 2), (12, 2)], ids=lambda h: f"{h[0]}q{h[1]}kv")
+@DIMS
+def test_unequal_values_do_not_depend_on_the_split(cuda_device, d, heads):
+    """Rows of the many-row form are the same bits however the session was cut into calls, blocks of any size beside and
+    after theirs."""
+    g = torch.Generator().manual_seed(27)
+    n = 450
+    q, k, v = (torch.randn((n, h, d), generator=g).to(torch.bfloat16) for h in (heads[0], 2, 2))
+    for b, e in enumerate((0, 25, -10, 3, 40, -30, 0, 20)):
+        v[64 * b:64 * b + 64] *= 2.0 ** e
+    v[64:128, :, 1:] = 0
+    v[320:384] = 0
+    outs = []
+    for cuts in ([0, n], [0, 100, 200, n], [0, 64, 128, 150, 256, 300, n]):
+        m = Bounded(heads, d, BF)
+        outs.append(torch.cat([m.step([1], [b - a], check=False, data=(q[a:b], k[a:b], v[a:b]))
+                               for a, b in zip(cuts, cuts[1:])]))
+        m.check_contents()
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
