@@ -8,10 +8,12 @@
 //                 row's own block, which is read as it came, is scaled by a power of two like a row of Q.
 //   O += P V      128 rows x d, K = 64 keys: P in TMEM as the A operand, V in shared memory. An 8-bit block: V int8 -> fp16
 //                 (exact), P = 2^{c s + dv - m} with the block's value scale over the unit of O, 2^dv (kv_attn.cuh), in
-//                 the weight and m the running maximum of exactly that exponent, so P <= 2^14 whatever the scales, and
-//                 fp16 rounds it by 2^-11 of its size (2^-25 absolute below 2^-14). The row's own block: V bf16, P in
-//                 two bf16 products, its upper and lower 8 bits: a row with few keys has nothing to average a rounding
-//                 out. The sum l takes the unrounded weights without the scale, 2^{c s - m}.
+//                 the weight and m 4 below the running maximum of exactly that exponent, so P <= 2^15.5 whatever the
+//                 scales, and fp16 rounds it by 2^-11 of its size down to 2^-18 of the segment's largest (2^-25 absolute
+//                 below 2^-14): keys beside a first token that takes nearly all of the weight, and whose value is next to
+//                 nothing, keep their bits. The row's own block: V bf16, P in two bf16 products, its upper and lower 8
+//                 bits: a row with few keys has nothing to average a rounding out. The sum l takes the unrounded weights
+//                 without the scale, 2^{c s - m}.
 //
 // CTA: one row tile of R = 256 rows (two MMA tiles of 128; d = 256: one tile) of one kv head, over one segment of keys.
 // Rows are the (token, query head of the group) pairs of a span: consecutive blocks of one request, aligned to `span`
@@ -24,8 +26,10 @@
 // tensor core waited for each other, 5,600 against 2,560 cycles per 128 keys of the two tiles). The weights overwrite the
 // scores that they came from.
 //
-// The running maximum m only moves when a block exceeds it by 14 (log2 domain; fp16 ends at 2^16): O is rescaled (by the softmax warps, after
-// the product before it) only then. Every decision is a row's own and every block is one softmax step, so a row's bits do
+// m only moves when a block's weights would pass 2^15.5 (fp16 ends at 2^16): O is rescaled (by the softmax warps, after the
+// product before it) only then. Room above m spares moves, room below spares the small weights' bits: with 14 above (and m
+// at the maximum) the turn below took 1,066 us, with 11.5 1,094, with 8 1,137, most of the moves being those of sharp rows
+// after their first block. Every decision is a row's own and every block is one softmax step, so a row's bits do
 // not depend on the rows beside it.
 //
 // Bound: the softmax warps' issue slots and the tensor core about evenly, 1,700 to 1,850 cycles for a block of 64 keys and
@@ -104,7 +108,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-constexpr float kSlack = 14.f;   // how far a weight's exponent may pass the running maximum
+constexpr float kLift = 4.f;     // where a row's largest weight stands when m moves, log2
+constexpr float kSlack = 11.5f;  // and how much further it may go before m moves again
 
 template <int D>
 struct PromptPlan {
@@ -565,7 +570,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             } else {
                 dv = kv_unit(x.lvs, lref, f);
             }
-            const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, c1152 + dv);
+            const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, c1152 + (dv - kLift));
             if (see > 0 && top > m + kSlack) {    // also the row's first keys (m = -inf)
                 const float g = ex2(m - top);  // 0 then
                 m = top;

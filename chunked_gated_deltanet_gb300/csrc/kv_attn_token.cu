@@ -1,7 +1,7 @@
 // Attention of few query rows (single tokens, short continuations) over the paged 8-bit key/value cache, bf16 inputs.
 //
 // The mathematics is that of kv_attn_prompt.cu (keys as 1152 + q in fp16 against rows scaled by a power of two, weights
-// in fp16 with the value scale over the unit of the warp's O; the row's own block in two bf16 products), on warp-level MMAs: with
+// in fp16 with the value scale over the unit of the warp's O, the largest so far at 2^15; the row's own block in two bf16 products), on warp-level MMAs: with
 // up to 16 rows the work is reading the cache, 2 d bytes a key and head against 4 d flops a row, and tcgen05's 128 rows
 // would be empty.
 //
@@ -71,6 +71,8 @@ __device__ __forceinline__ void ld_words(uint32_t *w, const void *p) {
     }
 }
 
+constexpr float kTokenLift = 15.f;   // log2 of a row's largest weight: fp16 keeps the 11 bits of those down to 2^-29 of it
+
 // Scores of 16 N keys -> weights: exponents c s + add, the running maximum and sum (of the lane's keys, without the value
 // scale, 1 / ivs; added over the lanes at the end), O rescaled.
 template <int N, int NT, int NO>
@@ -86,7 +88,7 @@ __device__ __forceinline__ void token_softmax(float (&s)[N][NT][4], const float 
             for (int x = 0; x < N; ++x) top = fmaxf(top, fmaxf(s[x][f][y], s[x][f][2 + y]));
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-            if (top > -INFINITY) top = fmaf(top, c[f][y], add[f][y]);
+            if (top > -INFINITY) top = fmaf(top, c[f][y], add[f][y] - kTokenLift);
             const float mn = fmaxf(m[f][y], top), base = mn == -INFINITY ? 0.f : mn;
             corr[y] = ex2(m[f][y] - base);
             m[f][y] = mn;

@@ -423,9 +423,11 @@ size_t gdn_kv_attention_workspace_min(const gdn_attn_desc *desc, int64_t max_len
  * gdn_device_status). Rows of out that belong to no unit are untouched.
  * Softmax, sums and outputs are accumulated in fp32. With bf16 inputs the
  * weights of complete blocks enter the second product in fp16, scaled so that
- * the largest stay in its range and unrounded in the sum; those of the row's
- * own block as the sum of two bf16 numbers. fp32 inputs run in fp32
- * throughout. Deterministic; a row's bits depend on the session, the
+ * the largest stay in its range, and unrounded in the sum: 11 bits of those down
+ * to 2^-18 of the largest among their segment's keys, fewer of smaller ones (in
+ * a block whose values are up to 2^4 smaller than the unit they are summed in,
+ * that much sooner); those of the row's own block as the sum of two bf16
+ * numbers. fp32 inputs run in fp32 throughout. Deterministic; a row's bits depend on the session, the
  * description and min(max_new, n_rows), which choose the form and how its keys
  * are cut into segments, not on the other requests. */
 gdn_status gdn_kv_attention(const gdn_attn_desc *desc, const gdn_kv_cache *cache, const gdn_kv_map *map,

@@ -3,8 +3,10 @@
 With p the softmax weights of a row, v the values they sum, N their number:
   scores        sums of d fp32 products, scalings and exponentials: kv_ref.py's share of every weight, 2 share sum p |v|;
   complete      weights in fp16, half a unit in the last place 2^-11 of their size, and where they are small 2^-25 of a unit
-  blocks        that is 2^-7 of the row's largest weight or less; blocks whose value scales differ by up to 2^8 share the
-                unit, so that a small one's weights lose as much: sum of 2^-11 p |v| + 2^-32 min(spread, 2^8) max(p) |v|;
+  blocks        that is 2^-4 of the row's largest weight or less (few rows: 2^-15). These roundings are independent, and of N
+                they add up to about 2 sqrt(N) of one, an eighth of N from some 300 keys on: 2^-32 each; blocks whose value
+                scales differ by up to 2^8 share the unit, so that a small one's weights lose as much:
+                sum of 2^-11 p |v| + 2^-32 min(spread, 2^8) max(p) |v|;
   own block     weights in two bf16 numbers of 8 bits: 2^-16 sum p |v|;
   sums          fp32, a rounding per 8 products: N / 8 2^-24 sum p |v|;
   result        bf16, 8 bits: 2^-8 (|out| + all of these).

@@ -71,6 +71,24 @@ def test_an_own_block_far_from_the_cache(cuda_device, d, n):
         m.step([0], [n], data=(m.draw(n, 8, 2.0), m.draw(n, 2), m.draw(n, 2, own)))
 
 
+@FORMS
+@DIMS
+@pytest.mark.parametrize("lead", [6.0, 14.0], ids=["e^6", "e^14"])
+def test_a_first_token_that_takes_the_weight(cuda_device, d, n, lead):
+    """An attention sink: the first key has e^lead times the weight of the others and a value of zero, so that the output
+    is what the small weights sum to."""
+    m = Bounded((4, 1), d, BF, seed=24)
+    q = m.draw(n, 4, 0.3)
+    q[:, :, 0] = 1.0
+    k, v = m.draw(500, 1, 0.3), m.draw(500, 1)
+    k[:, :, 0] = 0.0
+    k[0] = 0.0
+    k[0, :, 0] = lead * d ** 0.5
+    v[0] = 0.0
+    fill(m, k, v)
+    m.step([0], [n], data=(q, m.draw(n, 1, 0.3), m.draw(n, 1)))
+
+
 @DTYPES
 @pytest.mark.parametrize("heads", [(4, 4), (8, 1), (16, 1)], ids=lambda h: f"{h[0]}q{h[1]}kv")
 @DIMS
