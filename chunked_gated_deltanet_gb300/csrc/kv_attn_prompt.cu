@@ -3,9 +3,8 @@
 // The mathematics is that of kv_attn_simt.cu; here the two products of a block of 64 keys are tcgen05 MMAs:
 //   S = Q K^T     128 rows x 64 keys, K = d, operands fp16 in shared memory. A row of Q is scaled by a power of two to a
 //                 largest element in [2^14, 2^15), which is exact (but for elements 2^-32 of the largest), and taken out
-//                 of the scores again. An int8 key q is fed as 1152 + q, the fp16 that a byte under 0x64 reads as: the
-//                 scores are then off by 1152 times the row's sum of Q, which the softmax's fma subtracts. A key of the
-//                 row's own block, which is read as it came, is scaled by a power of two like a row of Q.
+//                 of the scores again. An int8 key is exact in fp16. A key of the row's own block, which is read as it
+//                 came, is scaled by a power of two like a row of Q.
 //   O += P V      128 rows x d, K = 64 keys: P in TMEM as the A operand, V in shared memory. An 8-bit block: V int8 -> fp16
 //                 (exact), P = 2^{c s + dv - m} with the block's value scale over the unit of O, 2^dv (kv_attn.cuh), in
 //                 the weight and m 4 below the running maximum of exactly that exponent, so P <= 2^15.5 whatever the
@@ -135,8 +134,8 @@ struct PromptPlan {
     __host__ __device__ static constexpr uint32_t key_slot(uint32_t i) { return kK + (kQT && i == 2 ? 4 : i) * kBlk; }
     __host__ __device__ static constexpr uint32_t val_slot(uint32_t i) { return kV + (kQT && i == 2 ? 3 : i) * kBlk; }
     static constexpr int kMaxBlocks = kKvMaxSegBlocks + 4;                // 8-bit blocks of a segment and raw blocks of a span
-    static constexpr uint32_t kRow = kInfo + kMaxBlocks * 16;        // float2 [R]: what takes Q's scaling out, 1152 sum(Q)
-    static constexpr uint32_t kRawK = kRow + R * 8;                  // float [4][64]: the scalings of the raw blocks' keys
+    static constexpr uint32_t kRow = kInfo + kMaxBlocks * 16;        // float [R]: what takes Q's scaling out
+    static constexpr uint32_t kRawK = kRow + R * 4;                  // float [4][64]: the scalings of the raw blocks' keys
     static constexpr uint32_t kBar = kRawK + 4 * 64 * 4;
     // barriers: key and value slots full and free, scores and weights of (tile, buffer), a tile's product before its last,
     // all products, the queries and the blocks' scales, the
@@ -206,7 +205,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + P::kSlot);
     uint32_t *bad_v = reinterpret_cast<uint32_t *>(sm + P::kBad);
     BlockInfo *info = reinterpret_cast<BlockInfo *>(sm + P::kInfo);
-    float2 *row_q = reinterpret_cast<float2 *>(sm + P::kRow);
+    float *row_q = reinterpret_cast<float *>(sm + P::kRow);
     float *raw_k = reinterpret_cast<float *>(sm + P::kRawK);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int pos0 = u.block * kKvBlock + u.first;
@@ -267,21 +266,15 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
 #pragma unroll
                 for (int i = 0; i < NP; ++i) w[i] = make_uint4(0, 0, 0, 0);
             }
-            float f[8], top = 0.f, sum = 0.f;
+            float f[8], top = 0.f;
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 b8_to_f(w[i], f);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    top = fmaxf(top, fabsf(f[k]));
-                    sum += f[k];
-                }
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]));
             }
 #pragma unroll
-            for (int o = 2; o > 0; o >>= 1) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            }
+            for (int o = 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             float back;
             const float up = pow2_to_2_15(top, back);
             unsigned char *dst = sm + P::kQ + (r >> 7) * P::kTile + ((r & 127) >> 3) * (D * 16) + c * 128 + (r & 7) * 16;
@@ -292,7 +285,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 for (int k = 0; k < 8; ++k) f[k] *= up;
                 *reinterpret_cast<uint4 *>(dst + 512 * i) = f8_to_h8(f);
             }
-            if (c == 0) row_q[r] = make_float2(back, 1152.f * up * sum);
+            if (c == 0) row_q[r] = back;
         }
         if constexpr (P::kQT) {   // each softmax thread its row, from the slots into TMEM
             kv_named_barrier(3, P::kKeys0);
@@ -430,12 +423,11 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         const int64_t stride = (int64_t)a.Hkv * (kKvBlock * D);
         const uint32_t full = bar(is_v ? P::bVFull : P::bKFull), free = bar(is_v ? P::bVFree : P::bKFree);
         auto load = [&](int n) { load_from(pool + info[min(n, nb - 1)].page * stride, cw); };   // a raw block: page 0, not used
-        auto store = [&](auto vals, unsigned char *dst) {
-            constexpr bool V = decltype(vals)::value;
+        auto store = [&](unsigned char *dst) {
 #pragma unroll
             for (int i = 0; i < P::kLoads; ++i) {
                 const int j = cw + P::CW * i;
-                const uint2 x0 = i8_to_f16x4<V>(w[i].x), x1 = i8_to_f16x4<V>(w[i].y), x2 = i8_to_f16x4<V>(w[i].z), x3 = i8_to_f16x4<V>(w[i].w);
+                const uint2 x0 = i8_to_f16x4(w[i].x), x1 = i8_to_f16x4(w[i].y), x2 = i8_to_f16x4(w[i].z), x3 = i8_to_f16x4(w[i].w);
                 unsigned char *o = dst + j / P::kVec * P::kGroup + j % P::kVec * (8 * P::kCore);
                 *reinterpret_cast<uint4 *>(o) = make_uint4(x0.x, x0.y, x1.x, x1.y);
                 *reinterpret_cast<uint4 *>(o + P::kCore) = make_uint4(x2.x, x2.y, x3.x, x3.y);
@@ -503,8 +495,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             }
             unsigned char *dst = sm + (is_v ? P::val_slot(slot) : P::key_slot(slot)) + kr * 16 + ch * (2 * P::kCore);
             if (n < n8) {
-                if (is_v) store(std::true_type{}, dst);
-                else store(std::false_type{}, dst);
+                store(dst);
                 load(n + 1);
             } else {
                 store_raw(blo + n - n8, dst);
@@ -521,7 +512,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int pos = pos0 + r / a.G, blk = pos / kKvBlock, off = pos % kKvBlock;
         const uint32_t o_tm = tmem + lanes + P::kO + tile * D;
-        const float2 rq = row_q[tr];
+        const float rq = row_q[tr];
         float m = -INFINITY, l = 0.f, lref = 0.f;
         auto block_step = [&](auto is_raw, int n) {
             constexpr bool raw = decltype(is_raw)::value;
@@ -534,7 +525,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             const BlockInfo x = info[n];
             // keys of the block that the row sees: all or none of an 8-bit block, up to its own offset of its raw block
             const int see = raw ? (blk == blo + n - n8 ? off + 1 : 0) : (blk > c0 + n ? kKvBlock : 0);
-            const float c = x.c * rq.x, c1152 = raw ? 0.f : -c * rq.y;
+            const float c = x.c * rq;
             float s[64];
             {
                 uint32_t w[4][16];
@@ -570,7 +561,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             } else {
                 dv = kv_unit(x.lvs, lref, f);
             }
-            const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, c1152 + (dv - kLift));
+            const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, dv - kLift);
             if (see > 0 && top > m + kSlack) {    // also the row's first keys (m = -inf)
                 const float g = ex2(m - top);  // 0 then
                 m = top;
@@ -602,7 +593,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             // the weights (8-bit blocks: times the value scale over the unit, which the sum takes out again); none of a block
             // that the row does not see
             const uint64_t cc = f2_pack(c, c);
-            const float add = see == 0 ? -INFINITY : c1152 + (dv - (m == -INFINITY ? 0.f : m));
+            const float add = see == 0 ? -INFINITY : dv - (m == -INFINITY ? 0.f : m);
             const uint64_t bb = f2_pack(add, add);
             uint64_t sum[2] = {0, 0};
 #pragma unroll

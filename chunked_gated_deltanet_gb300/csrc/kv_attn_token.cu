@@ -1,6 +1,6 @@
 // Attention of few query rows (single tokens, short continuations) over the paged 8-bit key/value cache, bf16 inputs.
 //
-// The mathematics is that of kv_attn_prompt.cu (keys as 1152 + q in fp16 against rows scaled by a power of two, weights
+// The mathematics is that of kv_attn_prompt.cu (keys in fp16 against rows scaled by a power of two, weights
 // in fp16 with the value scale over the unit of the warp's O, the largest so far at 2^15; the row's own block in two bf16 products), on warp-level MMAs: with
 // up to 16 rows the work is reading the cache, 2 d bytes a key and head against 4 d flops a row, and tcgen05's 128 rows
 // would be empty.
@@ -51,7 +51,7 @@ struct TokenPlan {
     static constexpr int NT = R / 8;                // row n-tiles
     static constexpr int NU = kKvBlock / UK;        // units of a block
     static constexpr size_t kSo = 0, kMl = kTokenWarps * R * D * sizeof(float), kQf = kMl + kTokenWarps * R * 8,
-                            kQr = kQf + 4 * J * 32 * 2 * NT * 4, kBytes = kQr + R * 8;
+                            kQr = kQf + 4 * J * 32 * 2 * NT * 4, kBytes = kQr + R * 4;
     // CTAs on an SM: as many as the accumulators and loads leave registers for
     static constexpr int kCtas = D * R <= 1024 ? 3 : 2;
 };
@@ -134,7 +134,8 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
     if ((int)blockIdx.z > last_seg) return;
     extern __shared__ __align__(16) unsigned char token_smem[];
     float *so = reinterpret_cast<float *>(token_smem + P::kSo);
-    float2 *sml = reinterpret_cast<float2 *>(token_smem + P::kMl), *sqr = reinterpret_cast<float2 *>(token_smem + P::kQr);
+    float2 *sml = reinterpret_cast<float2 *>(token_smem + P::kMl);
+    float *sqr = reinterpret_cast<float *>(token_smem + P::kQr);
     uint32_t *sqf = reinterpret_cast<uint32_t *>(token_smem + P::kQf);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = lane >> 2, tq = lane & 3;
     const int32_t *table = a.c.table + (int64_t)u.slot * a.c.max_blocks;
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
         for (int f = 0; f < NT; ++f) {
             const int r = g + 8 * f;
             uint4 w[J][2];
-            float top = 0.f, sum = 0.f, back;
+            float top = 0.f, back;
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -192,18 +193,12 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                     float x[8];
                     b8_to_f(w[j][i], x);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        top = fmaxf(top, fabsf(x[k]));
-                        sum += x[k];
-                    }
+                    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
                 }
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            }
+            for (int o = 1; o < 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const float up = pow2_to_2_15(top, back);
-            if (tq == 0) sqr[r] = make_float2(back, 1152.f * up * sum);
+            if (tq == 0) sqr[r] = back;
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -222,7 +217,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
         }
     }
     __syncthreads();
-    float2 qr[NT][2];   // of the lane's rows, 8 f + 2 tq + y
+    float qr[NT][2];   // of the lane's rows, 8 f + 2 tq + y
 #pragma unroll
     for (int f = 0; f < NT; ++f)
 #pragma unroll
@@ -432,8 +427,8 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
             for (int f = 0; f < NT; ++f)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    c[f][y] = ks * qr[f][y].x;
-                    add[f][y] = dv - c[f][y] * qr[f][y].y;
+                    c[f][y] = ks * qr[f][y];
+                    add[f][y] = dv;
                 }
 #pragma unroll 1
             for (int n = 0; n < NU; ++n) {
@@ -457,7 +452,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                         }
 #pragma unroll
                         for (int x = 0; x < NA; ++x) {
-                            const uint2 lo = i8_to_f16x4<false>(kb[x][0][j][k]), hi = i8_to_f16x4<false>(kb[x][1][j][k]);
+                            const uint2 lo = i8_to_f16x4(kb[x][0][j][k]), hi = i8_to_f16x4(kb[x][1][j][k]);
                             const uint32_t ka[4] = {lo.x, hi.x, lo.y, hi.y};
 #pragma unroll
                             for (int f = 0; f < NT; ++f) mma_f16(s[x][f], ka, b[f]);

@@ -5,6 +5,7 @@ import torch
 
 from chunked_gated_deltanet_gb300 import gdn
 from kv_bounds import Bounded
+from kv_ref import TORCH
 
 pytestmark = pytest.mark.gpu
 
@@ -87,6 +88,25 @@ def test_a_first_token_that_takes_the_weight(cuda_device, d, n, lead):
     v[0] = 0.0
     fill(m, k, v)
     m.step([0], [n], data=(q, m.draw(n, 1, 0.3), m.draw(n, 1)))
+
+
+@FORMS
+@DIMS
+@pytest.mark.parametrize("mean", [3.0, 10.0])
+@pytest.mark.parametrize("channel", [1.0, 30.0], ids=["even keys", "one large channel"])
+def test_queries_with_a_common_offset(cuda_device, d, n, mean, channel):
+    """Queries whose sum is far from zero, over complete blocks and the open one, with keys of one size and with a channel
+    that sets the blocks' scales."""
+    m = Bounded((8, 2), d, BF, seed=25)
+    k = m.draw(400, 2)
+    k[:, :, 5] *= channel
+    fill(m, k, m.draw(400, 2))
+    q = m.draw(n, 8) + mean
+    if channel > 1:
+        q[:, :, 5] = m.draw(n, 8)[:, :, 5]
+    own = m.draw(n, 2)
+    own[:, :, 5] *= channel
+    m.step([0], [n], data=(q.to(TORCH[BF]), own, m.draw(n, 2)))
 
 
 @DTYPES
