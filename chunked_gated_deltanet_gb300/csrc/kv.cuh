@@ -81,7 +81,7 @@ struct KvAttn {
     int unit0;                      // first unit of the launch (a call whose partials do not fit is several)
     int tok_stride;                 // most tokens of a unit: min(64, max_new)
     int seg_blocks, n_seg;          // segment s: blocks [s * seg_blocks, (s + 1) * seg_blocks), or by kv_grown_start with seg_blocks 0
-    int max_new;                    // the caller's bound on a request's new tokens
+    int max_new, max_len;           // the caller's bounds on a request's new tokens and on a slot's length after the plan
     long long wait_limit;           // polls before a bounded wait gives up
     int skip_first_copy;            // test hook: 3 = the prompt kernel never announces its first key tile
     unsigned int *err;
@@ -90,6 +90,12 @@ struct KvAttn {
 // Segment of a block, and a segment's first block.
 __device__ __forceinline__ int kv_seg_of(const KvAttn &a, int block) { return a.seg_blocks ? block / a.seg_blocks : kv_grown_seg(block); }
 __device__ __forceinline__ int kv_seg_start(const KvAttn &a, int seg) { return a.seg_blocks ? seg * a.seg_blocks : kv_grown_start(seg); }
+
+// A unit inside the sizes that the call was given: what the attention and the join work on.
+__device__ __forceinline__ bool kv_attn_unit_ok(const KvAttn &a, const KvUnit &u) {
+    return kv_unit_ok(u, a.c, a.n_rows) && u.count <= a.max_new && (int64_t)u.block * kKvBlock + u.first + u.count <= a.max_len &&
+           kv_seg_of(a, u.block) < a.n_seg;
+}
 
 // Row of the partial results: (unit, token of the unit, query head) of a segment.
 __device__ __forceinline__ int64_t kv_part_row(const KvAttn &a, int unit, int seg, int tok, int head) {

@@ -234,7 +234,7 @@ GDN_API gdn_status gdn_kv_attention(const gdn_attn_desc *d, const gdn_kv_cache *
     a.Hq = d->n_q_heads; a.Hkv = d->n_kv_heads; a.G = a.Hq / a.Hkv;
     a.scale_log2 = (float)((double)d->scale * 1.4426950408889634);
     a.seg_blocks = f.seg_blocks; a.n_seg = (int)f.n_seg;
-    a.max_new = max_new; a.tok_stride = f.tok_stride;
+    a.max_new = max_new; a.max_len = (int)max_len; a.tok_stride = f.tok_stride;
     a.wait_limit = g_wait_limit;
     a.skip_first_copy = g_skip_first_copy;
     cudaError_t e = gdn_device_error_word(&a.err);

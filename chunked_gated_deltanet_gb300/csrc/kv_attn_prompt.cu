@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     const KvUnit u = kv_load_unit(a.units, ui);   // inside the map whatever the count
     const int unit1 = min(a.unit0 + n_units, a.counts[0]);
     if (ui >= unit1) return;
-    bool ok = kv_unit_ok(u, a.c, a.n_rows) && u.count <= a.max_new && kv_seg_of(a, u.block) < a.n_seg;
+    bool ok = kv_attn_unit_ok(a, u);
     // the span's first unit works for all of it
     if (ok && ui > a.unit0 && u.block % span != 0) {
         const KvUnit w = kv_load_unit(a.units, ui - 1);
@@ -187,6 +187,10 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     for (int i = 1; ok && i < span && ui + i < unit1 && (u.block + i) % span != 0; ++i) {
         const KvUnit w = kv_load_unit(a.units, ui + i);
         if (w.slot != u.slot || w.block != u.block + i) break;
+        if ((int64_t)w.block * kKvBlock + w.first + w.count > a.max_len) {   // past max_len: left out, and what follows it
+            if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
+            break;
+        }
         ok = kv_unit_ok(w, a.c, a.n_rows) && w.first == 0 && w.row == u.row + n_tok;
         n_tok += w.count;
     }

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int r
     if (ui >= a.counts[0]) return;
     const KvUnit u = kv_load_unit(a.units, ui);
     const int last_seg = u.block / a.seg_blocks;
-    if (!kv_unit_ok(u, a.c, a.n_rows) || u.count > a.max_new || last_seg >= a.n_seg) {
+    if (!kv_attn_unit_ok(a, u)) {
         if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
         return;
     }
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(128) kv_attn_few_simt_kernel(const KvAttn a, i
     const KvUnit u = kv_load_unit(a.units, ui);   // inside the map whatever the count
     if (ui >= a.counts[0]) return;
     const int last_seg = u.block / a.seg_blocks, n_row = u.count * a.G;
-    if (!kv_unit_ok(u, a.c, a.n_rows) || u.count > a.max_new || last_seg >= a.n_seg) {
+    if (!kv_attn_unit_ok(a, u)) {
         if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
         return;
     }
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttn a) {
     if (ui >= a.counts[0]) return;
     const KvUnit u = kv_load_unit(a.units, ui);
     const int n_seg = kv_seg_of(a, u.block) + 1;
-    if (!kv_unit_ok(u, a.c, a.n_rows) || u.count > a.max_new || n_seg > a.n_seg || n_seg == 1) return;
+    if (!kv_attn_unit_ok(a, u) || n_seg == 1) return;
     constexpr int W = D == 64 ? 2 : 4, N = D / (32 * W);
     const int lane = threadIdx.x & 31;
     const int64_t stride = a.part_rows;
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(const KvAttn a) {
     const KvUnit u = kv_load_unit(a.units, ui);
     if (ui >= a.counts[0]) return;
     const int n_seg = u.block / a.seg_blocks + 1;
-    if (!kv_unit_ok(u, a.c, a.n_rows) || u.count > a.max_new || n_seg > a.n_seg || n_seg == 1 || r >= u.count * a.Hq) return;
+    if (!kv_attn_unit_ok(a, u) || n_seg == 1 || r >= u.count * a.Hq) return;
     constexpr int W = D == 64 ? 2 : 4, N = D / (32 * W);
     __shared__ float so[8][D], sl[8];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;

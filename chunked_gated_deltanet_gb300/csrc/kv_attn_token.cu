@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
     if (ui >= a.counts[0]) return;
     const int last_seg = u.block / a.seg_blocks;
     const int n_row = u.count * a.G;
-    if (!kv_unit_ok(u, a.c, a.n_rows) || u.count > a.max_new || last_seg >= a.n_seg || n_row > R) {
+    if (!kv_attn_unit_ok(a, u) || n_row > R) {
         if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
         return;
     }

@@ -419,7 +419,7 @@ size_t gdn_kv_attention_workspace_min(const gdn_attn_desc *desc, int64_t max_len
 /* Attention of the planned tokens, after their append: q, out in_dtype
  * [n_rows][Hq][d]; k, v the arrays given to the append. max_new bounds every
  * request's new tokens and max_len every slot's length after the plan (they
- * size the launches; a unit outside them is left out and reported by
+ * size the launches; units outside them are left out and reported by
  * gdn_device_status). Rows of out that belong to no unit are untouched.
  * Softmax, sums and outputs are accumulated in fp32. With bf16 inputs the
  * weights of complete blocks enter the second product in fp16, scaled so that

@@ -140,3 +140,32 @@ def test_unequal_values_do_not_depend_on_the_split(cuda_device, d, heads):
         m.check_contents()
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
+
+
+@DTYPES
+@pytest.mark.parametrize("heads,n", [((4, 2), 3), ((4, 2), 90), ((2, 2), 200)], ids=["few", "many", "many, one head a group"])
+def test_a_length_past_max_len_is_reported(cuda_device, heads, n, dtype):
+    """max_len below a slot's length, inside the last segment too: the blocks' rows past it are left out and the status says
+    so; the rows of the blocks before it, and those of the other request, are there."""
+    m = Bounded(heads, 64, dtype)
+    m.step([0, 1], [600, 30])
+    q, k = m.draw(2 * n, heads[0]).to(cuda_device), m.draw(2 * n, 2).to(cuda_device)
+    plan = gdn.KvPlan.new(2 * n, 2)
+    gdn.gdn_kv_plan(m.desc, m.cache, m.i32([0, 1]), m.i32([n, n]), plan)
+    gdn.gdn_kv_append(m.desc, m.cache, plan, k, k)
+    assert gdn.gdn_device_status() == gdn.GDN_OK
+    ws = gdn.kv_attention_workspace(m.desc, 2 * n, 2, 600 + n)
+
+    def attend(max_len):
+        out = torch.full_like(q, 7.0)
+        gdn.gdn_kv_attention(m.desc, m.cache, plan, q, k, k, out, ws, n, max_len)
+        return out, gdn.gdn_device_status()
+
+    want, status = attend(600 + n)
+    assert status == gdn.GDN_OK and not (want == 7.0).all(2).any()
+    for short in (599 + n, 599 + n // 2, 300):
+        out, status = attend(short)
+        assert status == gdn.GDN_ERR_INVALID_ARG and gdn.gdn_device_status() == gdn.GDN_OK
+        assert torch.equal(out[n:], want[n:])
+        kept = sum(min(n, b + 64 - 600) - max(0, b - 600) for b in range(576, 600 + n, 64) if min(b + 64, 600 + n) <= short)
+        assert torch.equal(out[:kept], want[:kept]) and (out[kept:n] == 7.0).all()
