@@ -178,23 +178,20 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     const int unit1 = min(a.unit0 + n_units, a.counts[0]);
     if (ui >= unit1) return;
     bool ok = kv_attn_unit_ok(a, u);
-    // the span's first unit works for all of it
+    // the span's first unit works for all of it (the first of a run of them, where one between is left out)
     if (ok && ui > a.unit0 && u.block % span != 0) {
         const KvUnit w = kv_load_unit(a.units, ui - 1);
-        if (w.slot == u.slot && w.block == u.block - 1) return;
+        if (w.slot == u.slot && w.block == u.block - 1 && kv_attn_unit_ok(a, w)) return;
     }
     int n_tok = u.count;
     for (int i = 1; ok && i < span && ui + i < unit1 && (u.block + i) % span != 0; ++i) {
         const KvUnit w = kv_load_unit(a.units, ui + i);
         if (w.slot != u.slot || w.block != u.block + i) break;
-        if ((int64_t)w.block * kKvBlock + w.first + w.count > a.max_len) {   // past max_len: left out, and what follows it
-            if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
-            break;
-        }
-        ok = kv_unit_ok(w, a.c, a.n_rows) && w.first == 0 && w.row == u.row + n_tok;
+        if (!kv_attn_unit_ok(a, w)) break;   // reported by its own CTA
+        ok = w.first == 0 && w.row == u.row + n_tok;
         n_tok += w.count;
     }
-    if (!ok || n_tok > a.max_new) {
+    if (!ok) {
         if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
         return;
     }
@@ -714,7 +711,7 @@ cudaError_t launch_prompt(const KvAttn &a, int n_units, cudaStream_t st) {
     // blocks of a span: enough rows to fill the tile where a block's tokens are too few (G = 1, 2), a power of two <= 4
     int span = 1;
     while (span < 4 && 2 * span * kKvBlock * a.G <= P::R) span *= 2;
-    const int64_t rows_max = (int64_t)std::min(span * kKvBlock, a.max_new) * a.G;
+    const int64_t rows_max = (int64_t)std::min(span * kKvBlock, a.max_new) * a.G;   // a span of several blocks is one tile
     const int row_tiles = (int)((rows_max + P::R - 1) / P::R);
     const dim3 grid((unsigned)((int64_t)n_units * row_tiles), (unsigned)a.Hkv, (unsigned)a.n_seg);
     e = gdn_launch_pdl(kv_attn_prompt_kernel<D>, grid, P::NT, P::kBytes, st, a, row_tiles, span, n_units);

@@ -169,3 +169,29 @@ def test_a_length_past_max_len_is_reported(cuda_device, heads, n, dtype):
         assert torch.equal(out[n:], want[n:])
         kept = sum(min(n, b + 64 - 600) - max(0, b - 600) for b in range(576, 600 + n, 64) if min(b + 64, 600 + n) <= short)
         assert torch.equal(out[:kept], want[:kept]) and (out[kept:n] == 7.0).all()
+
+
+@pytest.mark.parametrize("max_new", [64, 40])
+@pytest.mark.parametrize("d", [64, 256])
+def test_rows_past_max_new_are_right_or_left_out(cuda_device, d, max_new):
+    """A request of more than max_new tokens, over several segments, with blocks that share a tile: a row is what it is with
+    the right bound, or untouched and reported."""
+    m = Bounded((2, 2), d, BF, n_pages=80, n_slots=1, max_blocks=80)
+    m.step([0], [4480 + 30], check=False)
+    n = 200
+    q, k = m.draw(n, 2).to(cuda_device), m.draw(n, 2).to(cuda_device)
+    plan = gdn.KvPlan.new(n, 1)
+    gdn.gdn_kv_plan(m.desc, m.cache, m.i32([0]), m.i32([n]), plan)
+    gdn.gdn_kv_append(m.desc, m.cache, plan, k, k)
+    ws = gdn.kv_attention_workspace(m.desc, n, 1, 5000)
+    outs = []
+    for bound in (n, max_new):
+        ws.fill_(0xFF)     # NaN in what no segment writes
+        out = torch.full_like(q, 7.0)
+        gdn.gdn_kv_attention(m.desc, m.cache, plan, q, k, k, out, ws, bound, 5000)
+        outs.append((out, gdn.gdn_device_status()))
+    (want, ok), (out, status) = outs
+    assert ok == gdn.GDN_OK and torch.isfinite(want).all()
+    right, untouched = (out == want).all(2).all(1), (out == 7.0).all(2).all(1)
+    assert (right | untouched).all()
+    assert status == (gdn.GDN_ERR_INVALID_ARG if untouched.any() else gdn.GDN_OK)
