@@ -478,13 +478,13 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttn a) {
     }
 }
 
-// The same for the few-row form, whose rows have many segments: a CTA per (token, query head), warp w taking segments
-// w, w + 8, ... and the eight sums added in order.
+// The same for the few-row form, whose rows have many segments: a CTA per (token, query head) and unit, units innermost,
+// warp w taking segments w, w + 8, ... and the eight sums added in order.
 template <typename InT, int D, int B>
-__global__ void __launch_bounds__(256) kv_join_few_kernel(const KvAttn a) {
+__global__ void __launch_bounds__(256) kv_join_few_kernel(const KvAttn a, int n_units) {
     grid_dep_wait();
     grid_dep_launch();
-    const int ui = a.unit0 + blockIdx.x, r = blockIdx.y;
+    const int r = blockIdx.x / n_units, ui = a.unit0 + blockIdx.x % n_units;
     const KvUnit u = kv_load_unit(a.units, ui);
     if (ui >= a.counts[0]) return;
     const int n_seg = u.block / a.seg_blocks + 1;
@@ -582,9 +582,9 @@ cudaError_t launch_join(const KvAttn &a, int unit_bound, int few, cudaStream_t s
     if (few) {
         // loads under way against CTAs on an SM, with the attention: 82 segments of 16 rows, d = 256, 23.3 us with eight and
         // 24.7 with two; 8 segments of 2,048 rows, d = 128, 112.9 and 109.8
-        const dim3 grid((unsigned)unit_bound, (unsigned)per_unit);
-        const cudaError_t e = a.n_seg > 32 ? gdn_launch_pdl(kv_join_few_kernel<InT, D, 8>, grid, 256, 0, st, a)
-                                           : gdn_launch_pdl(kv_join_few_kernel<InT, D, 2>, grid, 256, 0, st, a);
+        const unsigned grid = (unsigned)((int64_t)unit_bound * per_unit);   // rows of the workspace: far below 2^31
+        const cudaError_t e = a.n_seg > 32 ? gdn_launch_pdl(kv_join_few_kernel<InT, D, 8>, grid, 256, 0, st, a, unit_bound)
+                                           : gdn_launch_pdl(kv_join_few_kernel<InT, D, 2>, grid, 256, 0, st, a, unit_bound);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     const dim3 grid((unsigned)unit_bound, (unsigned)std::min((per_unit + 7) / 8, 64));

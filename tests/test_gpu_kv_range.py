@@ -195,3 +195,30 @@ def test_rows_past_max_new_are_right_or_left_out(cuda_device, d, max_new):
     right, untouched = (out == want).all(2).all(1), (out == 7.0).all(2).all(1)
     assert (right | untouched).all()
     assert status == (gdn.GDN_ERR_INVALID_ARG if untouched.any() else gdn.GDN_OK)
+
+
+def test_many_heads_and_tokens_in_the_few_row_form(cuda_device):
+    """4,096 heads and 16 tokens over two segments, 65,536 rows to join for one block: every head as it is beside 7 others."""
+    H, n, ctx = 4096, 16, 530
+    g = torch.Generator(device=cuda_device).manual_seed(31)
+    mk = lambda k: torch.randn((k, H, 64), generator=g, device=cuda_device)   # noqa: E731
+    k0, q, k, v = mk(ctx), mk(n), mk(n), mk(n)
+
+    def run(h0, heads):
+        desc = gdn.make_attn_desc(heads, heads, 64, F32)
+        cache, plan = gdn.KvCache(desc, 9, 1, 9, cuda_device), gdn.KvPlan.new(ctx, 1)
+        cut = lambda t: t[:, h0:h0 + heads].contiguous()   # noqa: E731
+        one = lambda c: torch.tensor([c], dtype=torch.int32, device=cuda_device)   # noqa: E731
+        gdn.gdn_kv_plan(desc, cache, one(0), one(ctx), plan)
+        gdn.gdn_kv_append(desc, cache, plan, cut(k0), cut(k0))
+        gdn.gdn_kv_plan(desc, cache, one(0), one(n), plan)
+        gdn.gdn_kv_append(desc, cache, plan, cut(k), cut(v))
+        out = torch.zeros((n, heads, 64), device=cuda_device)
+        ws = gdn.kv_attention_workspace(desc, n, 1, ctx + n)
+        gdn.gdn_kv_attention(desc, cache, plan, cut(q), cut(k), cut(v), out, ws, n, ctx + n)
+        assert gdn.gdn_kv_status(plan) == gdn.GDN_OK and gdn.gdn_device_status() == gdn.GDN_OK
+        return out
+
+    out = run(0, H)
+    for h0 in (0, 2040, H - 8):
+        assert torch.equal(out[:, h0:h0 + 8], run(h0, 8))
