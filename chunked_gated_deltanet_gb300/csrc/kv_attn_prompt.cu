@@ -91,7 +91,13 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int limit) {
     bool ok = true;
     if ((threadIdx.x & 31) == 0) ok = bar_wait(bar, parity, limit);
-    return __all_sync(0xffffffffu, ok);
+    ok = __all_sync(0xffffffffu, ok);
+    __syncwarp();   // what lane 0 has acquired, for the other lanes: a vote alone orders no memory
+    return ok;
+}
+// The same with every lane polling, for waits that are rare.
+__device__ __forceinline__ bool lanes_wait(uint32_t bar, uint32_t parity, int limit) {
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, limit));
 }
 __device__ __forceinline__ void bar_commit(uint32_t bar) {   // once the MMAs this thread issued are done
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             fence_proxy_async();
         }
         warp_arrive(bar(P::bReady));
-        alive = warp_wait(bar(P::bReady), 0, limit);
+        alive = lanes_wait(bar(P::bReady), 0, limit);
     }
     if (t < P::kSoft0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
@@ -322,7 +328,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             constexpr uint32_t idS = umma_idesc_f16(128, 64, 0, 0), idO8 = umma_idesc_f16(128, D, 0, 1),
                                idOraw = umma_idesc_bf16(128, D, 0, 1);
             const bool elected = elect_one();
-            if constexpr (P::kQT) alive = warp_wait(bar(P::bQ), 0, limit) && alive;
+            if constexpr (P::kQT) alive = lanes_wait(bar(P::bQ), 0, limit) && alive;
             const uint64_t dq = umma_smem_desc(sm + P::kQ + tile * P::kTile, 128, D * 16),
                            dk0 = umma_smem_desc(sm, P::kCore, P::kGroup), dv0 = umma_smem_desc(sm, P::kGroup, P::kCore);
             const uint32_t s0_tm = tmem + 128 * tile, o_tm = tmem + P::kO + tile * D;
@@ -490,7 +496,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 alive = false;
                 break;
             }
-            if (P::kQT && n == 2 && !warp_wait(bar(P::bQ), 0, limit)) {   // the queries leave the third slots
+            if (P::kQT && n == 2 && !lanes_wait(bar(P::bQ), 0, limit)) {   // the queries leave the third slots
                 alive = false;
                 break;
             }
@@ -521,7 +527,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             const uint32_t s_tm = tmem + lanes + 64 * b;
             if (!warp_wait(bar(P::bS + b), (n >> 1) & 1, limit)) return false;
             // the key warps' scalings; no later block takes the slot (the pass ends with its at most NS raw blocks)
-            if (raw && !warp_wait(bar(P::bKFull + n % NS), (n / NS) & 1, limit)) return false;
+            if (raw && !lanes_wait(bar(P::bKFull + n % NS), (n / NS) & 1, limit)) return false;
             tc_fence_after();
             const BlockInfo x = info[n];
             // keys of the block that the row sees: all or none of an 8-bit block, up to its own offset of its raw block
@@ -573,7 +579,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             if (n > 0 && __any_sync(0xffffffffu, f != 1.f)) {
                 // the next scores were issued after that product
                 const bool last = n == nb - 1;
-                if (!warp_wait(bar(last ? P::bPV + tile : P::bS + 2 * tile + ((n + 1) & 1)), last ? 0 : ((n + 1) >> 1) & 1, limit))
+                if (!lanes_wait(bar(last ? P::bPV + tile : P::bS + 2 * tile + ((n + 1) & 1)), last ? 0 : ((n + 1) >> 1) & 1, limit))
                     return false;
                 tc_fence_after();
 #pragma unroll 1
@@ -628,7 +634,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         for (int n = n8; alive && n < nb; ++n) alive = block_step(std::true_type{}, n);
         // every product is done, and the value warps have said what they left out: the rows
         kv_named_barrier(1, P::NT - P::kSoft0);
-        if (alive) alive = warp_wait(bar(P::bDrain), 0, limit);
+        if (alive) alive = lanes_wait(bar(P::bDrain), 0, limit);
         if (alive) {
             tc_fence_after();
             const bool live = tr < rows_here;
