@@ -387,6 +387,10 @@ def gdn_attn_desc_check(desc: gdn_attn_desc) -> int:
     return int(load_library().gdn_attn_desc_check(ctypes.byref(desc)))
 
 
+def _on_gpu(*tensors: Optional[torch.Tensor]) -> bool:
+    return all(t is None or t.is_cuda for t in tensors)
+
+
 def _same_shape(name: str, t: torch.Tensor, shape, dtype):
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
@@ -421,6 +425,7 @@ class KvCache:
                 t = torch.empty(shape, dtype=dtype, device=device)
             setattr(self, name, t)
         self.c = gdn_kv_cache(*[_ptr(getattr(self, n)) for n in shapes], n_pages, n_slots, max_blocks)
+        self.on_gpu = _on_gpu(*(getattr(self, n) for n in shapes))
         if not buffers:
             gdn_kv_cache_init(desc, self, stream)
 
@@ -434,6 +439,7 @@ class KvPlan:
             _same_shape(name, t, shape, torch.int32)
         self.rows, self.units, self.counts = rows, units, counts
         self.c = gdn_kv_map(_ptr(rows), _ptr(units), _ptr(counts), rows.shape[0] - 1, units.shape[0])
+        self.on_gpu = _on_gpu(rows, units, counts)
 
     @classmethod
     def new(cls, max_tokens: int, max_requests: int, device=None) -> "KvPlan":
@@ -445,7 +451,16 @@ def gdn_kv_max_units(max_tokens: int, max_requests: int) -> int:
     return int(load_library().gdn_kv_max_units(max_tokens, max_requests))
 
 
+def _check_kv(desc: gdn_attn_desc, cache: KvCache, plan: Optional[KvPlan] = None):
+    """The call's description is the cache's (it sizes the buffers), and its handles are of GPU memory."""
+    if desc is not cache.desc and bytes(desc) != bytes(cache.desc):
+        raise ValueError("the cache was made for another description")
+    if not cache.on_gpu or not (plan is None or plan.on_gpu):
+        raise ValueError("the cache and the plan must be in GPU memory")
+
+
 def gdn_kv_cache_init(desc, cache: KvCache, stream=None):
+    _check_kv(desc, cache)
     _check(load_library().gdn_kv_cache_init(ctypes.byref(desc), ctypes.byref(cache.c), _stream(stream)))
 
 
@@ -455,12 +470,21 @@ def gdn_kv_plan(desc, cache: KvCache, slots: torch.Tensor, n_new: torch.Tensor, 
     n = slots.shape[0]
     if slots.dtype != torch.int32 or n_new.dtype != torch.int32 or n_new.shape != slots.shape:
         raise ValueError("slots and n_new must be int32 of one length")
+    _check_kv(desc, cache, plan)
+    if state_out is not None:
+        _same_shape("state_out", state_out, (cache.n_slots, 2), torch.int32)
+    if n_free_out is not None:
+        _same_shape("n_free_out", n_free_out, (1,), torch.int32)
+    if not _on_gpu(slots, n_new, state_out, n_free_out):
+        raise ValueError("slots, n_new, state_out and n_free_out must be in GPU memory")
     _check(load_library().gdn_kv_plan(ctypes.byref(desc), ctypes.byref(cache.c), _ptr(slots), _ptr(n_new), n,
                                       ctypes.byref(plan.c), _ptr(state_out), _ptr(n_free_out), _stream(stream)))
 
 
 def gdn_kv_status(plan: KvPlan, stream=None) -> int:
     """GDN_OK, or GDN_ERR_CAPACITY if the last plan did not fit its cache (synchronises)."""
+    if not plan.on_gpu:
+        raise ValueError("the plan must be in GPU memory")
     return int(load_library().gdn_kv_status(ctypes.byref(plan.c), _stream(stream)))
 
 
@@ -468,11 +492,14 @@ def _check_rows(name: str, t: torch.Tensor, desc: gdn_attn_desc, n_rows: int, he
     if t.shape != (n_rows, heads, desc.head_dim) or t.dtype != _TORCH_DT[desc.in_dtype]:
         raise ValueError(f"{name} must be {_TORCH_DT[desc.in_dtype]} {[n_rows, heads, desc.head_dim]}, got {t.dtype} "
                          f"{list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be in GPU memory")
 
 
 def gdn_kv_append(desc, cache: KvCache, plan: KvPlan, k: torch.Tensor, v: torch.Tensor, stream=None):
     """k, v: [n_rows][Hkv][d] in the plan's row order."""
     n, Hkv = k.shape[0], desc.n_kv_heads
+    _check_kv(desc, cache, plan)
     _check_rows("k", k, desc, n, Hkv)
     _check_rows("v", v, desc, n, Hkv)
     _check(load_library().gdn_kv_append(ctypes.byref(desc), ctypes.byref(cache.c), ctypes.byref(plan.c), _ptr(k),
@@ -496,6 +523,9 @@ def gdn_kv_attention(desc, cache: KvCache, plan: KvPlan, q: torch.Tensor, k: tor
                      out: torch.Tensor, ws: Optional[torch.Tensor], max_new: int, max_len: int, stream=None):
     """q, out: [n_rows][Hq][d]; k, v: the arrays given to gdn_kv_append; max_new, max_len: bounds over the batch."""
     n, Hq, Hkv = q.shape[0], desc.n_q_heads, desc.n_kv_heads
+    _check_kv(desc, cache, plan)
+    if not _on_gpu(ws):
+        raise ValueError("the workspace must be in GPU memory")
     _check_rows("q", q, desc, n, Hq)
     _check_rows("k", k, desc, n, Hkv)
     _check_rows("v", v, desc, n, Hkv)
@@ -506,10 +536,12 @@ def gdn_kv_attention(desc, cache: KvCache, plan: KvPlan, q: torch.Tensor, k: tor
 
 
 def gdn_kv_fork(desc, cache: KvCache, src_slot: int, dst_slot: int, stream=None):
+    _check_kv(desc, cache)
     _check(load_library().gdn_kv_fork(ctypes.byref(desc), ctypes.byref(cache.c), src_slot, dst_slot, _stream(stream)))
 
 
 def gdn_kv_release(desc, cache: KvCache, slot: int, stream=None):
+    _check_kv(desc, cache)
     _check(load_library().gdn_kv_release(ctypes.byref(desc), ctypes.byref(cache.c), slot, _stream(stream)))
 
 
