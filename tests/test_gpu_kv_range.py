@@ -222,3 +222,18 @@ def test_many_heads_and_tokens_in_the_few_row_form(cuda_device):
     out = run(0, H)
     for h0 in (0, 2040, H - 8):
         assert torch.equal(out[:, h0:h0 + 8], run(h0, 8))
+
+
+@DTYPES
+@pytest.mark.parametrize("heads,d", [((8, 2), 128), ((2, 2), 64), ((8, 1), 256)], ids=["8q2kv-128", "2q2kv-64", "8q1kv-256"])
+def test_segments_of_unequal_values_are_joined(cuda_device, heads, d, dtype):
+    """Contexts over several segments whose blocks' values are of any size from 2^-30 to 2^30, some zero: few rows and many."""
+    m = Bounded(heads, d, dtype, n_pages=80, n_slots=1, max_blocks=80, seed=28)
+    ctx = 4410
+    v = m.draw(ctx, heads[1])
+    e = torch.randint(-30, 31, (ctx // 64 + 1,), generator=m.gen)
+    v = (v.float() * 2.0 ** e.repeat_interleave(64)[:ctx, None, None]).to(v.dtype)
+    v[640:1280] = 0
+    fill(m, m.draw(ctx, heads[1]), v)
+    for n in (2, 70):
+        m.step([0], [n], data=(m.draw(n, heads[0], 2.0), m.draw(n, heads[1]), m.draw(n, heads[1], 2.0 ** int(e[n % 64]))))
