@@ -67,11 +67,11 @@ int64_t max_units(int64_t tokens, int32_t requests) { return std::min<int64_t>(t
 // Key segments of a row's attention, in blocks, cut at absolute positions. Few rows: 512 keys for fp32 and for up to three
 // key/value heads, so that one token's long context fills the GPU, up to 4,096 for more heads, which fill it with longer
 // ones. Many rows: by the CTAs of one request and segment. Up to 31, short segments fill the SMs; up to 159, growing ones
-// (0, kv_grown_start's); more fill them alone. Against 64 blocks throughout (us): 165 x 12 rows of 6 sessions over 18,107
-// keys 60 -> 37, 290 x 16 rows over 41,802 240 -> 220, 4,000 x 16 over 37,802 1,164 -> 1,075; and 180 x 16 rows of 16
-// sessions over 12,000, which fill the GPU together, 193 -> 198. In fp32, where 64 rows of one head take about 3 us a block:
-// 256 keys up to 159 CTAs, then 512 (against 512 throughout: a prompt of 2,048 x 2 rows 77 -> 47, 2 of 644 x 8 over 2,825
-// even; 2 of 2,099 x 32, which fill the SMs, lose 5 % with 256).
+// (0, kv_grown_start's); more fill them alone. Against 64 blocks throughout (us, L2 flushed): 165 x 12 rows over 18,107
+// keys 76 -> 66, 290 x 16 rows over 41,802 255 -> 229, 4,000 x 16 over 37,802 1,204 -> 1,115; requests that fill the GPU
+// together lose: 16 of up to 200 x 16 rows over 12,000 204 -> 206, 6 of 165 x 12 over 18,107 144 -> 161. In fp32, where 64
+// rows of one head take about 3 us a block: 256 keys up to 159 CTAs, then 512 (against 512 throughout: a prompt of 2,048 x 2
+// rows 77 -> 47, 2 of 644 x 8 over 2,825 even; 2 of 2,099 x 32, which fill the SMs, lose 5 % with 256).
 // A rule on the description and max_new: a row's segments do not depend on the batch.
 int many_rows(const gdn_attn_desc *d) { return d->in_dtype == GDN_FP32 ? gdn::kKvSimtRows : gdn::kv_prompt_rows(d->head_dim); }
 constexpr int kManySteps[] = {8, 32, 160}, kManySegs[] = {32, 48, 0, 128}, kManySegsFp32[] = {4, 4, 4, 8};

@@ -27,13 +27,14 @@
 //
 // m only moves when a block's weights would pass 2^15.5 (fp16 ends at 2^16): O is rescaled (by the softmax warps, after the
 // product before it) only then. Room above m spares moves, room below spares the small weights' bits: with 14 above (and m
-// at the maximum) the turn below took 1,066 us, with 11.5 1,094, with 8 1,137, most of the moves being those of sharp rows
+// at the maximum) the turn below took 1,066 us, with 11.5 1,095, with 8 1,137, most of the moves being those of sharp rows
 // after their first block. Every decision is a row's own and every block is one softmax step, so a row's bits do
 // not depend on the rows beside it.
 //
-// Bound: the softmax warps' issue slots and the tensor core about evenly, 1,700 to 1,850 cycles for a block of 64 keys and
-// two row tiles, of which the products are 1,024. 4,000 x 16 rows over 37,802 keys (d = 128): 1.07 ms, 1.22 PFLOP/s, tensor
-// pipe 52 %; 290 x 16 rows over 41,802 keys (d = 256): 212 us, 0.94 PFLOP/s.
+// Bound: the softmax warps' issue slots and the tensor core about evenly, 1,700 cycles for a block of 64 keys and two row
+// tiles (1,900 with a segment's start and end), of which the products are 1,280: the scores' 768, as their MMAs of 64 keys
+// take 48 cycles each, and the values' 512. 4,000 x 16 rows over 37,802 keys (d = 128): 1.10 ms, 1.18 PFLOP/s, tensor pipe
+// 51 %; 290 x 16 rows over 41,802 keys (d = 256): 217 us, 0.92 PFLOP/s; the same turn with d = 64: 0.93 ms.
 #include "kv_attn.cuh"
 
 #include <algorithm>

@@ -16,7 +16,7 @@
 // With the rows as the narrow side (8 or 16) no accumulator and no product is spent on rows that are not there.
 // Units of UK keys are loaded one ahead, across blocks and segments too. The four warps' results are added in order in shared memory
 // and leave as the segment's partial result (or the result, where there is one segment only).
-// Bound: HBM. 64 tokens over 500 to 16,384 keys (32/8 heads of 128): 109 us, 5.2 TB/s read; the registers hold one unit of
+// Bound: HBM. 64 tokens over 500 to 16,384 keys (32/8 heads of 128): 107 us, 5.2 TB/s read; the registers hold one unit of
 // loads ahead at 12 warps an SM. One token over 41,802 keys (16/2 heads of 256): 22 us, latency and the join's launch.
 #include "kv_attn.cuh"
 

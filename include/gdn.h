@@ -326,9 +326,10 @@ gdn_status gdn_gates(const gdn_layer_desc *desc, const float *a, const float *b,
  * taken from the block's finite elements. The open block at a slot's end is kept in
  * in_dtype as it came, in the slot's tail. A query at position p reads the
  * blocks before its own (p / 64) from 8 bits and its own block's positions
- * <= p as they came. So the pages' content and every row of the attention
- * depend on the session's tokens and positions only, not on how they were split
- * into calls; a complete block never changes, and forks share its page.
+ * <= p as they came. So the pages' content, and what a row of the attention
+ * attends to, depend on the session's tokens and positions only, not on how they
+ * were split into calls (a row's last bits: gdn_kv_attention); a complete block
+ * never changes, and forks share its page.
  *
  * One step for a batch of requests, whether prompts or single tokens:
  *   gdn_kv_plan       from the slots' lengths and the counts of new tokens: pages, block tables, unit map
@@ -370,7 +371,10 @@ typedef struct gdn_kv_cache {
  * {slot, block, page or -1 while the block stays open, offset of the first new
  * token, their number, row of the first one in the packed inputs, tail buffer
  * that holds the block's earlier tokens, tail buffer that receives an open
- * block's tokens or -1}. gdn_kv_max_units() of a batch is enough for max_units. */
+ * block's tokens or -1}. gdn_kv_max_units() of a batch is enough for max_units.
+ * The append and the attention launch for as many units as n_rows tokens of
+ * max_requests requests can have, whatever the plan holds: a map kept for a far
+ * larger batch costs its prompts empty launches and workspace. */
 typedef struct gdn_kv_map {
     int32_t *rows, *units, *counts;
     int32_t max_requests, max_units;
@@ -427,9 +431,12 @@ size_t gdn_kv_attention_workspace_min(const gdn_attn_desc *desc, int64_t max_len
  * to 2^-18 of the largest among their segment's keys, fewer of smaller ones (in
  * a block whose values are up to 2^4 smaller than the unit they are summed in,
  * that much sooner); those of the row's own block as the sum of two bf16
- * numbers. fp32 inputs run in fp32 throughout. Deterministic; a row's bits depend on the session, the
- * description and min(max_new, n_rows), which choose the form and how its keys
- * are cut into segments, not on the other requests. */
+ * numbers. fp32 inputs run in fp32 throughout. Deterministic. A row's bits
+ * depend on the session, the description and min(max_new, n_rows), which choose
+ * the form of the whole call and how its keys are cut into segments: with
+ * max_new <= n_rows not on the other requests, and not on how the session was
+ * split into calls of one form and segment length. As every request takes the
+ * form of max_new, prompts and single tokens are faster as two plans. */
 gdn_status gdn_kv_attention(const gdn_attn_desc *desc, const gdn_kv_cache *cache, const gdn_kv_map *map,
                             const void *q, const void *k, const void *v, void *out, int64_t n_rows, int32_t max_new,
                             int64_t max_len, void *workspace, size_t workspace_bytes, gdn_stream_t stream);
