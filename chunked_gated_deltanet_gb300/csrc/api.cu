@@ -104,7 +104,7 @@ namespace {
 
 const char *const kKindName[K_KINDS] = {"prep_wy", "conv_commit", "state_output", "state_copy", "decode", "gates",
                                         "prep_wy_tail", "prefill_fused", "kv_plan", "kv_append", "kv_state",
-                                        "kv_attention", "kv_join"};
+                                        "kv_attention", "kv_join", "kv_group", "rope"};
 
 // Workspace layout for a launch of up to nblk blocks. Offsets count from the workspace pointer
 // rounded up to 256 bytes (the kernels' widest stores want 32-byte alignment); `bytes` includes

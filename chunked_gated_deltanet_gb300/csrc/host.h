@@ -27,7 +27,8 @@ extern int g_skip_first_copy;
 
 // ---- optional per-kernel event timing (gdn_timing_begin / gdn_timing_end) ----
 enum Kind { K_PREP = 0, K_CONV = 1, K_STATE = 2, K_COPY = 3, K_DECODE = 4, K_GATES = 5, K_PREP_TAIL = 6, K_FUSED = 7,
-            K_KV_PLAN = 8, K_KV_APPEND = 9, K_KV_STATE = 10, K_KV_ATTN = 11, K_KV_JOIN = 12, K_KINDS = 13 };
+            K_KV_PLAN = 8, K_KV_APPEND = 9, K_KV_STATE = 10, K_KV_ATTN = 11, K_KV_JOIN = 12, K_KV_GROUP = 13, K_ROPE = 14,
+            K_KINDS = 15 };
 
 struct Timing {
     bool on = false;

@@ -85,7 +85,17 @@ struct KvAttn {
     long long wait_limit;           // polls before a bounded wait gives up
     int skip_first_copy;            // test hook: 3 = the prompt kernel never announces its first key tile
     unsigned int *err;
+    // shared-prefix calls (KvPart): groups {first row, rows, slot, shared blocks}, and the shared blocks of each unit's group
+    const int4 *groups;
+    const int32_t *starts;
+    int n_groups;
+    int pre_blocks, n_pre;          // segments of the shared blocks, cut every pre_blocks; most of them
+    int max_suffix;                 // the caller's bound on a request's tokens past its group's shared blocks
 };
+
+// What a launch of an attention kernel covers: a plan's units over all of their keys; the units over the keys past their
+// group's shared blocks; the groups' rows over the shared blocks. The last two leave partial results, by packed row.
+enum KvPart { kKvWhole = 0, kKvSuffix = 1, kKvShared = 2 };
 
 // Segment of a block, and a segment's first block.
 __device__ __forceinline__ int kv_seg_of(const KvAttn &a, int block) { return a.seg_blocks ? block / a.seg_blocks : kv_grown_seg(block); }
@@ -95,6 +105,59 @@ __device__ __forceinline__ int kv_seg_start(const KvAttn &a, int seg) { return a
 __device__ __forceinline__ bool kv_attn_unit_ok(const KvAttn &a, const KvUnit &u) {
     return kv_unit_ok(u, a.c, a.n_rows) && u.count <= a.max_new && (int64_t)u.block * kKvBlock + u.first + u.count <= a.max_len &&
            kv_seg_of(a, u.block) < a.n_seg;
+}
+
+// Shared-prefix calls. A unit's first block that is its own (its group's shared blocks lie before it); outside the sizes
+// given with the call the unit is left out like any other.
+__device__ __forceinline__ bool kv_suffix_unit_ok(const KvAttn &a, const KvUnit &u, int start) {
+    return kv_unit_ok(u, a.c, a.n_rows) && u.count <= a.max_new && (int64_t)u.block * kKvBlock + u.first + u.count <= a.max_len &&
+           start >= 0 && start <= u.block && (int64_t)(u.block - start) * kKvBlock + u.first + u.count <= a.max_suffix &&
+           u.block / a.seg_blocks - start / a.seg_blocks < a.n_seg && (start + a.pre_blocks - 1) / a.pre_blocks <= a.n_pre;
+}
+template <int PART>
+__device__ __forceinline__ bool kv_part_unit_ok(const KvAttn &a, const KvUnit &u, int start) {
+    if constexpr (PART == kKvSuffix) return kv_suffix_unit_ok(a, u, start);
+    else return kv_attn_unit_ok(a, u);
+}
+// Segments of a unit's own keys are cut at absolute multiples of seg_blocks too; the first starts at `start`.
+template <int PART>
+__device__ __forceinline__ int kv_part_seg0(const KvAttn &a, int start) { return PART == kKvSuffix ? start / a.seg_blocks : 0; }
+// Row of a shared-prefix call's partial results: (packed row, query head); the shared blocks' segments come first.
+__device__ __forceinline__ int64_t kv_shared_part_row(const KvAttn &a, int seg, int64_t row, int head) {
+    return seg * a.part_rows + row * a.Hq + head;
+}
+
+// Group of a shared-prefix launch's row tile `x`, tiles of R rows (token x G): its record and the tile's first row, -1 if
+// there is none. The same in every lane; a warp reads 32 groups at a time.
+__device__ __forceinline__ int kv_group_of_tile(const KvAttn &a, int x, int R, int4 &rec) {
+    const int lane = threadIdx.x & 31;
+    for (int g0 = 0; g0 < a.n_groups; g0 += 32) {
+        int4 r = make_int4(0, 0, 0, 0);
+        if (g0 + lane < a.n_groups) r = a.groups[g0 + lane];
+        const int tiles = r.w > 0 && r.y > 0 ? (int)(((int64_t)r.y * a.G + R - 1) / R) : 0;
+        int upto = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, upto > x);
+        if (hit) {
+            const int w = __ffs(hit) - 1;
+            const int before = __shfl_sync(0xffffffffu, upto - tiles, w);
+            rec.x = __shfl_sync(0xffffffffu, r.x, w);
+            rec.y = __shfl_sync(0xffffffffu, r.y, w);
+            rec.z = __shfl_sync(0xffffffffu, r.z, w);
+            rec.w = __shfl_sync(0xffffffffu, r.w, w);
+            return (x - before) * R;
+        }
+        x -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return -1;
+}
+// A group's record inside the sizes that the call was given (its blocks past the launch's segments are seen by no unit).
+__device__ __forceinline__ bool kv_group_ok(const KvAttn &a, const int4 &r) {
+    return r.x >= 0 && (int64_t)r.x + r.y <= a.n_rows && (unsigned)r.z < (unsigned)a.c.n_slots && r.w <= a.c.max_blocks;
 }
 
 // Row of the partial results: (unit, token of the unit, query head) of a segment.
@@ -120,5 +183,13 @@ cudaError_t gdn_launch_kv_attn_simt(const gdn::KvAttn &a, int d, int unit_bound,
 cudaError_t gdn_launch_kv_attn_token(const gdn::KvAttn &a, int d, int unit_bound, int rows_max, cudaStream_t st);
 // bf16 inputs, many rows:
 cudaError_t gdn_launch_kv_attn_prompt(const gdn::KvAttn &a, int d, int unit_bound, cudaStream_t st);
+// The parts of a shared-prefix call. Own keys: unit_bound units, in the form of rows_max (few rows: bf16 only). Shared keys:
+// tile_bound row tiles over all groups.
+cudaError_t gdn_launch_kv_suffix(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int rows_max, int few, cudaStream_t st);
+cudaError_t gdn_launch_kv_shared(const gdn::KvAttn &a, int d, int bf16, int tile_bound, cudaStream_t st);
+cudaError_t gdn_launch_kv_shared_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, cudaStream_t st);
+cudaError_t gdn_launch_kv_group(const gdn::KvCache &c, const int32_t *rows, const int32_t *units, const int32_t *counts,
+                                int max_requests, int max_units, const int32_t *bounds, int n_groups, int max_groups,
+                                int32_t *groups, int32_t *starts, unsigned *err, cudaStream_t st);
 // Joins the segments' partial results of every row that has more than one.
 cudaError_t gdn_launch_kv_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int few, cudaStream_t st);

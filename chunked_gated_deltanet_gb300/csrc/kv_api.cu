@@ -3,6 +3,7 @@
 #include "gdn.h"
 #include "host.h"
 #include "kv.cuh"
+#include "kv_pages.cuh"
 
 #include <algorithm>
 #include <array>
@@ -261,6 +262,202 @@ GDN_API gdn_status gdn_kv_attention(const gdn_attn_desc *d, const gdn_kv_cache *
         }
     }
     return GDN_OK;
+}
+
+// ---- requests that share their first blocks ----
+
+namespace {
+
+constexpr int kSharedSms = 152;          // CTAs at a time, one an SM
+constexpr int kSharedPieces = 2 * kSharedSms;
+// How a shared-prefix call's keys are cut. Shared blocks: a piece is a row tile, a key/value head and a segment; cut so that
+// the pieces fill the SMs evenly, a piece costing its blocks and about 12 blocks' time of its own, a segment more a row of partial
+// results written and read again.
+struct SharedForm {
+    bool few;
+    int rows_max, tok_stride, seg_blocks, pre_blocks;
+    int64_t n_seg, n_pre, tiles;
+};
+int suffix_seg_blocks(const gdn_attn_desc *d, bool few) {
+    return d->in_dtype == GDN_FP32 ? 8 : few ? seg_blocks(d, true, 1) : 64;
+}
+int64_t suffix_segs(int64_t max_suffix, int seg) { return ((max_suffix - 1) / kKvBlock + seg - 1) / seg + 1; }
+int64_t most_shared(int64_t max_len) { return std::max<int64_t>((max_len - 1) / kKvBlock, 1); }
+int64_t least_pieces(int64_t blocks) { return (blocks + gdn::kKvMaxSegBlocks - 1) / gdn::kKvMaxSegBlocks; }
+SharedForm shared_form(const gdn_attn_desc *d, int64_t n_rows, int64_t n_groups, int64_t max_new, int64_t max_len, int64_t max_suffix) {
+    SharedForm f;
+    const int G = d->n_q_heads / d->n_kv_heads, R = many_rows(d);
+    f.tok_stride = (int)std::min<int64_t>(max_new, kKvBlock);
+    f.rows_max = f.tok_stride * G;
+    f.few = max_new * G <= kFewRows;
+    f.seg_blocks = suffix_seg_blocks(d, f.few);
+    f.n_seg = suffix_segs(max_suffix, f.seg_blocks);
+    f.tiles = std::min((n_rows * G + n_groups * (R - 1)) / R, n_rows * G);
+    const int64_t items = f.tiles * d->n_kv_heads, blocks = most_shared(max_len), least = least_pieces(blocks);
+    const int64_t most = std::min(blocks, std::max(least, kSharedPieces / items));
+    const double block_s = 0.9e-6, row_s = 2.0 * d->head_dim * sizeof(float) / 4e12;
+    double best = 0;
+    f.n_pre = least;
+    for (int64_t p = least; p <= most; ++p) {
+        const double t = (double)((items * p + kSharedSms - 1) / kSharedSms) * ((blocks + p - 1) / p + 12) * block_s +
+                         (double)p * n_rows * d->n_q_heads * row_s;
+        if (p == least || t < best) {
+            best = t;
+            f.n_pre = p;
+        }
+    }
+    f.pre_blocks = (int)((blocks + f.n_pre - 1) / f.n_pre);
+    f.n_pre = (blocks + f.pre_blocks - 1) / f.pre_blocks;
+    return f;
+}
+
+gdn_status check_groups(const gdn_kv_group_map *g, const gdn_kv_map *m) {
+    if (!g) return fail(GDN_ERR_INVALID_ARG, "group map is NULL");
+    if (!aligned(g->groups, 16) || !aligned(g->starts, 4))
+        return fail(GDN_ERR_INVALID_ARG, "group map: groups (16-byte aligned) and starts must be non-NULL");
+    if (g->max_groups < 1 || g->max_groups > GDN_KV_MAX_REQUESTS || g->max_units < m->max_units)
+        return fail(GDN_ERR_INVALID_ARG, "group map: max_groups must be in [1, %d] and max_units the plan's at least (%d, %d of %d)",
+                    GDN_KV_MAX_REQUESTS, g->max_groups, g->max_units, m->max_units);
+    return GDN_OK;
+}
+
+}  // namespace
+
+GDN_API gdn_status gdn_kv_group(const gdn_attn_desc *d, const gdn_kv_cache *c, const gdn_kv_map *m, const int32_t *bounds,
+                                int32_t n_groups, const gdn_kv_group_map *g, gdn_stream_t stream) {
+    gdn_status st = check_attn(d);
+    if (st != GDN_OK || (st = check_cache(c, false, false)) != GDN_OK || (st = check_map(m)) != GDN_OK ||
+        (st = check_groups(g, m)) != GDN_OK)
+        return st;
+    if (n_groups < 1 || n_groups > g->max_groups)
+        return fail(GDN_ERR_INVALID_ARG, "n_groups must be in [1, %d] (got %d)", g->max_groups, n_groups);
+    if (!aligned(bounds, 4)) return fail(GDN_ERR_INVALID_ARG, "bounds must be non-NULL");
+    unsigned *err = nullptr;
+    cudaError_t e = gdn_device_error_word(&err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word lookup");
+    cudaStream_t cst = (cudaStream_t)stream;
+    e = launch_k(K_KV_GROUP, cst, [&] {
+        return gdn_launch_kv_group(device_cache(c), m->rows, m->units, m->counts, m->max_requests, m->max_units, bounds, n_groups,
+                                   g->max_groups, g->groups, g->starts, err, cst);
+    });
+    return e != cudaSuccess ? cuda_fail(e, "group kernel") : GDN_OK;
+}
+
+GDN_API size_t gdn_kv_shared_workspace(const gdn_attn_desc *d, int64_t max_rows, int64_t max_len, int64_t max_suffix) {
+    if (check_attn(d) != GDN_OK || max_rows < 0 || max_rows > INT32_MAX || max_len < 1 || max_len > INT32_MAX || max_suffix < 1 ||
+        max_suffix > INT32_MAX)
+        return 0;
+    // shared_form takes no more pieces than fill the SMs twice, unless segments of the longest kind are more
+    const int64_t rows = std::max<int64_t>(max_rows, 1) * d->n_q_heads;
+    const int64_t pre = std::max(least_pieces(most_shared(max_len)) * rows, (int64_t)kSharedPieces * many_rows(d));
+    const int64_t own = std::max(suffix_segs(max_suffix, suffix_seg_blocks(d, true)), suffix_segs(max_suffix, suffix_seg_blocks(d, false)));
+    return kWsSlack + (size_t)(pre + own * rows) * (d->head_dim * sizeof(float) + sizeof(float2));
+}
+
+GDN_API gdn_status gdn_kv_attention_shared(const gdn_attn_desc *d, const gdn_kv_cache *c, const gdn_kv_map *m,
+                                           const gdn_kv_group_map *g, const void *q, const void *k, const void *v, void *out,
+                                           int64_t n_rows, int32_t max_new, int64_t max_len, int64_t max_suffix, void *workspace,
+                                           size_t workspace_bytes, gdn_stream_t stream) {
+    gdn_status st = check_attn(d);
+    if (st != GDN_OK || (st = check_cache(c, false, true)) != GDN_OK || (st = check_map(m)) != GDN_OK ||
+        (st = check_groups(g, m)) != GDN_OK)
+        return st;
+    if (n_rows < 0 || n_rows > INT32_MAX / d->n_q_heads)
+        return fail(GDN_ERR_INVALID_ARG, "n_rows out of range (%lld of %d heads)", (long long)n_rows, d->n_q_heads);
+    if (max_new < 1 || max_len < 1 || max_len > INT32_MAX || max_suffix < 1 || max_suffix > INT32_MAX)
+        return fail(GDN_ERR_INVALID_ARG, "max_new, max_len and max_suffix must be >= 1 (%d, %lld, %lld)", max_new, (long long)max_len,
+                    (long long)max_suffix);
+    if (n_rows == 0) return GDN_OK;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16))
+        return fail(GDN_ERR_INVALID_ARG, "q, k, v and out must be non-NULL and 16-byte aligned");
+    max_new = (int32_t)std::min<int64_t>(max_new, n_rows);
+    max_suffix = std::min(max_suffix, max_len);
+    const SharedForm f = shared_form(d, n_rows, g->max_groups, max_new, max_len, max_suffix);
+    if (f.n_pre + f.n_seg > 65535)
+        return fail(GDN_ERR_INVALID_ARG, "max_len %lld needs more than 65,535 segments", (long long)max_len);
+    const size_t need = kWsSlack + (size_t)(f.n_pre + f.n_seg) * n_rows * d->n_q_heads * (d->head_dim * sizeof(float) + sizeof(float2));
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace needs at least %zu bytes (16-byte aligned), got %zu", need,
+                    workspace ? workspace_bytes : (size_t)0);
+    gdn::KvAttn a = {};
+    a.q = q; a.k_new = k; a.v_new = v; a.out = out;
+    a.c = device_cache(c);
+    a.units = m->units; a.counts = m->counts;
+    a.n_rows = n_rows;
+    a.Hq = d->n_q_heads; a.Hkv = d->n_kv_heads; a.G = a.Hq / a.Hkv;
+    a.scale_log2 = (float)((double)d->scale * 1.4426950408889634);
+    a.seg_blocks = f.seg_blocks; a.n_seg = (int)f.n_seg;
+    a.max_new = max_new; a.max_len = (int)max_len; a.tok_stride = f.tok_stride;
+    a.wait_limit = g_wait_limit;
+    a.skip_first_copy = g_skip_first_copy;
+    a.groups = reinterpret_cast<const int4 *>(g->groups); a.starts = g->starts;
+    a.n_groups = g->max_groups;
+    a.pre_blocks = f.pre_blocks; a.n_pre = (int)f.n_pre;
+    a.max_suffix = (int)max_suffix;
+    a.part_rows = n_rows * a.Hq;
+    char *ws = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
+    a.part_ml = reinterpret_cast<float2 *>(ws);
+    a.part_o = reinterpret_cast<float *>(ws + (((size_t)(f.n_pre + f.n_seg) * a.part_rows * sizeof(float2) + 255) & ~size_t(255)));
+    cudaError_t e = gdn_device_error_word(&a.err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word lookup");
+    cudaStream_t cst = (cudaStream_t)stream;
+    const bool bf16 = d->in_dtype == GDN_BF16;
+    const int bound = (int)std::min<int64_t>(m->max_units, max_units(n_rows, m->max_requests));
+    e = launch_k(K_KV_ATTN, cst, [&] { return gdn_launch_kv_shared(a, d->head_dim, bf16, (int)f.tiles, cst); });
+    if (e != cudaSuccess) return cuda_fail(e, "shared blocks' attention kernel");
+    e = launch_k(K_KV_ATTN, cst, [&] { return gdn_launch_kv_suffix(a, d->head_dim, bf16, bound, f.rows_max, f.few, cst); });
+    if (e != cudaSuccess) return cuda_fail(e, "own keys' attention kernel");
+    e = launch_k(K_KV_JOIN, cst, [&] { return gdn_launch_kv_shared_join(a, d->head_dim, bf16, bound, cst); });
+    return e != cudaSuccess ? cuda_fail(e, "attention join kernel") : GDN_OK;
+}
+
+// ---- forks, releases and compaction ----
+
+GDN_API gdn_status gdn_kv_fork_batch(const gdn_attn_desc *d, const gdn_kv_cache *c, const int32_t *src, const int32_t *dst, int32_t n,
+                                     gdn_stream_t stream) {
+    gdn_status st = check_attn(d);
+    if (st != GDN_OK || (st = check_cache(c, true, false)) != GDN_OK) return st;
+    if (!aligned(c->tail, 16)) return fail(GDN_ERR_INVALID_ARG, "cache: tail must be non-NULL and 16-byte aligned");
+    if (c->n_slots > kKvMaxBatchSlots)
+        return fail(GDN_ERR_SHAPE, "cache: at most %d slots (got %d)", kKvMaxBatchSlots, c->n_slots);
+    if (n < 0 || n > GDN_KV_MAX_REQUESTS) return fail(GDN_ERR_INVALID_ARG, "n must be in [0, %d] (got %d)", GDN_KV_MAX_REQUESTS, n);
+    if (n == 0) return GDN_OK;
+    if (!aligned(src, 4) || !aligned(dst, 4)) return fail(GDN_ERR_INVALID_ARG, "src and dst must be non-NULL");
+    unsigned *err = nullptr;
+    cudaError_t e = gdn_device_error_word(&err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word lookup");
+    cudaStream_t cst = (cudaStream_t)stream;
+    e = launch_k(K_KV_STATE, cst, [&] {
+        return gdn_launch_kv_fork_batch(device_cache(c), src, dst, n, d->n_kv_heads, d->head_dim, d->in_dtype == GDN_BF16 ? 2 : 4, err, cst);
+    });
+    return e != cudaSuccess ? cuda_fail(e, "fork kernel") : GDN_OK;
+}
+
+GDN_API size_t gdn_kv_compact_workspace(int32_t n_pages) { return n_pages < 1 ? 0 : (size_t)n_pages * 3 * sizeof(int32_t); }
+
+GDN_API gdn_status gdn_kv_compact(const gdn_attn_desc *d, const gdn_kv_cache *c, int32_t *table_out, int32_t *refs_out,
+                                  int32_t *free_out, int32_t *n_free_out, int32_t n_pages_out, int32_t *counts, void *workspace,
+                                  size_t workspace_bytes, gdn_stream_t stream) {
+    gdn_status st = check_attn(d);
+    if (st != GDN_OK || (st = check_cache(c, true, false)) != GDN_OK) return st;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return fail(GDN_ERR_INVALID_ARG, "cache: k, v (16-byte aligned), k_scale and v_scale must be non-NULL");
+    if (n_pages_out < 1) return fail(GDN_ERR_INVALID_ARG, "n_pages_out must be >= 1 (got %d)", n_pages_out);
+    if (!table_out) table_out = c->table;
+    if (!refs_out) refs_out = c->refs;
+    if (!free_out) free_out = c->free_pages;
+    if (!n_free_out) n_free_out = c->n_free;
+    if (!aligned(table_out, 4) || !aligned(refs_out, 4) || !aligned(free_out, 4) || !aligned(n_free_out, 4) || !aligned(counts, 4))
+        return fail(GDN_ERR_INVALID_ARG, "table_out, refs_out, free_out, n_free_out and counts must be 4-byte aligned, counts non-NULL");
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < gdn_kv_compact_workspace(c->n_pages))
+        return fail(GDN_ERR_WORKSPACE, "workspace needs at least %zu bytes (16-byte aligned), got %zu", gdn_kv_compact_workspace(c->n_pages),
+                    workspace ? workspace_bytes : (size_t)0);
+    cudaStream_t cst = (cudaStream_t)stream;
+    const KvBooksOut o = {table_out, refs_out, free_out, n_free_out, n_pages_out};
+    const cudaError_t e = launch_k(K_KV_STATE, cst, [&] {
+        return gdn_launch_kv_compact(device_cache(c), o, d->n_kv_heads, d->head_dim, static_cast<int32_t *>(workspace), counts, cst);
+    });
+    return e != cudaSuccess ? cuda_fail(e, "compaction kernels") : GDN_OK;
 }
 
 GDN_API gdn_status gdn_kv_fork(const gdn_attn_desc *d, const gdn_kv_cache *c, int32_t src, int32_t dst, gdn_stream_t stream) {

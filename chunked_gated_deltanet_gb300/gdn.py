@@ -34,6 +34,11 @@ GDN_ALLOW_PARTIAL = 1
 GDN_MAX_SESSIONS = 4096
 GDN_KV_BLOCK = 64
 GDN_KV_MAX_REQUESTS = 4096
+GDN_ROPE_HALF = 0
+GDN_ROPE_INTERLEAVED = 1
+GDN_ROPE_NONE = 0
+GDN_ROPE_LINEAR = 1
+GDN_ROPE_PARTS = 2
 
 EXPORTED = ["gdn_desc_tag", "gdn_desc_check", "gdn_state_bytes", "gdn_conv_state_bytes", "gdn_session_init",
             "gdn_workspace_size", "gdn_prefill_chunks", "gdn_prefill_varlen", "gdn_state_capture",
@@ -44,7 +49,9 @@ EXPORTED = ["gdn_desc_tag", "gdn_desc_check", "gdn_state_bytes", "gdn_conv_state
             "gdn_prefill_chunks_checkpoint", "gdn_prefill_varlen_checkpoint", "gdn_attn_desc_check",
             "gdn_kv_max_units", "gdn_kv_cache_init", "gdn_kv_plan", "gdn_kv_status", "gdn_kv_append",
             "gdn_kv_attention_workspace", "gdn_kv_attention_workspace_min", "gdn_kv_attention", "gdn_kv_fork",
-            "gdn_kv_release"]
+            "gdn_kv_release", "gdn_kv_fork_batch", "gdn_kv_compact_workspace", "gdn_kv_compact", "gdn_kv_group",
+            "gdn_kv_shared_workspace", "gdn_kv_attention_shared", "gdn_rope_desc_check", "gdn_rope_table",
+            "gdn_kv_positions", "gdn_rope"]
 
 
 class gdn_layer_desc(ctypes.Structure):
@@ -75,6 +82,18 @@ class gdn_kv_map(ctypes.Structure):
                 ("max_requests", ctypes.c_int32), ("max_units", ctypes.c_int32)]
 
 
+class gdn_kv_group_map(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("max_groups", ctypes.c_int32),
+                ("max_units", ctypes.c_int32)]
+
+
+class gdn_rope_desc(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("base", ctypes.c_float),
+                ("scaling", ctypes.c_int32), ("factor", ctypes.c_float), ("original_len", ctypes.c_int32),
+                ("beta_fast", ctypes.c_float), ("beta_slow", ctypes.c_float), ("magnitude", ctypes.c_float),
+                ("eps", ctypes.c_float)]
+
+
 class gdn_kernel_time(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int64), ("timed", ctypes.c_int64),
                 ("total_ms", ctypes.c_double)]
@@ -102,7 +121,7 @@ def load_library(path: Optional[str] = None):
     D = ctypes.POINTER(gdn_layer_desc)
     Sp = ctypes.POINTER(gdn_session)
     I64p = ctypes.POINTER(ctypes.c_int64)
-    A, Kp, Mp = (ctypes.POINTER(t) for t in (gdn_attn_desc, gdn_kv_cache, gdn_kv_map))
+    A, Kp, Mp, Gp, Rp = (ctypes.POINTER(t) for t in (gdn_attn_desc, gdn_kv_cache, gdn_kv_map, gdn_kv_group_map, gdn_rope_desc))
     sig = {
         "gdn_desc_tag": (ctypes.c_uint64, [D]),
         "gdn_desc_check": (ctypes.c_int, [D]),
@@ -143,6 +162,16 @@ def load_library(path: Optional[str] = None):
         "gdn_kv_attention": (ctypes.c_int, [A, Kp, Mp, vp, vp, vp, vp, i64, i32, i64, vp, ctypes.c_size_t, vp]),
         "gdn_kv_fork": (ctypes.c_int, [A, Kp, i32, i32, vp]),
         "gdn_kv_release": (ctypes.c_int, [A, Kp, i32, vp]),
+        "gdn_kv_fork_batch": (ctypes.c_int, [A, Kp, vp, vp, i32, vp]),
+        "gdn_kv_compact_workspace": (ctypes.c_size_t, [i32]),
+        "gdn_kv_compact": (ctypes.c_int, [A, Kp, vp, vp, vp, vp, i32, vp, vp, ctypes.c_size_t, vp]),
+        "gdn_kv_group": (ctypes.c_int, [A, Kp, Mp, vp, i32, Gp, vp]),
+        "gdn_kv_shared_workspace": (ctypes.c_size_t, [A, i64, i64, i64]),
+        "gdn_kv_attention_shared": (ctypes.c_int, [A, Kp, Mp, Gp, vp, vp, vp, vp, i64, i32, i64, i64, vp, ctypes.c_size_t, vp]),
+        "gdn_rope_desc_check": (ctypes.c_int, [Rp]),
+        "gdn_rope_table": (ctypes.c_int, [Rp, vp, vp]),
+        "gdn_kv_positions": (ctypes.c_int, [Mp, i64, vp, vp]),
+        "gdn_rope": (ctypes.c_int, [A, Rp, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp]),
         "gdn_state_blob_bytes": (ctypes.c_size_t, [D]),
         "gdn_state_serialize": (ctypes.c_int, [D, Sp, vp, ctypes.c_size_t, vp]),
         "gdn_state_deserialize": (ctypes.c_int, [D, vp, ctypes.c_size_t, Sp, vp]),
@@ -543,6 +572,181 @@ def gdn_kv_fork(desc, cache: KvCache, src_slot: int, dst_slot: int, stream=None)
 def gdn_kv_release(desc, cache: KvCache, slot: int, stream=None):
     _check_kv(desc, cache)
     _check(load_library().gdn_kv_release(ctypes.byref(desc), ctypes.byref(cache.c), slot, _stream(stream)))
+
+
+def gdn_kv_fork_batch(desc, cache: KvCache, src: torch.Tensor, dst: torch.Tensor, stream=None):
+    """dst[i] becomes a copy of slot src[i], or is emptied where src[i] is -1: int32 [n] on the GPU, dst distinct and not
+    among src."""
+    n = src.numel()
+    for name, t in (("src", src), ("dst", dst)):
+        _same_shape(name, t, (n,), torch.int32)
+    _check_kv(desc, cache)
+    if not _on_gpu(src, dst):
+        raise ValueError("src and dst must be in GPU memory")
+    _check(load_library().gdn_kv_fork_batch(ctypes.byref(desc), ctypes.byref(cache.c), _ptr(src), _ptr(dst), n, _stream(stream)))
+
+
+def gdn_kv_compact_workspace(n_pages: int) -> int:
+    return int(load_library().gdn_kv_compact_workspace(n_pages))
+
+
+def kv_compact_workspace(n_pages: int, device=None) -> torch.Tensor:
+    return torch.empty(max(gdn_kv_compact_workspace(n_pages), 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def gdn_kv_compact(desc, cache: KvCache, ws: torch.Tensor, counts: torch.Tensor, table_out: Optional[torch.Tensor] = None,
+                   refs_out: Optional[torch.Tensor] = None, free_out: Optional[torch.Tensor] = None,
+                   n_free_out: Optional[torch.Tensor] = None, n_pages_out: Optional[int] = None, stream=None):
+    """Pages in use to the lowest numbers. counts: int32 [3 or more] on the GPU: pages in use, status, pages moved.
+    n_pages_out: the pool's pages afterwards (refs_out's length, else the cache's); a cut or grown pool is then wrapped in
+    a KvCache of its own."""
+    _check_kv(desc, cache)
+    P = n_pages_out if n_pages_out is not None else (refs_out.shape[0] if refs_out is not None else cache.n_pages)
+    if counts.dtype != torch.int32 or counts.dim() != 1 or counts.shape[0] < 3:
+        raise ValueError("counts must be int32 of 3 elements at least")
+    for name, t, shape in (("table_out", table_out, (cache.n_slots, cache.max_blocks)), ("refs_out", refs_out, (P,)),
+                           ("free_out", free_out, (P,)), ("n_free_out", n_free_out, (1,))):
+        if t is not None:
+            _same_shape(name, t, shape, torch.int32)
+    if P > cache.n_pages and (refs_out is None or free_out is None):
+        raise ValueError("a grown pool needs refs_out and free_out")
+    if not _on_gpu(ws, counts, table_out, refs_out, free_out, n_free_out):
+        raise ValueError("the workspace, the counts and the outputs must be in GPU memory")
+    _check(load_library().gdn_kv_compact(ctypes.byref(desc), ctypes.byref(cache.c), _ptr(table_out), _ptr(refs_out),
+                                         _ptr(free_out), _ptr(n_free_out), P, _ptr(counts), _ptr(ws),
+                                         ws.numel() * ws.element_size(), _stream(stream)))
+
+
+class KvGroups:
+    """A group map's buffers plus the C struct; KvGroups.new(plan, max_groups) allocates them."""
+
+    def __init__(self, groups: torch.Tensor, starts: torch.Tensor):
+        _same_shape("groups", groups, (groups.shape[0], 4), torch.int32)
+        _same_shape("starts", starts, starts.shape[:1], torch.int32)
+        self.groups, self.starts = groups, starts
+        self.c = gdn_kv_group_map(_ptr(groups), _ptr(starts), groups.shape[0], starts.shape[0])
+        self.on_gpu = _on_gpu(groups, starts)
+
+    @classmethod
+    def new(cls, plan: KvPlan, max_groups: int) -> "KvGroups":
+        z = lambda *s: torch.zeros(s, dtype=torch.int32, device=plan.units.device)   # noqa: E731
+        return cls(z(max_groups, 4), z(plan.units.shape[0]))
+
+
+def gdn_kv_group(desc, cache: KvCache, plan: KvPlan, bounds: torch.Tensor, groups: KvGroups, stream=None):
+    """bounds: int32 [n_groups + 1] on the GPU: group i is requests bounds[i] .. bounds[i + 1] - 1 of the plan."""
+    if bounds.dtype != torch.int32 or bounds.dim() != 1:
+        raise ValueError("bounds must be int32 [n_groups + 1]")
+    _check_kv(desc, cache, plan)
+    if not _on_gpu(bounds) or not groups.on_gpu:
+        raise ValueError("bounds and the group map must be in GPU memory")
+    _check(load_library().gdn_kv_group(ctypes.byref(desc), ctypes.byref(cache.c), ctypes.byref(plan.c), _ptr(bounds),
+                                       bounds.shape[0] - 1, ctypes.byref(groups.c), _stream(stream)))
+
+
+def gdn_kv_shared_workspace(desc, max_rows: int, max_len: int, max_suffix: int) -> int:
+    return int(load_library().gdn_kv_shared_workspace(ctypes.byref(desc), max_rows, max_len, max_suffix))
+
+
+def kv_shared_workspace(desc, max_rows: int, max_len: int, max_suffix: int, device=None) -> torch.Tensor:
+    n = gdn_kv_shared_workspace(desc, max_rows, max_len, max_suffix)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def gdn_kv_attention_shared(desc, cache: KvCache, plan: KvPlan, groups: KvGroups, q: torch.Tensor, k: torch.Tensor,
+                            v: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, max_new: int, max_len: int,
+                            max_suffix: int, stream=None):
+    """As gdn_kv_attention, a group's shared blocks once for all of its rows; max_suffix: bound on a request's tokens past
+    them."""
+    n, Hq, Hkv = q.shape[0], desc.n_q_heads, desc.n_kv_heads
+    _check_kv(desc, cache, plan)
+    if not _on_gpu(ws) or not groups.on_gpu:
+        raise ValueError("the group map and the workspace must be in GPU memory")
+    _check_rows("q", q, desc, n, Hq)
+    _check_rows("k", k, desc, n, Hkv)
+    _check_rows("v", v, desc, n, Hkv)
+    _check_rows("out", out, desc, n, Hq)
+    _check(load_library().gdn_kv_attention_shared(ctypes.byref(desc), ctypes.byref(cache.c), ctypes.byref(plan.c),
+                                                  ctypes.byref(groups.c), _ptr(q), _ptr(k), _ptr(v), _ptr(out), n, max_new,
+                                                  max_len, max_suffix, _ptr(ws), ws.numel() * ws.element_size(),
+                                                  _stream(stream)))
+
+
+# ---- rotary positions ----
+
+def make_rope_desc(rotary_dim: int, layout: int = GDN_ROPE_HALF, base: float = 10000.0, scaling: int = GDN_ROPE_NONE,
+                   factor: float = 1.0, original_len: int = 1, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                   magnitude: float = 1.0, eps: float = 1e-6) -> gdn_rope_desc:
+    return gdn_rope_desc(rotary_dim, layout, base, scaling, factor, original_len, beta_fast, beta_slow, magnitude, eps)
+
+
+def gdn_rope_desc_check(rope: gdn_rope_desc) -> int:
+    return int(load_library().gdn_rope_desc_check(ctypes.byref(rope)))
+
+
+def gdn_rope_table(rope: gdn_rope_desc, table: torch.Tensor, stream=None):
+    """table: int64 [rotary_dim / 2] on the GPU (the bits of unsigned fractions of 2^64)."""
+    _same_shape("table", table, (rope.rotary_dim // 2,), torch.int64)
+    if not table.is_cuda:
+        raise ValueError("table must be in GPU memory")
+    _check(load_library().gdn_rope_table(ctypes.byref(rope), _ptr(table), _stream(stream)))
+
+
+def rope_table(rope: gdn_rope_desc, device=None, stream=None) -> torch.Tensor:
+    table = torch.empty(max(rope.rotary_dim // 2, 1), dtype=torch.int64, device=device or "cuda")
+    gdn_rope_table(rope, table, stream)
+    return table
+
+
+def gdn_kv_positions(plan: KvPlan, positions: torch.Tensor, stream=None):
+    """positions: int32 [n_rows] on the GPU, in the plan's row order."""
+    _same_shape("positions", positions, positions.shape[:1], torch.int32)
+    if not plan.on_gpu or not positions.is_cuda:
+        raise ValueError("the plan and positions must be in GPU memory")
+    _check(load_library().gdn_kv_positions(ctypes.byref(plan.c), positions.shape[0], _ptr(positions), _stream(stream)))
+
+
+def _head_rows(name: str, t: Optional[torch.Tensor], desc: gdn_attn_desc, n: int, heads: int):
+    """Row stride of [n][heads][d] whose rows may lie apart (a column range of a product), its address."""
+    if t is None:
+        return None, 0
+    if t.shape != (n, heads, desc.head_dim) or t.dtype != _TORCH_DT[desc.in_dtype]:
+        raise ValueError(f"{name} must be {_TORCH_DT[desc.in_dtype]} {[n, heads, desc.head_dim]}, got {t.dtype} "
+                         f"{list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be in GPU memory")
+    width = heads * desc.head_dim
+    s = t.stride()
+    if n == 0:
+        return t.data_ptr(), width
+    if s[2] != 1 or (heads > 1 and s[1] != desc.head_dim):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    return t.data_ptr(), s[0] if n > 1 else max(s[0], width)
+
+
+def gdn_rope(desc, rope: gdn_rope_desc, table: torch.Tensor, positions: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+             q_out: torch.Tensor, k_out: torch.Tensor, v: Optional[torch.Tensor] = None,
+             v_out: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+             k_weight: Optional[torch.Tensor] = None, stream=None):
+    """q [n][Hq][d], k, v [n][Hkv][d], rows apart or not -> q_out, k_out, v_out contiguous; weights [d] for the norm."""
+    n, Hq, Hkv = q.shape[0], desc.n_q_heads, desc.n_kv_heads
+    _same_shape("table", table, (rope.rotary_dim // 2,), torch.int64)
+    _same_shape("positions", positions, (n,), torch.int32)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _same_shape(name, w, (desc.head_dim,), _TORCH_DT[desc.in_dtype])
+    if not _on_gpu(table, positions, q_weight, k_weight):
+        raise ValueError("the table, the positions and the weights must be in GPU memory")
+    ins = [_head_rows(name, t, desc, n, h) for name, t, h in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv))]
+    if (v is None) != (v_out is None):
+        raise ValueError("v and v_out go together")
+    _check_rows("q_out", q_out, desc, n, Hq)
+    _check_rows("k_out", k_out, desc, n, Hkv)
+    if v_out is not None:
+        _check_rows("v_out", v_out, desc, n, Hkv)
+    _check(load_library().gdn_rope(ctypes.byref(desc), ctypes.byref(rope), _ptr(table), _ptr(positions), ins[0][0], ins[0][1],
+                                   ins[1][0], ins[1][1], ins[2][0], ins[2][1], _ptr(q_weight), _ptr(k_weight), _ptr(q_out),
+                                   _ptr(k_out), _ptr(v_out), n, _stream(stream)))
 
 
 def gdn_state_blob_bytes(desc) -> int:

@@ -452,6 +452,128 @@ gdn_status gdn_kv_fork(const gdn_attn_desc *desc, const gdn_kv_cache *cache, int
 /* Empties a slot; pages that no other slot names go back to the free stack. */
 gdn_status gdn_kv_release(const gdn_attn_desc *desc, const gdn_kv_cache *cache, int32_t slot, gdn_stream_t stream);
 
+/* Forks and releases of many slots in one call: for each i, dst[i] becomes a
+ * copy of src[i] as by gdn_kv_fork, or is emptied as by gdn_kv_release where
+ * src[i] is -1. src, dst: int32 device [n], n <= GDN_KV_MAX_REQUESTS; the dst
+ * distinct and none of them among the src (a src may stand there many times).
+ * All forks read the slots as they were before the call. Pages that no slot
+ * names any more go back to the free stack in the order of their numbers. The
+ * call reads nothing on the host and captures in a CUDA graph. A batch with a
+ * slot out of range, a dst twice or a dst among the src changes nothing and is
+ * reported by gdn_device_status. At most 2^20 slots. */
+gdn_status gdn_kv_fork_batch(const gdn_attn_desc *desc, const gdn_kv_cache *cache, const int32_t *src, const int32_t *dst,
+                             int32_t n, gdn_stream_t stream);
+
+/* Compaction: with U pages in use (a reference count above 0), the i-th page in
+ * use at or above U moves to the i-th free page below U, so that pages 0 .. U - 1
+ * are in use and the rest free. Block tables, counts and the free stack are
+ * rewritten (the lowest free page is popped first); slots keep their contents,
+ * shared pages stay shared. n_pages_out: the pool's pages afterwards, so a pool
+ * can be cut to no less than U pages or be grown (k, v, the scales and the books
+ * then have room for as many; cache->n_pages is what they held before). The
+ * *_out buffers ([n_slots][max_blocks], [n_pages_out], [n_pages_out], [1])
+ * receive the books, in place where NULL; the pages themselves move in place,
+ * so with books elsewhere the old ones no longer describe the pool. Only table
+ * entries of complete blocks are written. counts: int32 device [3] = {pages in
+ * use, status, pages moved}; status 1: more in use than n_pages_out, nothing
+ * changed. Captures in a CUDA graph; scratch of gdn_kv_compact_workspace bytes. */
+size_t gdn_kv_compact_workspace(int32_t n_pages);
+gdn_status gdn_kv_compact(const gdn_attn_desc *desc, const gdn_kv_cache *cache, int32_t *table_out, int32_t *refs_out,
+                          int32_t *free_out, int32_t *n_free_out, int32_t n_pages_out, int32_t *counts, void *workspace,
+                          size_t workspace_bytes, gdn_stream_t stream);
+
+/* ---- Requests that share their first blocks ----
+ *
+ * Forks of a session share its complete blocks. In a step for such a batch (the
+ * branches of "The shadow reader", section "Who asks"; the shared prefixes of
+ * gdn_prefill_branches), requests that stand side by side in the plan form a
+ * group, and the attention reads a group's shared blocks once for all of its
+ * tokens: after plan and append, gdn_kv_group once, then
+ * gdn_kv_attention_shared in place of gdn_kv_attention for every layer whose
+ * cache has the same tables.
+ *
+ * A group map's device buffers, written by gdn_kv_group: groups [max_groups][4] =
+ * {first row, rows, slot whose table names the shared blocks, their number}, and
+ * starts [max_units] = the shared blocks of each unit's group. */
+typedef struct gdn_kv_group_map {
+    int32_t *groups, *starts;       /* groups 16-byte aligned */
+    int32_t max_groups, max_units;  /* max_units: the plan's at least */
+} gdn_kv_group_map;
+
+/* Groups of the plan's requests: group i is requests [bounds[i], bounds[i + 1])
+ * of the plan, bounds: int32 device [n_groups + 1], not decreasing. Requests in no
+ * group share nothing. A group's shared blocks are those that all of its
+ * requests' tables name alike and that lie before each one's first new token,
+ * found on the GPU, so they need not be known; of a group of one request, all
+ * of its earlier blocks. A group whose bounds are out of order or range shares
+ * nothing (gdn_device_status reports it). A plan that did not fit has no groups. */
+gdn_status gdn_kv_group(const gdn_attn_desc *desc, const gdn_kv_cache *cache, const gdn_kv_map *map, const int32_t *bounds,
+                        int32_t n_groups, const gdn_kv_group_map *groups, gdn_stream_t stream);
+
+/* Workspace of calls of up to max_rows new tokens, max_len tokens a slot and
+ * max_suffix tokens past the shared blocks. Scratch of one call. */
+size_t gdn_kv_shared_workspace(const gdn_attn_desc *desc, int64_t max_rows, int64_t max_len, int64_t max_suffix);
+
+/* gdn_kv_attention for a plan with groups: the same rows, the same attention. max_suffix bounds every request's length
+ * after the plan past its group's shared blocks (max_len is always enough; it
+ * sizes launches and workspace). Units outside the bounds are left out and
+ * reported by gdn_device_status. Roundings as in gdn_kv_attention. Deterministic;
+ * a row's last bits depend on the batch: on n_rows, the number of groups, the
+ * bounds, and where the shared blocks end. n_rows * Hq < 2^31. */
+gdn_status gdn_kv_attention_shared(const gdn_attn_desc *desc, const gdn_kv_cache *cache, const gdn_kv_map *map,
+                                   const gdn_kv_group_map *groups, const void *q, const void *k, const void *v, void *out,
+                                   int64_t n_rows, int32_t max_new, int64_t max_len, int64_t max_suffix, void *workspace,
+                                   size_t workspace_bytes, gdn_stream_t stream);
+
+/* ---- Rotary positions ----
+ *
+ * Queries and keys before they reach the cache. Per row at position p and head,
+ * y = x w / sqrt(mean(x^2) + eps) with a weight, else y = x; then the pairs i of
+ * the head's first rotary_dim elements are turned by p f_i and scaled:
+ *   (y0, y1) -> magnitude (y0 cos - y1 sin, y0 sin + y1 cos),
+ * f_i = base^(-2 i / rotary_dim); the elements after them stay as they are.
+ * GDN_ROPE_LINEAR: f_i / factor. GDN_ROPE_PARTS ("NTK-by-parts" of Peng et al.,
+ * "YaRN", 2023): with t_i = original_len f_i / (2 pi) turns within the trained
+ * length and c_i = (t_i - beta_slow) / (beta_fast - beta_slow) held to [0, 1],
+ * c_i f_i + (1 - c_i) f_i / factor. */
+enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 };   /* pairs (i, i + rotary_dim / 2), or (2 i, 2 i + 1) */
+enum { GDN_ROPE_NONE = 0, GDN_ROPE_LINEAR = 1, GDN_ROPE_PARTS = 2 };
+typedef struct gdn_rope_desc {
+    int32_t rotary_dim;   /* a multiple of 16 in [16, head_dim] */
+    int32_t layout;       /* GDN_ROPE_HALF or GDN_ROPE_INTERLEAVED */
+    float base;           /* >= 1 */
+    int32_t scaling;      /* GDN_ROPE_NONE, _LINEAR or _PARTS */
+    float factor;         /* >= 1 (unused without scaling) */
+    int32_t original_len; /* >= 1, of _PARTS */
+    float beta_fast, beta_slow; /* 0 <= beta_slow < beta_fast, of _PARTS (32 and 1 usually) */
+    float magnitude;      /* of cos and sin: 1, or 0.1 ln(factor) + 1 with _PARTS usually; > 0 */
+    float eps;            /* of the norm, >= 0 */
+} gdn_rope_desc;
+
+/* GDN_OK if the description is supported. */
+gdn_status gdn_rope_desc_check(const gdn_rope_desc *rope);
+
+/* Writes table: uint64 device [rotary_dim / 2], 16-byte aligned: f_i / (2 pi) as
+ * a fraction of 2^64. Once per description; calls of gdn_rope read it. */
+gdn_status gdn_rope_table(const gdn_rope_desc *rope, uint64_t *table, gdn_stream_t stream);
+
+/* Position of every row of a plan's packed inputs, -1 of rows in no unit:
+ * positions int32 device [n_rows]. Once per plan, for every layer. */
+gdn_status gdn_kv_positions(const gdn_kv_map *map, int64_t n_rows, int32_t *positions, gdn_stream_t stream);
+
+/* q, k (and v, which is only copied; NULL with v_out NULL) of n_rows rows, head h
+ * of row r at element r * stride + h * d of in_dtype (strides in elements: at
+ * least the row's heads, a multiple of 16 bytes; so the columns of one q/k/v
+ * product do as they are) -> contiguous [n_rows][heads][d]. An output may be its
+ * own contiguous input; other overlaps are refused. positions: int32 device
+ * [n_rows]; rows of a negative position are left as they are. q_weight,
+ * k_weight: in_dtype [d] device, NULL for no norm. fp32 arithmetic, one rounding
+ * at the end; an angle is exact to p 2^-53 turns. */
+gdn_status gdn_rope(const gdn_attn_desc *desc, const gdn_rope_desc *rope, const uint64_t *table, const int32_t *positions,
+                    const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                    const void *q_weight, const void *k_weight, void *q_out, void *k_out, void *v_out, int64_t n_rows,
+                    gdn_stream_t stream);
+
 /* Per-kernel timing with CUDA events, for benchmarks (off by default).
  * gdn_timing_begin(max_launches) creates 2 * max_launches events and starts
  * recording: every kernel the library launches afterwards, on whatever stream
@@ -465,7 +587,7 @@ typedef struct gdn_kernel_time {
     char name[32];        /* kernel kind: prep_wy, prep_wy_tail (the prologue of a call's last blocks, run
                              beside the state pass of its first ones), conv_commit, state_output, state_copy,
                              decode, gates, prefill_fused, kv_plan, kv_append, kv_state (init, forks, releases),
-                             kv_attention, kv_join */
+                             kv_attention, kv_join, kv_group, rope (and its table and positions) */
     int64_t launches;     /* launches while recording */
     int64_t timed;        /* launches with an event pair */
     double total_ms;      /* summed device time of the timed launches */
