@@ -59,6 +59,7 @@ __host__ __device__ __forceinline__ int64_t kv_tail_offset(int slot, int buf, in
 // costs its CTA about 12 blocks' time besides its own (queries in, outputs out) and the join a row of partial results, so
 // long contexts want long ones, and short contexts short ones, to have CTAs for all SMs. Cut at absolute positions.
 constexpr int kKvMaxSegBlocks = 256;
+constexpr int kKvPieceBlocks = 128;                                    // of a shared-prefix call's piece (kv_attn_shared.cuh)
 constexpr int kv_prompt_rows(int d) { return d == 256 ? 128 : 256; }   // rows of a CTA of that form
 constexpr int kKvSimtRows = 64;                                        // and of its fp32 form
 __host__ __device__ constexpr int kv_grown_seg(int block) {
@@ -90,6 +91,8 @@ struct KvAttn {
     const int32_t *starts;
     int n_groups;
     int pre_blocks, n_pre;          // segments of the shared blocks, cut every pre_blocks; most of them
+    int *cut;                       // bf16: the cut of the shared blocks, chosen on the GPU (pre_blocks: the largest)
+    int head_dim;
     int max_suffix;                 // the caller's bound on a request's tokens past its group's shared blocks
 };
 
@@ -183,10 +186,11 @@ cudaError_t gdn_launch_kv_attn_simt(const gdn::KvAttn &a, int d, int unit_bound,
 cudaError_t gdn_launch_kv_attn_token(const gdn::KvAttn &a, int d, int unit_bound, int rows_max, cudaStream_t st);
 // bf16 inputs, many rows:
 cudaError_t gdn_launch_kv_attn_prompt(const gdn::KvAttn &a, int d, int unit_bound, cudaStream_t st);
-// The parts of a shared-prefix call. Own keys: unit_bound units, in the form of rows_max (few rows: bf16 only). Shared keys:
-// tile_bound row tiles over all groups.
-cudaError_t gdn_launch_kv_suffix(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int rows_max, int few, cudaStream_t st);
-cudaError_t gdn_launch_kv_shared(const gdn::KvAttn &a, int d, int bf16, int tile_bound, cudaStream_t st);
+// The parts of a shared-prefix call. bf16: the shared blocks and, with own_units > 0, the own keys of that many units, n_pieces
+// at most; own keys of few rows in a launch of their own otherwise. fp32: two launches, tile_bound row tiles over all groups.
+cudaError_t gdn_launch_kv_shared(const gdn::KvAttn &a, int d, int own_units, int64_t n_pieces, cudaStream_t st);
+cudaError_t gdn_launch_kv_suffix_few(const gdn::KvAttn &a, int d, int unit_bound, int rows_max, cudaStream_t st);
+cudaError_t gdn_launch_kv_shared_fp32(const gdn::KvAttn &a, int d, int tile_bound, int unit_bound, int rows_max, cudaStream_t st);
 cudaError_t gdn_launch_kv_shared_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, cudaStream_t st);
 cudaError_t gdn_launch_kv_group(const gdn::KvCache &c, const int32_t *rows, const int32_t *units, const int32_t *counts,
                                 int max_requests, int max_units, const int32_t *bounds, int n_groups, int max_groups,
