@@ -59,7 +59,6 @@ __host__ __device__ __forceinline__ int64_t kv_tail_offset(int slot, int buf, in
 // costs its CTA about 12 blocks' time besides its own (queries in, outputs out) and the join a row of partial results, so
 // long contexts want long ones, and short contexts short ones, to have CTAs for all SMs. Cut at absolute positions.
 constexpr int kKvMaxSegBlocks = 256;
-constexpr int kKvPieceBlocks = 128;                                    // of a shared-prefix call's piece (kv_attn_shared.cuh)
 constexpr int kv_prompt_rows(int d) { return d == 256 ? 128 : 256; }   // rows of a CTA of that form
 constexpr int kKvSimtRows = 64;                                        // and of its fp32 form
 __host__ __device__ constexpr int kv_grown_seg(int block) {
@@ -90,8 +89,8 @@ struct KvAttn {
     const int4 *groups;
     const int32_t *starts;
     int n_groups;
-    int pre_blocks, n_pre;          // segments of the shared blocks, cut every pre_blocks; most of them
-    int *cut;                       // bf16: the cut of the shared blocks, chosen on the GPU (pre_blocks: the largest)
+    int pre_blocks, n_pre;          // segments of the shared blocks, cut every pre_blocks (one group) or *cut; most of them
+    int *cut;                       // several groups: the cut of the shared blocks, chosen on the GPU
     int head_dim;
     int max_suffix;                 // the caller's bound on a request's tokens past its group's shared blocks
 };
@@ -115,7 +114,7 @@ __device__ __forceinline__ bool kv_attn_unit_ok(const KvAttn &a, const KvUnit &u
 __device__ __forceinline__ bool kv_suffix_unit_ok(const KvAttn &a, const KvUnit &u, int start) {
     return kv_unit_ok(u, a.c, a.n_rows) && u.count <= a.max_new && (int64_t)u.block * kKvBlock + u.first + u.count <= a.max_len &&
            start >= 0 && start <= u.block && (int64_t)(u.block - start) * kKvBlock + u.first + u.count <= a.max_suffix &&
-           u.block / a.seg_blocks - start / a.seg_blocks < a.n_seg && (start + a.pre_blocks - 1) / a.pre_blocks <= a.n_pre;
+           u.block / a.seg_blocks - start / a.seg_blocks < a.n_seg;
 }
 template <int PART>
 __device__ __forceinline__ bool kv_part_unit_ok(const KvAttn &a, const KvUnit &u, int start) {
@@ -130,34 +129,6 @@ __device__ __forceinline__ int64_t kv_shared_part_row(const KvAttn &a, int seg, 
     return seg * a.part_rows + row * a.Hq + head;
 }
 
-// Group of a shared-prefix launch's row tile `x`, tiles of R rows (token x G): its record and the tile's first row, -1 if
-// there is none. The same in every lane; a warp reads 32 groups at a time.
-__device__ __forceinline__ int kv_group_of_tile(const KvAttn &a, int x, int R, int4 &rec) {
-    const int lane = threadIdx.x & 31;
-    for (int g0 = 0; g0 < a.n_groups; g0 += 32) {
-        int4 r = make_int4(0, 0, 0, 0);
-        if (g0 + lane < a.n_groups) r = a.groups[g0 + lane];
-        const int tiles = r.w > 0 && r.y > 0 ? (int)(((int64_t)r.y * a.G + R - 1) / R) : 0;
-        int upto = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, upto > x);
-        if (hit) {
-            const int w = __ffs(hit) - 1;
-            const int before = __shfl_sync(0xffffffffu, upto - tiles, w);
-            rec.x = __shfl_sync(0xffffffffu, r.x, w);
-            rec.y = __shfl_sync(0xffffffffu, r.y, w);
-            rec.z = __shfl_sync(0xffffffffu, r.z, w);
-            rec.w = __shfl_sync(0xffffffffu, r.w, w);
-            return (x - before) * R;
-        }
-        x -= __shfl_sync(0xffffffffu, upto, 31);
-    }
-    return -1;
-}
 // A group's record inside the sizes that the call was given (its blocks past the launch's segments are seen by no unit).
 __device__ __forceinline__ bool kv_group_ok(const KvAttn &a, const int4 &r) {
     return r.x >= 0 && (int64_t)r.x + r.y <= a.n_rows && (unsigned)r.z < (unsigned)a.c.n_slots && r.w <= a.c.max_blocks;
@@ -186,11 +157,10 @@ cudaError_t gdn_launch_kv_attn_simt(const gdn::KvAttn &a, int d, int unit_bound,
 cudaError_t gdn_launch_kv_attn_token(const gdn::KvAttn &a, int d, int unit_bound, int rows_max, cudaStream_t st);
 // bf16 inputs, many rows:
 cudaError_t gdn_launch_kv_attn_prompt(const gdn::KvAttn &a, int d, int unit_bound, cudaStream_t st);
-// The parts of a shared-prefix call. bf16: the shared blocks and, with own_units > 0, the own keys of that many units, n_pieces
-// at most; own keys of few rows in a launch of their own otherwise. fp32: two launches, tile_bound row tiles over all groups.
-cudaError_t gdn_launch_kv_shared(const gdn::KvAttn &a, int d, int own_units, int64_t n_pieces, cudaStream_t st);
-cudaError_t gdn_launch_kv_suffix_few(const gdn::KvAttn &a, int d, int unit_bound, int rows_max, cudaStream_t st);
-cudaError_t gdn_launch_kv_shared_fp32(const gdn::KvAttn &a, int d, int tile_bound, int unit_bound, int rows_max, cudaStream_t st);
+// The parts of a shared-prefix call. Own keys: unit_bound units, in the form of rows_max (few rows: bf16 only). Shared keys: at
+// most n_pieces pieces.
+cudaError_t gdn_launch_kv_suffix(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int rows_max, int few, cudaStream_t st);
+cudaError_t gdn_launch_kv_shared(const gdn::KvAttn &a, int d, int bf16, int n_pieces, cudaStream_t st);
 cudaError_t gdn_launch_kv_shared_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, cudaStream_t st);
 cudaError_t gdn_launch_kv_group(const gdn::KvCache &c, const int32_t *rows, const int32_t *units, const int32_t *counts,
                                 int max_requests, int max_units, const int32_t *bounds, int n_groups, int max_groups,

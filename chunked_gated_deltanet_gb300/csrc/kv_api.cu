@@ -4,6 +4,7 @@
 #include "host.h"
 #include "kv.cuh"
 #include "kv_pages.cuh"
+#include "kv_shared_piece.cuh"
 
 #include <algorithm>
 #include <array>
@@ -268,43 +269,49 @@ GDN_API gdn_status gdn_kv_attention(const gdn_attn_desc *d, const gdn_kv_cache *
 
 namespace {
 
-constexpr int kSharedSms = 152;                // CTAs at a time, one an SM
-constexpr int kSharedPieces = 2 * kSharedSms;  // shared pieces beyond what one cut of the blocks makes
-// How a shared-prefix call's keys are cut. The shared blocks of bf16 calls by the kernel, from the groups' real sizes, into
-// n_pre segments at most; of fp32 calls here. Own keys in the form of max_new; few rows go into the list of pieces while they
-// are no more than would fill the SMs twice, and are a launch of their own otherwise.
+constexpr int kSharedPieces = 2 * gdn::kSharedSms;   // shared pieces beyond one cut of every row tile
+// How a shared-prefix call's keys are cut. The shared blocks into pieces (kv_shared_piece.cuh): of one group here, from max_len;
+// of several by the kernel, which knows how long each one's are, n_pre segments at most. Own keys in the form of max_new.
 struct SharedForm {
-    bool few, listed;
+    bool few;
     int rows_max, tok_stride, seg_blocks, pre_blocks;
-    int64_t n_seg, n_pre, tiles, pieces;
+    int64_t n_seg, n_pre, pieces;
 };
 int suffix_seg_blocks(const gdn_attn_desc *d, bool few) {
     return d->in_dtype == GDN_FP32 ? 8 : few ? seg_blocks(d, true, 1) : 64;
 }
 int64_t suffix_segs(int64_t max_suffix, int seg) { return ((max_suffix - 1) / kKvBlock + seg - 1) / seg + 1; }
 int64_t most_shared(int64_t max_len) { return std::max<int64_t>((max_len - 1) / kKvBlock, 1); }
-int64_t least_pieces(int64_t blocks) { return (blocks + gdn::kKvPieceBlocks - 1) / gdn::kKvPieceBlocks; }
-SharedForm shared_form(const gdn_attn_desc *d, int64_t n_rows, int64_t n_groups, int64_t units, int64_t max_new, int64_t max_len,
-                       int64_t max_suffix) {
+int64_t least_pieces(int64_t blocks) { return (blocks + gdn::kKvMaxSegBlocks - 1) / gdn::kKvMaxSegBlocks; }
+SharedForm shared_form(const gdn_attn_desc *d, int64_t n_rows, int64_t n_groups, int64_t max_new, int64_t max_len, int64_t max_suffix) {
     SharedForm f;
     const int G = d->n_q_heads / d->n_kv_heads, R = many_rows(d);
     f.tok_stride = (int)std::min<int64_t>(max_new, kKvBlock);
     f.rows_max = f.tok_stride * G;
     f.few = max_new * G <= kFewRows && d->in_dtype == GDN_BF16;
-    f.listed = !f.few || units * d->n_kv_heads <= kSharedPieces;
-    f.seg_blocks = suffix_seg_blocks(d, f.few && !f.listed);
+    f.seg_blocks = suffix_seg_blocks(d, f.few);
     f.n_seg = suffix_segs(max_suffix, f.seg_blocks);
-    f.tiles = std::min((n_rows * G + n_groups * (R - 1)) / R, n_rows * G);
+    const int64_t tiles = std::min((n_rows * G + n_groups * (R - 1)) / R, n_rows * G), items = tiles * d->n_kv_heads;
     const int64_t blocks = most_shared(max_len), least = least_pieces(blocks), rows = n_rows * d->n_q_heads;
     f.n_pre = std::min(blocks, std::max(least, (int64_t)kSharedPieces * R / rows));
-    f.pre_blocks = gdn::kKvPieceBlocks;
-    if (d->in_dtype == GDN_FP32) {   // enough segments for all SMs
-        const int64_t items = f.tiles * d->n_kv_heads;
-        f.n_pre = std::min(f.n_pre, std::max(least, (kSharedSms + items - 1) / items));
-        f.pre_blocks = (int)((blocks + f.n_pre - 1) / f.n_pre);
+    f.pre_blocks = gdn::kKvMaxSegBlocks;
+    f.pieces = std::max(items * least, std::min(items * f.n_pre, items + kSharedPieces));
+    if (n_groups > 32) f.pieces = std::min(items * f.n_pre, std::max(f.pieces, items * ((blocks + 31) / 32)));
+    if (n_groups == 1) {
+        const double part = (double)rows * 8 * d->head_dim / 3.6e6;   // of a segment: in blocks of about 0.9 us
+        double best = 0;
+        int64_t best_p = least;
+        for (int64_t p = least; p <= f.n_pre && items * p <= f.pieces; ++p) {
+            const double t = (double)((items * p + gdn::kSharedSms - 1) / gdn::kSharedSms) * ((blocks + p - 1) / p + gdn::kSharedPieceCost) + part * p;
+            if (p == least || t < best) {
+                best = t;
+                best_p = p;
+            }
+        }
+        f.pre_blocks = (int)((blocks + best_p - 1) / best_p);
         f.n_pre = (blocks + f.pre_blocks - 1) / f.pre_blocks;
+        f.pieces = items * f.n_pre;
     }
-    f.pieces = f.tiles * d->n_kv_heads * f.n_pre + units * ((int64_t)f.rows_max / R + 2) * d->n_kv_heads * f.n_seg;
     return f;
 }
 
@@ -370,8 +377,8 @@ GDN_API gdn_status gdn_kv_attention_shared(const gdn_attn_desc *d, const gdn_kv_
     max_new = (int32_t)std::min<int64_t>(max_new, n_rows);
     max_suffix = std::min(max_suffix, max_len);
     const int bound = (int)std::min<int64_t>(m->max_units, max_units(n_rows, m->max_requests));
-    const SharedForm f = shared_form(d, n_rows, g->max_groups, bound, max_new, max_len, max_suffix);
-    if (f.n_pre + f.n_seg > 65535)
+    const SharedForm f = shared_form(d, n_rows, g->max_groups, max_new, max_len, max_suffix);
+    if (f.n_pre + f.n_seg > 65535 || f.pieces > INT32_MAX)
         return fail(GDN_ERR_INVALID_ARG, "max_len %lld needs more than 65,535 segments", (long long)max_len);
     const size_t need = kWsSlack + 256 + (size_t)(f.n_pre + f.n_seg) * n_rows * d->n_q_heads * (d->head_dim * sizeof(float) + sizeof(float2));
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)
@@ -396,22 +403,17 @@ GDN_API gdn_status gdn_kv_attention_shared(const gdn_attn_desc *d, const gdn_kv_
     a.head_dim = d->head_dim;
     char *ws = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
     const bool bf16 = d->in_dtype == GDN_BF16;
-    a.cut = bf16 ? reinterpret_cast<int *>(ws) : nullptr;
+    a.cut = g->max_groups > 1 ? reinterpret_cast<int *>(ws) : nullptr;
     ws += 256;
     a.part_ml = reinterpret_cast<float2 *>(ws);
     a.part_o = reinterpret_cast<float *>(ws + (((size_t)(f.n_pre + f.n_seg) * a.part_rows * sizeof(float2) + 255) & ~size_t(255)));
     cudaError_t e = gdn_device_error_word(&a.err);
     if (e != cudaSuccess) return cuda_fail(e, "device error word lookup");
     cudaStream_t cst = (cudaStream_t)stream;
-    e = launch_k(K_KV_ATTN, cst, [&] {
-        return bf16 ? gdn_launch_kv_shared(a, d->head_dim, f.listed ? bound : 0, f.pieces, cst)
-                    : gdn_launch_kv_shared_fp32(a, d->head_dim, (int)f.tiles, bound, f.rows_max, cst);
-    });
-    if (e != cudaSuccess) return cuda_fail(e, "shared-prefix attention kernel");
-    if (bf16 && !f.listed) {
-        e = launch_k(K_KV_ATTN, cst, [&] { return gdn_launch_kv_suffix_few(a, d->head_dim, bound, f.rows_max, cst); });
-        if (e != cudaSuccess) return cuda_fail(e, "own keys' attention kernel");
-    }
+    e = launch_k(K_KV_ATTN, cst, [&] { return gdn_launch_kv_shared(a, d->head_dim, bf16, (int)f.pieces, cst); });
+    if (e != cudaSuccess) return cuda_fail(e, "shared blocks' attention kernel");
+    e = launch_k(K_KV_ATTN, cst, [&] { return gdn_launch_kv_suffix(a, d->head_dim, bf16, bound, f.rows_max, f.few, cst); });
+    if (e != cudaSuccess) return cuda_fail(e, "own keys' attention kernel");
     e = launch_k(K_KV_JOIN, cst, [&] { return gdn_launch_kv_shared_join(a, d->head_dim, bf16, bound, cst); });
     return e != cudaSuccess ? cuda_fail(e, "attention join kernel") : GDN_OK;
 }

@@ -38,6 +38,7 @@
 #pragma once
 
 #include "kv_attn.cuh"
+#include "kv_shared_piece.cuh"
 
 #include <algorithm>
 #include <type_traits>
@@ -172,41 +173,62 @@ struct __align__(16) BlockInfo {
 constexpr float kRawSpan = 16.f;   // how far a raw block's values, whose two-part weights have 8-bit exponents, may be from the unit 1
 
 
-template <int D>
+template <int D, int PART = kKvWhole>
 __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(const KvAttn a, int row_tiles, int span, int n_units) {
     using P = PromptPlan<D>;
     using bf = __nv_bfloat16;
     constexpr int NS = P::NS;
     grid_dep_wait();
     grid_dep_launch();
-    // later units (longer contexts) first: a causal launch then ends on its short ones
-    const int ui = a.unit0 + n_units - 1 - (int)(blockIdx.x / row_tiles), rt = blockIdx.x % row_tiles, h = blockIdx.y;
-    // and of growing segments the longer ones
-    const int seg = a.seg_blocks ? (int)blockIdx.z : a.n_seg - 1 - (int)blockIdx.z;
-    const KvUnit u = kv_load_unit(a.units, ui);   // inside the map whatever the count
-    const int unit1 = min(a.unit0 + n_units, a.counts[0]);
-    if (ui >= unit1) return;
-    bool ok = kv_attn_unit_ok(a, u);
-    // the span's first unit works for all of it (the first of a run of them, where one between is left out)
-    if (ok && ui > a.unit0 && u.block % span != 0) {
-        const KvUnit w = kv_load_unit(a.units, ui - 1);
-        if (w.slot == u.slot && w.block == u.block - 1 && kv_attn_unit_ok(a, w)) return;
+    int h = blockIdx.y, ui = 0, rt = 0, seg = 0, n_tok = 0, seg0 = 0, last_seg = 0, r0 = 0, cut = 0;
+    KvUnit u;
+    if constexpr (PART == kKvShared) {
+        // a group's rows as those of one unit that starts where the shared blocks end: every row sees all of them
+        int4 rec;
+        if (!kv_shared_piece<P::R>(a, blockIdx.x, r0, h, seg, cut, rec)) return;
+        if (!kv_group_ok(a, rec)) {
+            if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
+            return;
+        }
+        u = {rec.z, rec.w, -1, 0, rec.y, rec.x, 0, 0};
+        n_tok = rec.y;
+        last_seg = INT32_MAX;   // no segment has a block of the rows' own
+    } else {
+        // later units (longer contexts) first: a causal launch then ends on its short ones
+        ui = a.unit0 + n_units - 1 - (int)(blockIdx.x / row_tiles);
+        rt = blockIdx.x % row_tiles;
+        // and of growing segments the longer ones
+        seg = a.seg_blocks ? (int)blockIdx.z : a.n_seg - 1 - (int)blockIdx.z;
+        u = kv_load_unit(a.units, ui);   // inside the map whatever the count
+        const int unit1 = min(a.unit0 + n_units, a.counts[0]);
+        if (ui >= unit1) return;
+        const int start = PART == kKvSuffix ? a.starts[ui] : 0;   // the first block of the pass
+        bool ok = kv_part_unit_ok<PART>(a, u, start);
+        // the span's first unit works for all of it (the first of a run of them, where one between is left out)
+        if (ok && ui > a.unit0 && u.block % span != 0) {
+            const KvUnit w = kv_load_unit(a.units, ui - 1);
+            if (w.slot == u.slot && w.block == u.block - 1 && kv_part_unit_ok<PART>(a, w, start)) return;
+        }
+        n_tok = u.count;
+        for (int i = 1; ok && i < span && ui + i < unit1 && (u.block + i) % span != 0; ++i) {
+            const KvUnit w = kv_load_unit(a.units, ui + i);
+            if (w.slot != u.slot || w.block != u.block + i) break;
+            if (!kv_part_unit_ok<PART>(a, w, start)) break;   // reported by its own CTA
+            ok = w.first == 0 && w.row == u.row + n_tok;
+            n_tok += w.count;
+        }
+        if (!ok) {
+            if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
+            return;
+        }
+        last_seg = kv_seg_of(a, u.block);   // a span lies in one segment: span divides their starts
+        seg0 = kv_part_seg0<PART>(a, start);
+        seg += seg0;
+        r0 = rt * P::R;
+        if (seg > last_seg) return;
     }
-    int n_tok = u.count;
-    for (int i = 1; ok && i < span && ui + i < unit1 && (u.block + i) % span != 0; ++i) {
-        const KvUnit w = kv_load_unit(a.units, ui + i);
-        if (w.slot != u.slot || w.block != u.block + i) break;
-        if (!kv_attn_unit_ok(a, w)) break;   // reported by its own CTA
-        ok = w.first == 0 && w.row == u.row + n_tok;
-        n_tok += w.count;
-    }
-    if (!ok) {
-        if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
-        return;
-    }
-    const int last_seg = kv_seg_of(a, u.block);   // a span lies in one segment: span divides their starts
-    const int n_row = n_tok * a.G, r0 = rt * P::R;
-    if (r0 >= n_row || seg > last_seg) return;
+    const int n_row = n_tok * a.G;
+    if (r0 >= n_row) return;
 
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t *bar64 = reinterpret_cast<uint64_t *>(sm + P::kBar);
@@ -222,10 +244,12 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     const int rows_here = min(P::R, n_row - r0);
     const int nt = rows_here > 128 ? 2 : 1;        // MMA tiles in use
     // blocks of this tile's rows, and the blocks of the pass: 8-bit [c0, c0 + n8), then raw from blo
-    const int blo = (pos0 + r0 / a.G) / kKvBlock, bhi = (pos0 + (r0 + rows_here - 1) / a.G) / kKvBlock;
-    const int c0 = kv_seg_start(a, seg);
-    const int n8 = min(bhi, kv_seg_start(a, seg + 1)) - c0;
-    const int nb = n8 + (seg == last_seg ? bhi - blo + 1 : 0);
+    const int blo = PART == kKvShared ? u.block : (pos0 + r0 / a.G) / kKvBlock,
+              bhi = PART == kKvShared ? u.block : (pos0 + (r0 + rows_here - 1) / a.G) / kKvBlock;
+    const int c0 = PART == kKvShared ? seg * cut
+                   : PART == kKvSuffix ? max(kv_seg_start(a, seg), a.starts[ui]) : kv_seg_start(a, seg);
+    const int n8 = min(bhi, PART == kKvShared ? c0 + cut : kv_seg_start(a, seg + 1)) - c0;
+    const int nb = n8 + (PART != kKvShared && seg == last_seg ? bhi - blo + 1 : 0);
 
     if (t == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -453,6 +477,48 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 else if (pos < pos0 + n_tok)
                     src = static_cast<const bf *>(is_v ? a.v_new : a.k_new) + ((int64_t)(u.row + pos - pos0) * a.Hkv + h) * D;
                 float top = 0.f, up = 1.f;
+                if constexpr (PART == kKvSuffix) {
+                    // raw blocks are most of such a pass: a row's pieces loaded together, where the loop below (whose few
+                    // instructions leave the instruction cache to the complete blocks) waits for memory four times
+                    uint4 y[P::kVec][2];
+#pragma unroll
+                    for (int dg = 0; dg < P::kVec; ++dg)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            y[dg][k] = src ? reinterpret_cast<const uint4 *>(src + dg * 64 + ch * 16)[k] : make_uint4(0, 0, 0, 0);
+                    if (!is_v) {
+#pragma unroll
+                        for (int dg = 0; dg < P::kVec; ++dg)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                float f[8];
+                                b8_to_f(y[dg][k], f);
+#pragma unroll
+                                for (int x = 0; x < 8; ++x) top = fmaxf(top, fabsf(f[x]));
+                            }
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                        float back;
+                        up = pow2_to_2_15(top, back);
+                        if (ch == 0) raw_k[(block - blo) * 64 + off] = back;
+                    }
+#pragma unroll
+                    for (int dg = 0; dg < P::kVec; ++dg)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            if (is_v) {
+                                if (drop_not_finite(y[dg][k])) atomicOr(&bad_v[block - blo], 1u);   // added by the rows that see it
+                            } else {
+                                float f[8];
+                                b8_to_f(y[dg][k], f);
+#pragma unroll
+                                for (int x = 0; x < 8; ++x) f[x] *= up;
+                                y[dg][k] = f8_to_h8(f);
+                            }
+                            *reinterpret_cast<uint4 *>(dst + kg * P::kGroup + dg * (8 * P::kCore) + k * P::kCore) = y[dg][k];
+                        }
+                    continue;
+                }
 #pragma unroll 1
                 for (int pass = is_v ? 1 : 0; pass < 2; ++pass) {   // keys: the largest element first, then the scaled key
 #pragma unroll 1
@@ -534,7 +600,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             tc_fence_after();
             const BlockInfo x = info[n];
             // keys of the block that the row sees: all or none of an 8-bit block, up to its own offset of its raw block
-            const int see = raw ? (blk == blo + n - n8 ? off + 1 : 0) : (blk > c0 + n ? kKvBlock : 0);
+            const int see = raw ? (blk == blo + n - n8 ? off + 1 : 0) : (PART == kKvShared || blk > c0 + n ? kKvBlock : 0);
             const float c = x.c * rq;
             float s[64];
             {
@@ -642,14 +708,15 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
             tc_fence_after();
             const bool live = tr < rows_here;
             const int head = h * a.G + r % a.G, tok = r / a.G;
-            const bool one = last_seg == 0;
+            const bool one = PART == kKvWhole && last_seg == 0;
             const float inv = (one ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f) * pow2_of(lref);   // no key: zero; NaN stays
             int64_t pr = 0;
             if (live && !one) {
-                pr = kv_part_row(a, ui + blk - u.block, seg, blk == u.block ? tok : off, head);
+                pr = PART == kKvWhole ? kv_part_row(a, ui + blk - u.block, seg, blk == u.block ? tok : off, head)
+                                      : kv_shared_part_row(a, PART == kKvShared ? seg : a.n_pre + seg - seg0, u.row + tok, head);
                 a.part_ml[pr] = make_float2(m, l);
             }
-            const bool fix = live && seg == last_seg && bad_v[min(max(blk - blo, 0), 3)] != 0;
+            const bool fix = PART != kKvShared && live && seg == last_seg && bad_v[min(max(blk - blo, 0), 3)] != 0;
             // The warp's 32 rows pass through shared memory (the operands', which every product has read), 128 bytes of a row at a time
             // with the 16-byte chunks of row i at chunk ^ (i % 8), so that the stores to global memory are of whole rows.
             unsigned char *stage = sm + (warp - P::kSoft0 / 32) * (32 * 128);
@@ -712,19 +779,31 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     if (warp == 0) tmem_dealloc(tmem, P::kTmemCols);
 }
 
-template <int D>
+// n_units: units, or the most pieces of the shared blocks (kKvShared)
+template <int D, int PART = kKvWhole>
 cudaError_t launch_prompt(const KvAttn &a, int n_units, cudaStream_t st) {
     using P = PromptPlan<D>;
-    cudaError_t e = cudaFuncSetAttribute(kv_attn_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::kBytes);
+    cudaError_t e = cudaFuncSetAttribute(kv_attn_prompt_kernel<D, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::kBytes);
     if (e != cudaSuccess) return e;
+    if constexpr (PART == kKvShared) {
+        e = gdn_launch_pdl(kv_attn_prompt_kernel<D, PART>, dim3((unsigned)n_units), P::NT, P::kBytes, st, a, 1, 1, n_units);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
     // blocks of a span: enough rows to fill the tile where a block's tokens are too few (G = 1, 2), a power of two <= 4
     int span = 1;
     while (span < 4 && 2 * span * kKvBlock * a.G <= P::R) span *= 2;
     const int64_t rows_max = (int64_t)std::min(span * kKvBlock, a.max_new) * a.G;   // a span of several blocks is one tile
     const int row_tiles = (int)((rows_max + P::R - 1) / P::R);
     const dim3 grid((unsigned)((int64_t)n_units * row_tiles), (unsigned)a.Hkv, (unsigned)a.n_seg);
-    e = gdn_launch_pdl(kv_attn_prompt_kernel<D>, grid, P::NT, P::kBytes, st, a, row_tiles, span, n_units);
+    e = gdn_launch_pdl(kv_attn_prompt_kernel<D, PART>, grid, P::NT, P::kBytes, st, a, row_tiles, span, n_units);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int PART>
+cudaError_t launch_prompt_part(const KvAttn &a, int d, int n, cudaStream_t st) {
+    if (d == 64) return launch_prompt<64, PART>(a, n, st);
+    if (d == 128) return launch_prompt<128, PART>(a, n, st);
+    return launch_prompt<256, PART>(a, n, st);
 }
 
 }  // namespace gdn

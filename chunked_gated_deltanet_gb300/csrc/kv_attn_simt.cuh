@@ -9,7 +9,7 @@
 // the cache alone, not on the other rows of the call.
 #pragma once
 
-#include "kv.cuh"
+#include "kv_shared_piece.cuh"
 
 #include <algorithm>
 #include <type_traits>
@@ -91,21 +91,18 @@ __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int r
     constexpr int R = P::R, LD = P::LD, PLD = P::PLD, CT = D / 16;
     grid_dep_wait();
     grid_dep_launch();
-    const int h = blockIdx.y;
-    int ui = 0, r0 = 0, seg = blockIdx.z, seg0 = 0, last_seg = 0, start = 0;
+    int h = blockIdx.y, ui = 0, r0 = 0, seg = blockIdx.z, seg0 = 0, last_seg = 0, start = 0, cut = a.seg_blocks;
     KvUnit u;
     if constexpr (PART == kKvShared) {
         // a group's rows as those of one unit that starts where the shared blocks end: every row sees all of them
         int4 rec;
-        r0 = kv_group_of_tile(a, blockIdx.x, R, rec);
-        if (r0 < 0) return;
+        if (!kv_shared_piece<R>(a, blockIdx.x, r0, h, seg, cut, rec)) return;
         if (!kv_group_ok(a, rec)) {
             if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
             return;
         }
         u = {rec.z, rec.w, -1, 0, rec.y, rec.x, 0, 0};
-        last_seg = a.n_pre;   // no segment has a block of the rows' own
-        if (seg * a.pre_blocks >= rec.w) return;
+        last_seg = INT32_MAX;   // no segment has a block of the rows' own
     } else {
         ui = a.unit0 + blockIdx.x / row_tiles;
         r0 = blockIdx.x % row_tiles * R;
@@ -225,7 +222,6 @@ __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int r
             }
         }
     };
-    const int cut = PART == kKvShared ? a.pre_blocks : a.seg_blocks;
     const int b0 = max(seg * cut, start), b1 = min(u.block, (seg + 1) * cut);
     const int32_t *table = a.c.table + (int64_t)u.slot * a.c.max_blocks;
     // the head's part of block b's page, the page in bounds whatever the table holds (the result is reported as invalid then)
@@ -292,12 +288,12 @@ __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int r
 }
 
 template <int D, int PART = kKvWhole>
-cudaError_t launch_simt_many(const KvAttn &a, int n, int rows_max, cudaStream_t st) {   // n: units, or row tiles of all groups
+cudaError_t launch_simt_many(const KvAttn &a, int n, int rows_max, cudaStream_t st) {   // n: units, or the most pieces (kKvShared)
     using P = SimtPlan<D>;
     const cudaError_t e = cudaFuncSetAttribute(kv_attn_simt_kernel<D, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::kBytes);
     if (e != cudaSuccess) return e;
     const int row_tiles = PART == kKvShared ? 1 : (rows_max + P::R - 1) / P::R;
-    const dim3 grid((unsigned)((int64_t)n * row_tiles), (unsigned)a.Hkv, (unsigned)(PART == kKvShared ? a.n_pre : a.n_seg));
+    const dim3 grid = PART == kKvShared ? dim3((unsigned)n) : dim3((unsigned)((int64_t)n * row_tiles), (unsigned)a.Hkv, (unsigned)a.n_seg);
     return gdn_launch_pdl(kv_attn_simt_kernel<D, PART>, grid, 256, P::kBytes, st, a, row_tiles);
 }
 

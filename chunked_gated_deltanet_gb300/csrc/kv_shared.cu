@@ -4,7 +4,7 @@
 // Softmax over a row's keys as that over two sets of them: each part leaves (O, m, l) of its segments, O the sum of
 // 2^{x - m} v and l that of 2^{x - m} over its keys, and the row is sum 2^{m_s - M} O_s / sum 2^{m_s - M} l_s with M the
 // largest m_s, in the order of s: the shared blocks' segments, then the own ones.
-#include "kv_attn_shared.cuh"
+#include "kv_attn_prompt.cuh"
 #include "kv_attn_simt.cuh"
 #include "kv_attn_token.cuh"
 
@@ -78,12 +78,31 @@ __global__ void __launch_bounds__(kGroupThreads) kv_group_kernel(const KvCache c
     int upto = u1 > u0 && ok ? most : 0;
     if (n > 1 && upto > 0) {
         const int32_t *mine = c.table + (int64_t)slot * c.max_blocks;
-        const int64_t pairs = (int64_t)n * most;
-#pragma unroll 4
-        for (int64_t e = rank * kGroupThreads + t; e < pairs; e += n_cl * kGroupThreads) {
-            const int r = (int)(e / most), b = (int)(e - (int64_t)r * most), s = slots[r];
-            if ((unsigned)s >= (unsigned)c.n_slots) upto = 0;
-            else if (c.table[(int64_t)s * c.max_blocks + b] != mine[b]) upto = min(upto, b);
+        // a warp takes 128 blocks of a request at a time: four loads of either table a lane
+        const int warps = n_cl * (kGroupThreads / 32), chunks = (most + 127) / 128, lane = t & 31;
+        int r = 0, c0 = rank * (kGroupThreads / 32) + (t >> 5);
+        for (;; c0 += warps) {
+            while (r < n && c0 >= chunks) {
+                c0 -= chunks;
+                ++r;
+            }
+            if (r >= n) break;
+            const int s = slots[r];
+            if ((unsigned)s >= (unsigned)c.n_slots) {
+                upto = 0;
+                continue;
+            }
+            const int32_t *theirs = c.table + (int64_t)s * c.max_blocks;
+            int x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int b = 128 * c0 + 32 * i + lane;
+                x[i] = b < most ? mine[b] : 0;
+                y[i] = b < most ? theirs[b] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (x[i] != y[i]) upto = min(upto, 128 * c0 + 32 * i + lane);
         }
     }
     upto = __reduce_min_sync(0xffffffffu, upto);
@@ -232,21 +251,18 @@ cudaError_t gdn_launch_kv_group(const gdn::KvCache &c, const int32_t *rows, cons
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t gdn_launch_kv_shared(const gdn::KvAttn &a, int d, int own_units, int64_t n_pieces, cudaStream_t st) {
+cudaError_t gdn_launch_kv_suffix(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int rows_max, int few, cudaStream_t st) {
     using namespace gdn;
-    if (d == 64) return launch_shared<64>(a, own_units, n_pieces, st);
-    if (d == 128) return launch_shared<128>(a, own_units, n_pieces, st);
-    return launch_shared<256>(a, own_units, n_pieces, st);
+    const cudaError_t e = !bf16 ? launch_simt_part<kKvSuffix>(a, d, unit_bound, rows_max, st)
+                          : few ? launch_token_part<kKvSuffix>(a, d, unit_bound, rows_max, st)
+                                : launch_prompt_part<kKvSuffix>(a, d, unit_bound, st);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t gdn_launch_kv_suffix_few(const gdn::KvAttn &a, int d, int unit_bound, int rows_max, cudaStream_t st) {
-    return gdn::launch_token_part<gdn::kKvSuffix>(a, d, unit_bound, rows_max, st);
-}
-
-cudaError_t gdn_launch_kv_shared_fp32(const gdn::KvAttn &a, int d, int tile_bound, int unit_bound, int rows_max, cudaStream_t st) {
+cudaError_t gdn_launch_kv_shared(const gdn::KvAttn &a, int d, int bf16, int n_pieces, cudaStream_t st) {
     using namespace gdn;
-    const cudaError_t e = launch_simt_part<kKvShared>(a, d, tile_bound, 0, st);
-    return e != cudaSuccess ? e : launch_simt_part<kKvSuffix>(a, d, unit_bound, rows_max, st);
+    const cudaError_t e = bf16 ? launch_prompt_part<kKvShared>(a, d, n_pieces, st) : launch_simt_part<kKvShared>(a, d, n_pieces, 0, st);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t gdn_launch_kv_shared_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, cudaStream_t st) {
