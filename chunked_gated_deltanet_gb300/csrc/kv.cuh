@@ -91,7 +91,7 @@ struct KvAttn {
     int n_groups;
     int pre_blocks, n_pre;          // segments of the shared blocks, cut every pre_blocks (one group) or *cut; most of them
     int *cut;                       // several groups: the cut of the shared blocks, chosen on the GPU
-    int head_dim;
+    int head_dim, own_apart;
     int max_suffix;                 // the caller's bound on a request's tokens past its group's shared blocks
 };
 
@@ -109,12 +109,18 @@ __device__ __forceinline__ bool kv_attn_unit_ok(const KvAttn &a, const KvUnit &u
            kv_seg_of(a, u.block) < a.n_seg;
 }
 
-// Shared-prefix calls. A unit's first block that is its own (its group's shared blocks lie before it); outside the sizes
+// Shared-prefix calls. Segments of a unit's own keys, those of its blocks [start, block) and of its own block, which few rows
+// have as a segment by itself and many rows in the last one.
+__device__ __forceinline__ int kv_own_segs(const KvAttn &a, int block, int start) {
+    if (!a.own_apart) return block / a.seg_blocks - start / a.seg_blocks + 1;
+    return (block > start ? (block - 1) / a.seg_blocks - start / a.seg_blocks + 1 : 0) + 1;
+}
+// A unit's first block that is its own (its group's shared blocks lie before it); outside the sizes
 // given with the call the unit is left out like any other.
 __device__ __forceinline__ bool kv_suffix_unit_ok(const KvAttn &a, const KvUnit &u, int start) {
     return kv_unit_ok(u, a.c, a.n_rows) && u.count <= a.max_new && (int64_t)u.block * kKvBlock + u.first + u.count <= a.max_len &&
            start >= 0 && start <= u.block && (int64_t)(u.block - start) * kKvBlock + u.first + u.count <= a.max_suffix &&
-           u.block / a.seg_blocks - start / a.seg_blocks < a.n_seg;
+           kv_own_segs(a, u.block, start) <= a.n_seg;
 }
 template <int PART>
 __device__ __forceinline__ bool kv_part_unit_ok(const KvAttn &a, const KvUnit &u, int start) {

@@ -277,10 +277,13 @@ struct SharedForm {
     int rows_max, tok_stride, seg_blocks, pre_blocks;
     int64_t n_seg, n_pre, pieces;
 };
-int suffix_seg_blocks(const gdn_attn_desc *d, bool few) {
-    return d->in_dtype == GDN_FP32 ? 8 : few ? seg_blocks(d, true, 1) : 64;
+// Own keys of few rows: 256 keys, a block a warp, and the open block apart, as there is little of them and a CTA's time is
+// that of its longest chain of reads.
+int suffix_seg_blocks(const gdn_attn_desc *d, bool few) { return d->in_dtype == GDN_FP32 ? 8 : few ? 4 : 64; }
+int64_t suffix_segs(const gdn_attn_desc *d, int64_t max_suffix, bool few) {
+    const int seg = suffix_seg_blocks(d, few);
+    return ((max_suffix - 1) / kKvBlock + seg - 1) / seg + 1 + (few ? 1 : 0);
 }
-int64_t suffix_segs(int64_t max_suffix, int seg) { return ((max_suffix - 1) / kKvBlock + seg - 1) / seg + 1; }
 int64_t most_shared(int64_t max_len) { return std::max<int64_t>((max_len - 1) / kKvBlock, 1); }
 int64_t least_pieces(int64_t blocks) { return (blocks + gdn::kKvMaxSegBlocks - 1) / gdn::kKvMaxSegBlocks; }
 SharedForm shared_form(const gdn_attn_desc *d, int64_t n_rows, int64_t n_groups, int64_t max_new, int64_t max_len, int64_t max_suffix) {
@@ -290,7 +293,7 @@ SharedForm shared_form(const gdn_attn_desc *d, int64_t n_rows, int64_t n_groups,
     f.rows_max = f.tok_stride * G;
     f.few = max_new * G <= kFewRows && d->in_dtype == GDN_BF16;
     f.seg_blocks = suffix_seg_blocks(d, f.few);
-    f.n_seg = suffix_segs(max_suffix, f.seg_blocks);
+    f.n_seg = suffix_segs(d, max_suffix, f.few);
     const int64_t tiles = std::min((n_rows * G + n_groups * (R - 1)) / R, n_rows * G), items = tiles * d->n_kv_heads;
     const int64_t blocks = most_shared(max_len), least = least_pieces(blocks), rows = n_rows * d->n_q_heads;
     f.n_pre = std::min(blocks, std::max(least, (int64_t)kSharedPieces * R / rows));
@@ -354,7 +357,7 @@ GDN_API size_t gdn_kv_shared_workspace(const gdn_attn_desc *d, int64_t max_rows,
     // shared_form: no more segments than make row tiles that fill the SMs twice, unless those of the longest kind are more
     const int64_t rows = std::max<int64_t>(max_rows, 1) * d->n_q_heads;
     const int64_t pre = std::max(least_pieces(most_shared(max_len)) * rows, (int64_t)kSharedPieces * many_rows(d));
-    const int64_t own = std::max(suffix_segs(max_suffix, suffix_seg_blocks(d, true)), suffix_segs(max_suffix, suffix_seg_blocks(d, false)));
+    const int64_t own = std::max(suffix_segs(d, max_suffix, true), suffix_segs(d, max_suffix, false));
     return kWsSlack + 256 + (size_t)(pre + own * rows) * (d->head_dim * sizeof(float) + sizeof(float2));
 }
 
@@ -401,6 +404,7 @@ GDN_API gdn_status gdn_kv_attention_shared(const gdn_attn_desc *d, const gdn_kv_
     a.max_suffix = (int)max_suffix;
     a.part_rows = n_rows * a.Hq;
     a.head_dim = d->head_dim;
+    a.own_apart = f.few;
     char *ws = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
     const bool bf16 = d->in_dtype == GDN_BF16;
     a.cut = g->max_groups > 1 ? reinterpret_cast<int *>(ws) : nullptr;

@@ -128,7 +128,9 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
     const KvUnit u = kv_load_unit(a.units, ui);   // inside the map whatever the count
     if (ui >= a.counts[0]) return;
     const int start = PART == kKvSuffix ? a.starts[ui] : 0;   // the first block of the pass
-    const int seg0 = kv_part_seg0<PART>(a, start), last_seg = u.block / a.seg_blocks;
+    // own keys past shared ones: a short pass, so the rows' own block is a segment (and a CTA) by itself
+    const int seg0 = kv_part_seg0<PART>(a, start);
+    const int last_seg = PART == kKvSuffix ? seg0 + kv_own_segs(a, u.block, start) - 1 : u.block / a.seg_blocks;
     const int n_row = u.count * a.G;
     if (!kv_part_unit_ok<PART>(a, u, start) || n_row > R) {
         if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(const KvAttn a) {
     const KvUnit u = kv_load_unit(a.units, ui);   // inside the map whatever the count
     const int start = a.starts[ui], cut = a.cut ? *a.cut : a.pre_blocks;
     if (ui >= a.counts[0] || !kv_suffix_unit_ok(a, u, start)) return;
-    const int pre = (start + cut - 1) / cut, n = pre + u.block / a.seg_blocks - start / a.seg_blocks + 1;
+    const int pre = (start + cut - 1) / cut, n = pre + kv_own_segs(a, u.block, start);
     constexpr int V = D == 64 ? 2 : 4, N = D / (32 * V), B = W == 8 ? 4 : 2;   // B segments loaded together
     __shared__ float so[W > 1 ? W : 1][D], sl[W > 1 ? W : 1];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, mine = warp % W;
