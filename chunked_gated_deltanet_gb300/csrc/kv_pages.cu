@@ -54,8 +54,8 @@ __device__ int cluster_exclusive(int x, int *ws, int *total) {
 
 // ---- forks and releases ----
 
-struct ForkPair {
-    int src, dst, len, buf;   // len: the source's (0 of a release), buf: the tail buffer that the slot then has
+struct __align__(16) ForkPair {
+    int src, dst, now, before;   // slots; complete blocks that dst will name, and names
 };
 
 // Whether a batch's pairs are sound: slots in range, no slot twice among dst, no dst among src. Every CTA looks for itself.
@@ -89,7 +89,8 @@ __global__ void __launch_bounds__(kPageThreads) kv_fork_batch_kernel(const KvCac
     grid_dep_launch();
     extern __shared__ __align__(16) unsigned char fork_smem[];
     __shared__ int ws[34], most;
-    unsigned *bits = reinterpret_cast<unsigned *>(fork_smem);
+    ForkPair *pairs = reinterpret_cast<ForkPair *>(fork_smem);
+    unsigned *bits = reinterpret_cast<unsigned *>(pairs + n);
     const int t = threadIdx.x;
     const int2 *state = reinterpret_cast<const int2 *>(c.state);
     if (!fork_batch_ok(src, dst, n, c.n_slots, bits)) {
@@ -111,39 +112,48 @@ __global__ void __launch_bounds__(kPageThreads) kv_fork_batch_kernel(const KvCac
     }
     const int rank = blockIdx.x, first = rank * kPageThreads + t;
     constexpr int kAll = kPageCluster * kPageThreads;
-    // the most blocks that a pair has to do with, before and after
+    // the pairs, and the most blocks that one has to do with
     if (t == 0) most = 0;
     __syncthreads();
     for (int i = t; i < n; i += kPageThreads) {
-        const int s = src[i];
-        const int len = max(max(s >= 0 ? state[s].x : 0, state[dst[i]].x), 0);
-        atomicMax(&most, min(len / kKvBlock, c.max_blocks));
+        const int s = src[i], d = dst[i];
+        auto blocks = [&](int slot) { return min(max(state[slot].x, 0) / kKvBlock, c.max_blocks); };
+        const ForkPair p = {s, d, s >= 0 ? blocks(s) : 0, blocks(d)};
+        pairs[i] = p;
+        atomicMax(&most, max(p.now, p.before));
     }
     const int n_free = *c.n_free;
     __syncthreads();
-    const int nb = most;
+    const unsigned nb = most;
     const int64_t entries = (int64_t)n * nb;
-    auto blocks_of = [&](int slot) { return min(max(state[slot].x, 0) / kKvBlock, c.max_blocks); };
-    for (int64_t e = first; e < entries; e += kAll) {
-        const int i = (int)(e / nb), b = (int)(e - (int64_t)i * nb), s = src[i];
-        if (s < 0 || b >= blocks_of(s)) continue;
-        const int page = c.table[(int64_t)s * c.max_blocks + b];
-        if ((unsigned)page < (unsigned)c.n_pages) atomicAdd(&c.refs[page], 1);
-    }
-    cluster_sync();
-    int freed = 0;
-    for (int64_t e = first; e < entries; e += kAll) {
-        const int i = (int)(e / nb), b = (int)(e - (int64_t)i * nb), s = src[i], d = dst[i];
-        int32_t *mine = c.table + (int64_t)d * c.max_blocks + b;
-        if (b < blocks_of(d)) {
-            const int page = *mine;
-            if ((unsigned)page < (unsigned)c.n_pages && atomicSub(&c.refs[page], 1) == 1) {
-                c.refs[page] = kFreedMark;
-                ++freed;
+    // f(pair, block) over all of them, four a thread under way
+    auto each = [&](auto f) {
+        for (int64_t e0 = first; e0 < entries; e0 += 4 * kAll) {
+            int64_t e = e0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k, e += kAll) {
+                if (e >= entries) break;
+                const int i = entries <= UINT32_MAX ? (int)((unsigned)e / nb) : (int)(e / nb);
+                f(pairs[i], (int)(e - (int64_t)i * nb));
             }
         }
-        if (s >= 0 && b < blocks_of(s)) *mine = c.table[(int64_t)s * c.max_blocks + b];
-    }
+    };
+    each([&](const ForkPair &p, int b) {
+        if (b >= p.now) return;
+        const int page = c.table[(int64_t)p.src * c.max_blocks + b];
+        if ((unsigned)page < (unsigned)c.n_pages) atomicAdd(&c.refs[page], 1);
+    });
+    cluster_sync();
+    int freed = 0;
+    each([&](const ForkPair &p, int b) {
+        int32_t *mine = c.table + (int64_t)p.dst * c.max_blocks + b;
+        const int to = b < p.now ? c.table[(int64_t)p.src * c.max_blocks + b] : -1, page = b < p.before ? *mine : -1;
+        if ((unsigned)page < (unsigned)c.n_pages && atomicSub(&c.refs[page], 1) == 1) {
+            c.refs[page] = kFreedMark;
+            ++freed;
+        }
+        if (b < p.now) *mine = to;
+    });
     int total;
     cluster_exclusive(freed, ws, &total);   // and the barrier after the last read of the old states
     for (int i = first; i < n; i += kAll) {
@@ -297,9 +307,10 @@ cudaError_t launch_clusters(void (*kernel)(K...), unsigned grid, size_t smem, cu
 cudaError_t gdn_launch_kv_fork_batch(const gdn::KvCache &c, const int32_t *src, const int32_t *dst, int n, int Hkv, int d, int elt,
                                      unsigned *err, cudaStream_t st) {
     using namespace gdn;
-    const size_t smem = ((size_t)c.n_slots + 31) / 32 * 4;
+    const size_t smem = (size_t)n * sizeof(ForkPair) + ((size_t)c.n_slots + 31) / 32 * 4;
     if (smem > 32 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kv_fork_batch_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvMaxBatchSlots / 8);
+        const cudaError_t e = cudaFuncSetAttribute(kv_fork_batch_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)(kKvMaxRequests * sizeof(ForkPair) + kKvMaxBatchSlots / 8));
         if (e != cudaSuccess) return e;
     }
     const int64_t tasks = (int64_t)n * 2 * Hkv;   // copies, an eighth of a cluster each
