@@ -2,7 +2,9 @@
 fork into branches, and single tokens for all branches from one CUDA graph.
 
 Per session the GDN layer keeps its state (S, conv) and the attention layer its keys and values, in 8-bit pages of 64
-tokens that branches share. Weights and inputs are random: the layers' outputs stand in for token embeddings.
+tokens that branches share: they are forked in one call, and their tokens attend to the shared pages together. Queries
+and keys are normalised and rotated in half of each head on their way out of the q/k/v product. Weights and inputs are
+random: the layers' outputs stand in for token embeddings.
 
     python examples/hybrid_session.py [--turn 2048] [--branches 8] [--steps 64]
 """
@@ -35,6 +37,9 @@ class HybridBlock:
         self.A_log, self.dt_bias = rand(hv, scale=0.2), rand(hv, scale=0.2)
         self.w_gdn_out = rand(hv * 128, HIDDEN, scale=HIDDEN ** -0.5).to(BF)
         self.w_qkv = rand(HIDDEN, (8 + 2 * 2) * 128, scale=HIDDEN ** -0.5).to(BF)
+        self.q_norm, self.k_norm = (1 + rand(128, scale=0.1)).to(BF), (1 + rand(128, scale=0.1)).to(BF)
+        self.rope = gdn.make_rope_desc(64, gdn.GDN_ROPE_HALF, 1e6)
+        self.rope_table = gdn.rope_table(self.rope, self.dev)
         self.w_attn_out = rand(8 * 128, HIDDEN, scale=HIDDEN ** -0.5).to(BF)
         # what the sessions hold, and the scratch of a call
         self.states = [gdn.Session(self.gd, self.dev) for _ in range(n_sessions)]
@@ -43,6 +48,8 @@ class HybridBlock:
         self.plan = gdn.KvPlan.new(max_tokens, n_sessions, self.dev)
         self.gdn_ws = gdn.workspace(self.gd, max_tokens, 1, self.dev)
         self.attn_ws = gdn.kv_attention_workspace(self.ad, max_tokens, n_sessions, max_len, self.dev)
+        self.groups = gdn.KvGroups.new(self.plan, 1)
+        self.shared_ws = gdn.kv_shared_workspace(self.ad, n_sessions, max_len, max_len, self.dev)
 
     def _gdn_inputs(self, x):
         n, hk, hv = x.shape[0], self.gd.n_qk_heads * 128, self.gd.n_v_heads
@@ -52,15 +59,24 @@ class HybridBlock:
         gdn.gdn_gates(self.gd, a, b, self.A_log, self.dt_bias, a, b)
         return q, k, v, a, b, torch.empty((n, hv, 128), dtype=BF, device=self.dev)
 
-    def _attention(self, x, slots, counts, max_new):
-        """slots, counts: int32 on the GPU; x in their order. One plan serves every attention layer of a model."""
+    def _attention(self, x, slots, counts, max_new, family=None):
+        """slots, counts: int32 on the GPU; x in their order. family: [0, n] on the GPU where all requests are forks of one
+        session. One plan, with its positions and groups, serves every attention layer of a model."""
         n = x.shape[0]
-        q, k, v = (t.reshape(n, -1, 128).contiguous() for t in
-                   (torch.nn.functional.rms_norm(x, (HIDDEN,)) @ self.w_qkv).split([1024, 256, 256], 1))
-        out = torch.empty_like(q)
         gdn.gdn_kv_plan(self.ad, self.cache, slots, counts, self.plan)
+        pos = torch.empty(n, dtype=torch.int32, device=self.dev)
+        gdn.gdn_kv_positions(self.plan, pos)
+        qkv = (torch.nn.functional.rms_norm(x, (HIDDEN,)) @ self.w_qkv).view(n, 12, 128).split([8, 2, 2], 1)
+        q, k, v = (torch.empty((n, h, 128), dtype=BF, device=self.dev) for h in (8, 2, 2))
+        gdn.gdn_rope(self.ad, self.rope, self.rope_table, pos, qkv[0], qkv[1], q, k, qkv[2], v, self.q_norm, self.k_norm)
         gdn.gdn_kv_append(self.ad, self.cache, self.plan, k, v)
-        gdn.gdn_kv_attention(self.ad, self.cache, self.plan, q, k, v, out, self.attn_ws, max_new, self.max_len)
+        out = torch.empty_like(q)
+        if family is None:
+            gdn.gdn_kv_attention(self.ad, self.cache, self.plan, q, k, v, out, self.attn_ws, max_new, self.max_len)
+        else:
+            gdn.gdn_kv_group(self.ad, self.cache, self.plan, family, self.groups)
+            gdn.gdn_kv_attention_shared(self.ad, self.cache, self.plan, self.groups, q, k, v, out, self.shared_ws, max_new,
+                                        self.max_len, self.max_len)
         return x + out.reshape(n, -1) @ self.w_attn_out
 
     def prompt(self, session: int, x):
@@ -72,17 +88,19 @@ class HybridBlock:
         i32 = lambda v: torch.tensor([v], dtype=torch.int32, device=self.dev)   # noqa: E731
         return self._attention(x, i32(session), i32(len(x)), len(x))
 
-    def fork(self, src: int, dst: int):
-        """dst continues where src is: a copy of the GDN state, and src's complete blocks by reference."""
-        gdn.gdn_state_restore(self.gd, self.states[dst], self.states[src])
-        gdn.gdn_kv_fork(self.ad, self.cache, src, dst)
+    def fork(self, src: int, dst):
+        """The sessions dst continue where src is: copies of the GDN state, and src's complete blocks by reference."""
+        for s in dst:
+            gdn.gdn_state_restore(self.gd, self.states[s], self.states[src])
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=self.dev)   # noqa: E731
+        gdn.gdn_kv_fork_batch(self.ad, self.cache, i32([src] * len(dst)), i32(list(dst)))
 
-    def token(self, sessions, slots, ones, x):
-        """The next token of every session; captures in a CUDA graph."""
+    def token(self, sessions, slots, ones, x, family):
+        """The next token of every session, all of them forks of one; captures in a CUDA graph."""
         q, k, v, g, beta, out = self._gdn_inputs(x)
         gdn.gdn_decode_step(self.gd, [self.states[s] for s in sessions], q, k, v, g, beta, self.conv_w, out)
         x = x + out.reshape(len(x), -1) @ self.w_gdn_out
-        return self._attention(x, slots, ones, 1)
+        return self._attention(x, slots, ones, 1, family)
 
 
 def run(turn=2048, branches=8, steps=64, device="cuda"):
@@ -95,22 +113,22 @@ def run(turn=2048, branches=8, steps=64, device="cuda"):
     draw = lambda k: torch.randn((k, HIDDEN), generator=gen).to(BF).to(dev)   # noqa: E731
     for x in (draw(turn), draw(turn)):
         m.prompt(0, x)
-    for s in range(1, n):
-        m.fork(0, s)
+    m.fork(0, range(1, n))
     if gdn.gdn_kv_status(m.plan) != gdn.GDN_OK:
         raise RuntimeError("the cache is too small")
     families = [list(range(branches)), list(range(branches, n))]
     slots = [torch.tensor(f, dtype=torch.int32, device=dev) for f in families]
     ones = torch.ones(branches, dtype=torch.int32, device=dev)
+    family = torch.tensor([0, branches], dtype=torch.int32, device=dev)
     x0 = draw(branches)
     want, x = [], x0
     for _ in range(steps):
-        x = m.token(families[0], slots[0], ones, x)
+        x = m.token(families[0], slots[0], ones, x, family)
         want.append(x)
     buf = x0.clone()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        buf.copy_(m.token(families[1], slots[1], ones, buf))
+        buf.copy_(m.token(families[1], slots[1], ones, buf, family))
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     got = torch.empty((steps, *buf.shape), dtype=BF, device=dev)
     start.record()
