@@ -298,9 +298,11 @@ SharedForm shared_form(const gdn_attn_desc *d, int64_t n_rows, int64_t n_groups,
     const int64_t blocks = most_shared(max_len), least = least_pieces(blocks), rows = n_rows * d->n_q_heads;
     f.n_pre = std::min(blocks, std::max(least, (int64_t)kSharedPieces * R / rows));
     f.pre_blocks = gdn::kKvMaxSegBlocks;
-    f.pieces = std::max(items * least, std::min(items * f.n_pre, items + kSharedPieces));
-    if (n_groups > 32) f.pieces = std::min(items * f.n_pre, std::max(f.pieces, items * ((blocks + 31) / 32)));
+    // several groups: the CTAs of one wave, as those that find no piece cost an SM some 4 us each, or what the longest cut makes
+    f.pieces = std::max(items * least, std::min(items * f.n_pre, (int64_t)gdn::kSharedSms));
+    if (n_groups > gdn::kSharedGroups) f.pieces = items * std::min(f.n_pre, (blocks + gdn::kSharedManyCut - 1) / gdn::kSharedManyCut);
     if (n_groups == 1) {
+        f.pieces = std::max(items * least, std::min(items * f.n_pre, items + kSharedPieces));
         const double part = (double)rows * 8 * d->head_dim / 3.6e6;   // of a segment: in blocks of about 0.9 us
         double best = 0;
         int64_t best_p = least;

@@ -8,6 +8,7 @@ namespace gdn {
 
 constexpr int kSharedSms = 152;        // pieces at a time, one an SM
 constexpr int kSharedPieceCost = 12;   // a piece's own time, in blocks
+constexpr int kSharedGroups = 32, kSharedManyCut = 128;   // groups whose cut is searched for; the cut of more groups
 
 // Blocks of a piece: those that make the fullest use of the SMs with no more pieces than the launch has CTAs. A lane tries a
 // number of segments of the longest group. The same in every CTA and for the join, which reads it from *a.cut. One group: the
@@ -18,7 +19,7 @@ __device__ int kv_shared_cut(const KvAttn &a, int tiles, int blocks) {   // of t
     if (a.n_groups == 1) return a.pre_blocks;
     const int longest = __reduce_max_sync(0xffffffffu, blocks);
     const int least = min(max((longest + a.n_pre - 1) / a.n_pre, 1), kKvMaxSegBlocks);
-    if (a.n_groups > 32) return max(least, 32);   // many groups fill the SMs by themselves
+    if (a.n_groups > kSharedGroups) return max(least, kSharedManyCut);   // they fill the SMs by themselves
     // a segment more costs every row a partial result written and read again: in blocks of about 0.9 us
     const float part = (float)a.part_rows * (8.f * a.head_dim) / 3.6e6f;
     float best = INFINITY;
