@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     if constexpr (PART == kKvShared) {
         // a group's rows as those of one unit that starts where the shared blocks end: every row sees all of them
         int4 rec;
-        if (!kv_shared_piece<P::R>(a, blockIdx.x, r0, h, seg, cut, rec)) return;
+        if (!kv_shared_piece<P::R>(a, r0, h, seg, cut, rec)) return;
         if (!kv_group_ok(a, rec)) {
             if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
             return;
@@ -286,10 +286,8 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
         // and the 32 stores of a piece fill four K-major core matrices (8 rows x 16 bytes) side by side, free of conflicts ----
         constexpr int NP = D / 32, STEP = P::kKeys0 / 32 * 8;
         const int c = lane & 3;
-#pragma unroll 1
-        for (int rb = warp * 8; rb < nt * 128; rb += STEP) {
-            const int r = rb + (lane >> 2), rr = r0 + r;
-            uint4 w[NP];
+        auto load_row = [&](int r, uint4 (&w)[NP]) {
+            const int rr = r0 + r;
             if (r < rows_here) {
                 const int tok = rr / a.G;
                 const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const bf *>(a.q) +
@@ -300,6 +298,8 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
 #pragma unroll
                 for (int i = 0; i < NP; ++i) w[i] = make_uint4(0, 0, 0, 0);
             }
+        };
+        auto put_row = [&](int r, const uint4 (&w)[NP]) {
             float f[8], top = 0.f;
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
@@ -320,6 +320,24 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 *reinterpret_cast<uint4 *>(dst + 512 * i) = f8_to_h8(f);
             }
             if (c == 0) row_q[r] = back;
+        };
+        const int r1 = warp * 8 + (lane >> 2);
+        if constexpr (PART == kKvShared && P::NQ == 2) {   // short passes: every row under way before the first is put down
+            constexpr int IT = (P::R + STEP - 1) / STEP;
+            uint4 w[IT][NP];
+#pragma unroll
+            for (int i = 0; i < IT; ++i)
+                if (r1 + i * STEP < nt * 128) load_row(r1 + i * STEP, w[i]);
+#pragma unroll
+            for (int i = 0; i < IT; ++i)
+                if (r1 + i * STEP < nt * 128) put_row(r1 + i * STEP, w[i]);
+        } else {
+#pragma unroll 1
+            for (int r = r1; r < nt * 128; r += STEP) {
+                uint4 w[NP];
+                load_row(r, w);
+                put_row(r, w);
+            }
         }
         if constexpr (P::kQT) {   // each softmax thread its row, from the slots into TMEM
             kv_named_barrier(3, P::kKeys0);
@@ -425,10 +443,12 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 w[i] = __ldg(reinterpret_cast<const uint4 *>(src + j / P::kVec * (8 * D) + j % P::kVec * 64));
             }
         };
-        // pages and scales of the pass's blocks, which the softmax warps read as well; with d = 256 the first block's loads
-        // before them (2.5 % of 290 x 16 rows over 41,802 keys; the two-tile form has no registers left for that: 6 % slower)
+        // pages and scales of the pass's blocks, which the softmax warps read as well; with d = 256 and over shared blocks the
+        // first block's loads before them (2.5 % of 290 x 16 rows over 41,802 keys; the two-tile form over whole contexts has no
+        // registers left for that: 6 % slower)
         const int32_t *table = a.c.table + (int64_t)u.slot * a.c.max_blocks;
-        if (P::kQT && n8 > 0) {
+        constexpr bool kEarly = P::kQT || PART == kKvShared;
+        if (kEarly && n8 > 0) {
             int page = table[c0];
             if ((unsigned)page >= (unsigned)a.c.n_pages) page = 0;
             load_from((is_v ? a.c.v : a.c.k) + ((int64_t)page * a.Hkv + h) * (kKvBlock * D) + (lane >> 2) * D + (lane & 3) * 16, warp % P::CW);
@@ -557,7 +577,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
                 }
             }
         };
-        if (!P::kQT) load(0);
+        if (!kEarly) load(0);
 #pragma unroll 1
         for (int n = 0; n < nb; ++n) {
             const int slot = n % NS;
@@ -786,7 +806,7 @@ cudaError_t launch_prompt(const KvAttn &a, int n_units, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kv_attn_prompt_kernel<D, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::kBytes);
     if (e != cudaSuccess) return e;
     if constexpr (PART == kKvShared) {
-        e = gdn_launch_pdl(kv_attn_prompt_kernel<D, PART>, dim3((unsigned)n_units), P::NT, P::kBytes, st, a, 1, 1, n_units);
+        e = gdn_launch_pdl(kv_attn_prompt_kernel<D, PART>, kv_shared_grid(a, n_units), P::NT, P::kBytes, st, a, 1, 1, n_units);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     // blocks of a span: enough rows to fill the tile where a block's tokens are too few (G = 1, 2), a power of two <= 4

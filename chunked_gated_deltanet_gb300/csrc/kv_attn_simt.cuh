@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int r
     if constexpr (PART == kKvShared) {
         // a group's rows as those of one unit that starts where the shared blocks end: every row sees all of them
         int4 rec;
-        if (!kv_shared_piece<R>(a, blockIdx.x, r0, h, seg, cut, rec)) return;
+        if (!kv_shared_piece<R>(a, r0, h, seg, cut, rec)) return;
         if (!kv_group_ok(a, rec)) {
             if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
             return;
@@ -293,7 +293,7 @@ cudaError_t launch_simt_many(const KvAttn &a, int n, int rows_max, cudaStream_t 
     const cudaError_t e = cudaFuncSetAttribute(kv_attn_simt_kernel<D, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::kBytes);
     if (e != cudaSuccess) return e;
     const int row_tiles = PART == kKvShared ? 1 : (rows_max + P::R - 1) / P::R;
-    const dim3 grid = PART == kKvShared ? dim3((unsigned)n) : dim3((unsigned)((int64_t)n * row_tiles), (unsigned)a.Hkv, (unsigned)a.n_seg);
+    const dim3 grid = PART == kKvShared ? kv_shared_grid(a, n) : dim3((unsigned)((int64_t)n * row_tiles), (unsigned)a.Hkv, (unsigned)a.n_seg);
     return gdn_launch_pdl(kv_attn_simt_kernel<D, PART>, grid, 256, P::kBytes, st, a, row_tiles);
 }
 

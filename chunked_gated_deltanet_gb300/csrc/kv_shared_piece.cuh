@@ -11,12 +11,11 @@ constexpr int kSharedPieceCost = 12;   // a piece's own time, in blocks
 constexpr int kSharedGroups = 32, kSharedManyCut = 128;   // groups whose cut is searched for; the cut of more groups
 
 // Blocks of a piece: those that make the fullest use of the SMs with no more pieces than the launch has CTAs. A lane tries a
-// number of segments of the longest group. The same in every CTA and for the join, which reads it from *a.cut. One group: the
-// host's choice, made the same way (kv_api.cu).
+// number of segments of the longest group. The same in every CTA and for the join, which reads it from *a.cut. (One group: the
+// host's choice, made the same way, kv_api.cu.)
 template <int R>
 __device__ int kv_shared_cut(const KvAttn &a, int tiles, int blocks) {   // of the lane's group
     const int lane = threadIdx.x & 31;
-    if (a.n_groups == 1) return a.pre_blocks;
     const int longest = __reduce_max_sync(0xffffffffu, blocks);
     const int least = min(max((longest + a.n_pre - 1) / a.n_pre, 1), kKvMaxSegBlocks);
     if (a.n_groups > kSharedGroups) return max(least, kSharedManyCut);   // they fill the SMs by themselves
@@ -45,11 +44,21 @@ __device__ int kv_shared_cut(const KvAttn &a, int tiles, int blocks) {   // of t
     return best_cut;
 }
 
-// Piece p: its group's record, first row of the tile, kv head and segment of `cut` blocks; false past the last one. The row
-// tiles of the same blocks follow one another, so that CTAs that run together read the same pages.
+// This CTA's piece: its group's record, first row of the tile, kv head and segment of `cut` blocks; false where there is none.
+// One group: the launch's grid is (row tiles, kv heads, segments). Several: the CTA's number counts the pieces off, the row
+// tiles of the same blocks in a row, so that CTAs that run together read the same pages (as the grid of one group has it).
 template <int R>
-__device__ bool kv_shared_piece(const KvAttn &a, int p, int &r0, int &h, int &seg, int &cut, int4 &rec) {
+__device__ bool kv_shared_piece(const KvAttn &a, int &r0, int &h, int &seg, int &cut, int4 &rec) {
     const int lane = threadIdx.x & 31;
+    if (a.n_groups == 1) {
+        rec = a.groups[0];
+        cut = a.pre_blocks;
+        r0 = (int)blockIdx.x * R;
+        h = blockIdx.y;
+        seg = blockIdx.z;
+        return rec.w > 0 && r0 < (int64_t)rec.y * a.G && (int64_t)seg * cut < min(rec.w, (a.max_len - 1) / kKvBlock);
+    }
+    int p = blockIdx.x;
     for (int g0 = 0; g0 < a.n_groups; g0 += 32) {
         int4 r = make_int4(0, 0, 0, 0);
         if (g0 + lane < a.n_groups) r = a.groups[g0 + lane];
@@ -60,7 +69,7 @@ __device__ bool kv_shared_piece(const KvAttn &a, int p, int &r0, int &h, int &se
             int longest = blocks;   // more than 32 groups: the longest of all
             for (int g = 32 + lane; g < a.n_groups; g += 32) longest = max(longest, min(a.groups[g].w, most));
             cut = kv_shared_cut<R>(a, tiles, a.n_groups > 32 ? longest : blocks);
-            if (p == 0 && threadIdx.x == 0 && a.cut) *a.cut = cut;
+            if (blockIdx.x == 0 && threadIdx.x == 0) *a.cut = cut;
         }
         const int segs = (blocks + cut - 1) / cut;
         const int here = tiles * a.Hkv * segs;
@@ -90,6 +99,12 @@ __device__ bool kv_shared_piece(const KvAttn &a, int p, int &r0, int &h, int &se
         p -= __shfl_sync(0xffffffffu, upto, 31);
     }
     return false;
+}
+
+// The launch's grid.
+inline dim3 kv_shared_grid(const KvAttn &a, int n_pieces) {
+    if (a.n_groups > 1) return dim3((unsigned)n_pieces);
+    return dim3((unsigned)(n_pieces / (a.Hkv * a.n_pre)), (unsigned)a.Hkv, (unsigned)a.n_pre);
 }
 
 }  // namespace gdn
