@@ -41,12 +41,8 @@ __device__ int cluster_exclusive(int x, int *ws, int *total) {
     cluster_sync();
     const cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), n = (int)cl.num_blocks();
-    int before = 0, sum = 0;
-    for (int i = 0; i < n; ++i) {
-        const int v = *cl.map_shared_rank(&ws[32], i);
-        if (i < rank) before += v;
-        sum += v;
-    }
+    const int v = lane < n ? *cl.map_shared_rank(&ws[32], lane) : 0;   // a lane a CTA
+    const int sum = __reduce_add_sync(0xffffffffu, v), before = __reduce_add_sync(0xffffffffu, lane < rank ? v : 0);
     cluster_sync();   // every CTA has read the others' sums
     *total = sum;
     return before + (warp > 0 ? ws[warp - 1] : 0) + in - x;
