@@ -1,6 +1,6 @@
 // Attention of many query rows over the paged 8-bit key/value cache on the 5th-generation tensor core (bf16 inputs).
 //
-// The mathematics is that of kv_attn_simt.cu; here the two products of a block of 64 keys are tcgen05 MMAs:
+// The mathematics is that of kv_attn_simt.cuh; here the two products of a block of 64 keys are tcgen05 MMAs:
 //   S = Q K^T     128 rows x 64 keys, K = d, operands fp16 in shared memory. A row of Q is scaled by a power of two to a
 //                 largest element in [2^14, 2^15), which is exact (but for elements 2^-32 of the largest), and taken out
 //                 of the scores again. An int8 key is exact in fp16. A key of the row's own block, which is read as it
@@ -31,10 +31,17 @@
 // after their first block. Every decision is a row's own and every block is one softmax step, so a row's bits do
 // not depend on the rows beside it.
 //
+// Built for each part (KvPart): whole contexts; a request's own keys past the blocks that its group shares, from the first of
+// them on; and a group's shared blocks (kv_shared_piece.cuh), where rows are the group's, in tiles that go across its requests,
+// no row has a mask and no block is raw, and the loop is that much shorter.
+//
 // Bound: the softmax warps' issue slots and the tensor core about evenly, 1,700 cycles for a block of 64 keys and two row
 // tiles (1,900 with a segment's start and end), of which the products are 1,280: the scores' 768, as their MMAs of 64 keys
 // take 48 cycles each, and the values' 512. 4,000 x 16 rows over 37,802 keys (d = 128): 1.10 ms, 1.18 PFLOP/s, tensor pipe
 // 51 %; 290 x 16 rows over 41,802 keys (d = 256): 217 us, 0.92 PFLOP/s; the same turn with d = 64: 0.93 ms.
+// Shared blocks: 8,000 x 16 rows over 37,760 keys (d = 128) 1.71 ms, 1.45 PFLOP/s, tensor pipe 59 %; 64 x 16 rows over 41,792
+// keys (d = 256, 35 blocks a CTA) 50 us, 0.88 PFLOP/s, a quarter of it start and end. Tried there and slower: two threads a row
+// (a block's cost is not its elements'), persistent CTAs that walk a list of pieces (2.0 ms: the issuing warps' waits grow).
 #pragma once
 
 #include "kv_attn.cuh"

