@@ -135,9 +135,14 @@ __device__ __forceinline__ int64_t kv_shared_part_row(const KvAttn &a, int seg, 
     return seg * a.part_rows + row * a.Hq + head;
 }
 
-// A group's record inside the sizes that the call was given (its blocks past the launch's segments are seen by no unit).
+// A group's record, its rows no more than the call's (those past them are of units that are left out).
+__device__ __forceinline__ int4 kv_load_group(const KvAttn &a, int g) {
+    int4 r = a.groups[g];
+    r.y = r.x < 0 ? 0 : (int)min((int64_t)r.y, max(a.n_rows - r.x, (int64_t)0));
+    return r;
+}
 __device__ __forceinline__ bool kv_group_ok(const KvAttn &a, const int4 &r) {
-    return r.x >= 0 && (int64_t)r.x + r.y <= a.n_rows && (unsigned)r.z < (unsigned)a.c.n_slots && r.w <= a.c.max_blocks;
+    return (unsigned)r.z < (unsigned)a.c.n_slots && r.w <= a.c.max_blocks;
 }
 
 // Row of the partial results: (unit, token of the unit, query head) of a segment.

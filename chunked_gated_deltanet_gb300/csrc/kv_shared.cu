@@ -41,20 +41,24 @@ __global__ void __launch_bounds__(kGroupThreads) kv_group_kernel(const KvCache c
         return;
     }
     const int n_units = min(counts[0], max_units);
-    const int b0 = bounds[g], b1 = bounds[g + 1];
     if (t == 0) {
         n_slots = before0 = before1 = 0;
         first = common = INT32_MAX;
     }
-    int row0 = 0, row1 = 0;
-    const bool in = n_units > 0 && b0 >= 0 && b0 <= b1 && b1 <= max_requests;
-    if (in) {
-        row0 = rows[b0];
-        row1 = rows[b1];
+    // the bounds of all groups, requests and rows: one out of order or range and none shares anything, as groups could overlap
+    bool bad = false;
+    for (int i = t; n_units > 0 && i < n_groups; i += kGroupThreads) {
+        const int from = bounds[i], to = bounds[i + 1];
+        bad = bad || from < 0 || from > to || to > max_requests || rows[max(min(from, max_requests), 0)] < 0 ||
+              rows[max(min(from, max_requests), 0)] > rows[max(min(to, max_requests), 0)];
     }
-    bool ok = n_units <= 0 || (in && row0 >= 0 && row0 <= row1);
+    int row0 = 0, row1 = 0;
+    if (n_units > 0) {
+        row0 = rows[max(min(bounds[g], max_requests), 0)];
+        row1 = rows[max(min(bounds[g + 1], max_requests), 0)];
+    }
+    bool ok = __syncthreads_or(bad) == 0;
     if (!ok) row0 = row1 = 0;
-    __syncthreads();
     // the group's units: those before its first row and before its end, the first block of any, a slot per request
     int n0 = 0, n1 = 0, low = INT32_MAX;
     for (int i = t; i < n_units; i += kGroupThreads) {
@@ -63,7 +67,7 @@ __global__ void __launch_bounds__(kGroupThreads) kv_group_kernel(const KvCache c
         n1 += u.row < row1;
         if (u.row < row0 || u.row >= row1) continue;
         low = min(low, u.block);
-        if (u.row == row0 || units[8 * (int64_t)(i - 1)] != u.slot) {   // a request's first unit stands for it
+        if (i == 0 || u.row == row0 || units[8 * (int64_t)(i - 1)] != u.slot) {   // a request's first unit stands for it
             const int k = atomicAdd(&n_slots, 1);
             if (k < kKvMaxRequests) slots[k] = u.slot;
         }

@@ -51,23 +51,23 @@ template <int R>
 __device__ bool kv_shared_piece(const KvAttn &a, int &r0, int &h, int &seg, int &cut, int4 &rec) {
     const int lane = threadIdx.x & 31;
     if (a.n_groups == 1) {
-        rec = a.groups[0];
+        rec = kv_load_group(a, 0);
         cut = a.pre_blocks;
         r0 = (int)blockIdx.x * R;
         h = blockIdx.y;
         seg = blockIdx.z;
-        return rec.w > 0 && r0 < (int64_t)rec.y * a.G && (int64_t)seg * cut < min(rec.w, (a.max_len - 1) / kKvBlock);
+        return rec.w > 0 && rec.y > 0 && r0 < (int64_t)rec.y * a.G && (int64_t)seg * cut < min(rec.w, (a.max_len - 1) / kKvBlock);
     }
     int p = blockIdx.x;
     for (int g0 = 0; g0 < a.n_groups; g0 += 32) {
         int4 r = make_int4(0, 0, 0, 0);
-        if (g0 + lane < a.n_groups) r = a.groups[g0 + lane];
+        if (g0 + lane < a.n_groups) r = kv_load_group(a, g0 + lane);
         const bool in = r.w > 0 && r.y > 0;
         const int most = (a.max_len - 1) / kKvBlock;   // blocks past max_len are of units that are left out
         const int tiles = in ? (int)(((int64_t)r.y * a.G + R - 1) / R) : 0, blocks = in ? min(r.w, most) : 0;
         if (g0 == 0) {
             int longest = blocks;   // more than 32 groups: the longest of all
-            for (int g = 32 + lane; g < a.n_groups; g += 32) longest = max(longest, min(a.groups[g].w, most));
+            for (int g = 32 + lane; g < a.n_groups; g += 32) longest = max(longest, min(kv_load_group(a, g).w, most));
             cut = kv_shared_cut<R>(a, tiles, a.n_groups > 32 ? longest : blocks);
             if (blockIdx.x == 0 && threadIdx.x == 0) *a.cut = cut;
         }

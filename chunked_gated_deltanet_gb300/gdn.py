@@ -721,7 +721,7 @@ def _head_rows(name: str, t: Optional[torch.Tensor], desc: gdn_attn_desc, n: int
         return t.data_ptr(), width
     if s[2] != 1 or (heads > 1 and s[1] != desc.head_dim):
         raise ValueError(f"{name}: a row's heads must be contiguous")
-    return t.data_ptr(), s[0] if n > 1 else max(s[0], width)
+    return t.data_ptr(), s[0] if n > 1 else width
 
 
 def gdn_rope(desc, rope: gdn_rope_desc, table: torch.Tensor, positions: torch.Tensor, q: torch.Tensor, k: torch.Tensor,

@@ -505,8 +505,10 @@ typedef struct gdn_kv_group_map {
  * group share nothing. A group's shared blocks are those that all of its
  * requests' tables name alike and that lie before each one's first new token,
  * found on the GPU, so they need not be known; of a group of one request, all
- * of its earlier blocks. A group whose bounds are out of order or range shares
- * nothing (gdn_device_status reports it). A plan that did not fit has no groups. */
+ * of its earlier blocks. With bounds out of order or range no group shares
+ * anything (gdn_device_status reports it). A plan that did not fit has no groups.
+ * Records past n_groups are left empty; the attention looks at max_groups, so a
+ * map kept for many more groups than there are costs its calls time. */
 gdn_status gdn_kv_group(const gdn_attn_desc *desc, const gdn_kv_cache *cache, const gdn_kv_map *map, const int32_t *bounds,
                         int32_t n_groups, const gdn_kv_group_map *groups, gdn_stream_t stream);
 

@@ -92,6 +92,91 @@ def test_as_the_unshared_attention(cuda_device, heads, dtype):
 
 
 @both
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("ratio", [12, 30, 80], ids=lambda r: f"2^{r}")
+@pytest.mark.parametrize("sizes", [[0, 0, 1, 1, 1, 1], [1, 1, 0, 0, 0, 0], [0, 1, 0, 1, 1, 0], [0, 0, 0, 0, 0, 1], [1, 1, 1, 1, 1, 0]],
+                         ids=["grows", "falls", "alternates", "last large", "last small"])
+def test_shared_blocks_of_unequal_values(cuda_device, sizes, ratio, n, dtype):
+    """Values of shared blocks (and of the open one) that are 2^ratio apart, in one column of the large ones only, so that
+    every other column is the small ones' alone; a block of zeros between."""
+    m = Shared((4, 2), 128, dtype, n_slots=4, seed=22)
+    v = m.draw(384, 2)
+    for b, big in enumerate([*sizes[:3], 2, *sizes[3:5]]):
+        rows = v[64 * b:64 * b + 64]
+        if big:
+            keep = rows[:, :, 3].clone()
+            rows.zero_()
+            rows[:, :, 3] = keep * (2.0 ** ratio if big == 1 else 0.0)
+    m.step([0], [384], check=False, data=(m.draw(384, 4), m.draw(384, 2), v))
+    m.fork(0, 1, 2)
+    own = m.draw(3 * n, 2)
+    if sizes[5]:
+        own[:, :, 3] *= 2.0 ** ratio
+    m.shared_step([0, 1, 2], [n] * 3, [0, 3], data=(m.draw(3 * n, 4, 2.0), m.draw(3 * n, 2), own))
+
+
+@both
+def test_empty_sessions(cuda_device, dtype):
+    """First tokens and prompts of slots that hold nothing, alone in a group and beside one another."""
+    m = Shared((4, 2), 64, dtype, n_slots=5, seed=4)
+    q, k, v = m.draw(2, 4), m.draw(2, 2), m.draw(2, 2)
+    out = m.shared_step([0, 3], [1, 1], [0, 2], data=(q, k, v))
+    assert torch.equal(out.cpu(), v.repeat_interleave(2, 1))       # each sees itself alone
+    m.shared_step([1, 2, 0], [70, 64, 63], [0, 2, 3])
+    m.check_contents()
+
+
+def test_more_groups_than_a_warp_looks_at(cuda_device):
+    m = Shared((2, 1), 64, BF, n_pages=400, n_slots=90, max_blocks=8, seed=12)
+    sources, dst = list(range(0, 80, 2)), list(range(1, 80, 2))
+    m.step(sources, [60 + 5 * i for i in range(40)], check=False)
+    gdn.gdn_kv_fork_batch(m.desc, m.cache, m.i32(sources), m.i32(dst))
+    for s, t in zip(sources, dst):
+        m.slots[t] = m.slots[s].copy()
+    m.shared_step(list(range(80)), [1] * 80, list(range(0, 81, 2)))
+    m.shared_step(list(range(80)), [1 + i % 3 for i in range(80)], list(range(0, 81, 2)))
+    m.check_contents()
+
+
+@both
+def test_shared_pages_past_two_gigabytes(cuda_device, dtype):
+    n_pages = 2 ** 31 // (8 * 64 * 256) + 40
+    m = Shared((8, 8), 256, dtype, n_pages=n_pages, n_slots=3, max_blocks=8)
+    m.cache.free.copy_(torch.arange(n_pages, dtype=torch.int32, device=cuda_device))
+    m.step([0], [140], check=False)
+    m.fork(0, 1, 2)
+    m.shared_step([0, 1, 2], [1, 1, 70], [0, 3])
+    assert int(m.cache.table[1, 0]) * 8 * 64 * 256 > 2 ** 31
+
+
+@pytest.mark.parametrize("heads,dtype", [((8, 2), BF), ((24, 1), BF), ((4, 2), F32)])
+def test_fewer_rows_than_the_plan(cuda_device, heads, dtype):
+    """Arrays that end before the plan does: the units past them are left out (the launch may not even look at them), the
+    others right."""
+    m = Shared(heads, 128, dtype, n_slots=5, seed=3)
+    m.step([0], [200], check=False)
+    m.fork(0, 1, 2)
+    n = 3
+    plan = gdn.KvPlan.new(n, n, m.dev)
+    groups = gdn.KvGroups.new(plan, 1)
+    gdn.gdn_kv_plan(m.desc, m.cache, m.i32([0, 1, 2]), m.i32([1] * n), plan)
+    q, k, v = m.draw(2, m.hq), m.draw(2, m.hkv), m.draw(2, m.hkv)
+    qd, kd, vd = (t.to(m.dev) for t in (q, k, v))
+    gdn.gdn_kv_append(m.desc, m.cache, plan, kd, vd)
+    gdn.gdn_kv_group(m.desc, m.cache, plan, m.i32([0, n]), groups)
+    out = torch.full_like(qd, float("nan"))
+    ws = gdn.kv_shared_workspace(m.desc, 2, 300, 300, m.dev)
+    ws.fill_(255)
+    gdn.gdn_kv_attention_shared(m.desc, m.cache, plan, groups, qd, kd, vd, out, ws, 1, 300, 300)
+    gdn.gdn_device_status()                                        # says so, or not
+    for i in (0, 1):
+        m.slots[i].k.append(k[i].float().numpy())
+        m.slots[i].v.append(v[i].float().numpy())
+        ref, bound = m.attention(i, 200, q[i:i + 1].double().numpy())
+        assert (np.abs(out[i:i + 1].double().cpu().numpy() - ref) <= bound).all()
+
+
+@both
 def test_what_is_not_finite_keeps_to_its_rows(cuda_device, dtype):
     """A query that is not finite, and keys and values that are not in a fork's own block, reach the other rows in no way."""
     for new in (1, 40):
@@ -127,13 +212,13 @@ def test_bounds_out_of_order_share_nothing(cuda_device):
     m.fork(0, 1, 2)
     before = len(m.slots[0].k)
     data = (m.draw(3, 4), m.draw(3, 2), m.draw(3, 2))
-    for bounds in ([2, 0], [-1, 3], [0, 9]):
+    for bounds in ([2, 0], [-1, 3], [0, 9], [0, 2, 1, 3], [0, 9, 3]):
         for s in (0, 1, 2):
             del m.slots[s].k[before:], m.slots[s].v[before:]
         m.cache.state[:3, 0] = before
         out = m.shared_step([0, 1, 2], [1, 1, 1], bounds, data=data, check=False)
         assert gdn.gdn_device_status() == gdn.GDN_ERR_INVALID_ARG
-        assert m.last[1].groups[0, 3] == 0 and not m.last[1].starts[:3].any()
+        assert not m.last[1].groups[:, 3].any() and not m.last[1].starts[:3].any()
         for i in range(3):
             ref, bound = m.attention(i, before, data[0][i:i + 1].double().numpy())
             assert (np.abs(out[i:i + 1].double().cpu().numpy() - ref) <= bound).all()
