@@ -92,12 +92,14 @@ struct KvAttn {
     int pre_blocks, n_pre;          // segments of the shared blocks, cut every pre_blocks (one group) or *cut; most of them
     int *cut;                       // several groups: the cut of the shared blocks, chosen on the GPU
     int head_dim, own_apart;
+    int n_own;                      // few rows: CTAs [0, n_own) take units, the others row tiles of the groups
     int max_suffix;                 // the caller's bound on a request's tokens past its group's shared blocks
 };
 
 // What a launch of an attention kernel covers: a plan's units over all of their keys; the units over the keys past their
-// group's shared blocks; the groups' rows over the shared blocks. The last two leave partial results, by packed row.
-enum KvPart { kKvWhole = 0, kKvSuffix = 1, kKvShared = 2 };
+// group's shared blocks; the groups' rows over the shared blocks; the last two side by side (few rows). These leave partial
+// results, by packed row.
+enum KvPart { kKvWhole = 0, kKvSuffix = 1, kKvShared = 2, kKvFew = 3 };
 
 // Segment of a block, and a segment's first block.
 __device__ __forceinline__ int kv_seg_of(const KvAttn &a, int block) { return a.seg_blocks ? block / a.seg_blocks : kv_grown_seg(block); }
@@ -124,12 +126,12 @@ __device__ __forceinline__ bool kv_suffix_unit_ok(const KvAttn &a, const KvUnit 
 }
 template <int PART>
 __device__ __forceinline__ bool kv_part_unit_ok(const KvAttn &a, const KvUnit &u, int start) {
-    if constexpr (PART == kKvSuffix) return kv_suffix_unit_ok(a, u, start);
+    if constexpr (PART != kKvWhole) return kv_suffix_unit_ok(a, u, start);
     else return kv_attn_unit_ok(a, u);
 }
 // Segments of a unit's own keys are cut at absolute multiples of seg_blocks too; the first starts at `start`.
 template <int PART>
-__device__ __forceinline__ int kv_part_seg0(const KvAttn &a, int start) { return PART == kKvSuffix ? start / a.seg_blocks : 0; }
+__device__ __forceinline__ int kv_part_seg0(const KvAttn &a, int start) { return PART == kKvWhole ? 0 : start / a.seg_blocks; }
 // Row of a shared-prefix call's partial results: (packed row, query head); the shared blocks' segments come first.
 __device__ __forceinline__ int64_t kv_shared_part_row(const KvAttn &a, int seg, int64_t row, int head) {
     return seg * a.part_rows + row * a.Hq + head;
@@ -140,6 +142,33 @@ __device__ __forceinline__ int4 kv_load_group(const KvAttn &a, int g) {
     int4 r = a.groups[g];
     r.y = r.x < 0 ? 0 : (int)min((int64_t)r.y, max(a.n_rows - r.x, (int64_t)0));
     return r;
+}
+// Few rows: group of row tile x (of R rows), its record, and the tile's first row; -1 if there is none. The same in every lane.
+template <int R>
+__device__ __forceinline__ int kv_group_of_tile(const KvAttn &a, int x, int4 &rec) {
+    const int lane = threadIdx.x & 31;
+    for (int g0 = 0; g0 < a.n_groups; g0 += 32) {
+        int4 r = make_int4(0, 0, 0, 0);
+        if (g0 + lane < a.n_groups) r = kv_load_group(a, g0 + lane);
+        const int tiles = r.w > 0 && r.y > 0 ? (int)(((int64_t)r.y * a.G + R - 1) / R) : 0;
+        int upto = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, upto > x);
+        if (hit) {
+            const int w = __ffs(hit) - 1;
+            rec.x = __shfl_sync(0xffffffffu, r.x, w);
+            rec.y = __shfl_sync(0xffffffffu, r.y, w);
+            rec.z = __shfl_sync(0xffffffffu, r.z, w);
+            rec.w = __shfl_sync(0xffffffffu, r.w, w);
+            return (x - __shfl_sync(0xffffffffu, upto - tiles, w)) * R;
+        }
+        x -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return -1;
 }
 __device__ __forceinline__ bool kv_group_ok(const KvAttn &a, const int4 &r) {
     return (unsigned)r.z < (unsigned)a.c.n_slots && r.w <= a.c.max_blocks;
@@ -168,9 +197,10 @@ cudaError_t gdn_launch_kv_attn_simt(const gdn::KvAttn &a, int d, int unit_bound,
 cudaError_t gdn_launch_kv_attn_token(const gdn::KvAttn &a, int d, int unit_bound, int rows_max, cudaStream_t st);
 // bf16 inputs, many rows:
 cudaError_t gdn_launch_kv_attn_prompt(const gdn::KvAttn &a, int d, int unit_bound, cudaStream_t st);
-// The parts of a shared-prefix call. Own keys: unit_bound units, in the form of rows_max (few rows: bf16 only). Shared keys: at
-// most n_pieces pieces.
-cudaError_t gdn_launch_kv_suffix(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int rows_max, int few, cudaStream_t st);
+// The parts of a shared-prefix call. Own keys: unit_bound units. Shared keys: at most n_pieces pieces. Few rows (bf16): own keys
+// of up to rows_max rows a unit, and the shared keys of `tiles` row tiles at most (0: they are a launch of their own).
+cudaError_t gdn_launch_kv_suffix(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int rows_max, cudaStream_t st);
+cudaError_t gdn_launch_kv_few(const gdn::KvAttn &a, int d, int unit_bound, int tiles, int rows_max, cudaStream_t st);
 cudaError_t gdn_launch_kv_shared(const gdn::KvAttn &a, int d, int bf16, int n_pieces, cudaStream_t st);
 cudaError_t gdn_launch_kv_shared_join(const gdn::KvAttn &a, int d, int bf16, int unit_bound, cudaStream_t st);
 cudaError_t gdn_launch_kv_group(const gdn::KvCache &c, const int32_t *rows, const int32_t *units, const int32_t *counts,

@@ -272,10 +272,16 @@ namespace {
 constexpr int kSharedPieces = 2 * gdn::kSharedSms;   // shared pieces beyond one cut of every row tile
 // How a shared-prefix call's keys are cut. The shared blocks into pieces (kv_shared_piece.cuh): of one group here, from max_len;
 // of several by the kernel, which knows how long each one's are, n_pre segments at most. Own keys in the form of max_new.
+// together: single tokens of few forks or over few keys, where one launch takes the shared blocks of tiles of 8 or 16 rows beside
+// the own keys (kv_attn_token.cuh). It reads the shared bytes once per tile, mostly from L2, at some 7 TB/s (d = 64, where the
+// arithmetic is more a byte: 4.2); the tensor core's tiles of up to 256 rows read them once, take 0.75 to 1.05 us a block on an
+// SM, and 7 us more for the two launches and their joins. The two times so estimated choose. Measured, together and tensor core
+// (us; 16/4 heads, d = 128): 2 forks over 1,000 keys 12 and 17, 16 over 8,000 23 and 23, 4 over 40,000 25 and 31, 8 over 40,000
+// 39 and 31; 8 families of 4 over 8,000 33 and 43, 8 of 8 over 40,000 221 and 152.
 struct SharedForm {
-    bool few;
+    bool few, together;
     int rows_max, tok_stride, seg_blocks, pre_blocks;
-    int64_t n_seg, n_pre, pieces;
+    int64_t n_seg, n_pre, pieces;   // pieces: together, row tiles
 };
 // Own keys of few rows: 256 keys, a block a warp, and the open block apart, as there is little of them and a CTA's time is
 // that of its longest chain of reads.
@@ -287,7 +293,7 @@ int64_t suffix_segs(const gdn_attn_desc *d, int64_t max_suffix, bool few) {
 int64_t most_shared(int64_t max_len) { return std::max<int64_t>((max_len - 1) / kKvBlock, 1); }
 int64_t least_pieces(int64_t blocks) { return (blocks + gdn::kKvMaxSegBlocks - 1) / gdn::kKvMaxSegBlocks; }
 SharedForm shared_form(const gdn_attn_desc *d, int64_t n_rows, int64_t n_groups, int64_t max_new, int64_t max_len, int64_t max_suffix) {
-    SharedForm f;
+    SharedForm f = {};
     const int G = d->n_q_heads / d->n_kv_heads, R = many_rows(d);
     f.tok_stride = (int)std::min<int64_t>(max_new, kKvBlock);
     f.rows_max = f.tok_stride * G;
@@ -298,6 +304,23 @@ SharedForm shared_form(const gdn_attn_desc *d, int64_t n_rows, int64_t n_groups,
     const int64_t blocks = most_shared(max_len), least = least_pieces(blocks), rows = n_rows * d->n_q_heads;
     f.n_pre = std::min(blocks, std::max(least, (int64_t)kSharedPieces * R / rows));
     f.pre_blocks = gdn::kKvMaxSegBlocks;
+    if (f.few) {
+        const int rows_max = f.rows_max <= 8 ? 8 : kFewRows;
+        const int64_t row_tiles = std::min((n_rows * G + n_groups * (rows_max - 1)) / rows_max, n_rows * G), ctas = row_tiles * d->n_kv_heads;
+        // tiles as families of like sizes have them (row_tiles is the most there can be); us
+        const double like = std::min((double)row_tiles, std::max((double)n_groups, (double)(n_rows * G) / rows_max + n_groups / 2));
+        const double reads = like * d->n_kv_heads * blocks * (2 * kKvBlock * d->head_dim) / (d->head_dim == 64 ? 4.2e6 : 7e6);
+        const double block_us = d->head_dim == 64 ? 0.75 : d->head_dim == 128 ? 0.85 : 1.05;
+        const double chains = (double)items * blocks * block_us / gdn::kSharedSms + 7;
+        if ((f.together = reads < chains)) {   // about four CTAs an SM, a warp's share two blocks at least
+            const int64_t segs = std::max<int64_t>(1, std::min((4 * gdn::kSharedSms + ctas - 1) / ctas, blocks / 8));
+            f.rows_max = rows_max;
+            f.pieces = row_tiles;
+            f.pre_blocks = (int)(((blocks + segs - 1) / segs + 3) / 4 * 4);
+            f.n_pre = (blocks + f.pre_blocks - 1) / f.pre_blocks;
+            return f;
+        }
+    }
     // several groups: the CTAs of one wave, as those that find no piece cost an SM some 4 us each, or what the longest cut makes
     f.pieces = std::max(items * least, std::min(items * f.n_pre, (int64_t)gdn::kSharedSms));
     if (n_groups > gdn::kSharedGroups) f.pieces = items * std::min(f.n_pre, (blocks + gdn::kSharedManyCut - 1) / gdn::kSharedManyCut);
@@ -409,16 +432,22 @@ GDN_API gdn_status gdn_kv_attention_shared(const gdn_attn_desc *d, const gdn_kv_
     a.own_apart = f.few;
     char *ws = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
     const bool bf16 = d->in_dtype == GDN_BF16;
-    a.cut = g->max_groups > 1 ? reinterpret_cast<int *>(ws) : nullptr;
+    a.cut = g->max_groups > 1 && !f.together ? reinterpret_cast<int *>(ws) : nullptr;
+    a.n_own = bound;
     ws += 256;
     a.part_ml = reinterpret_cast<float2 *>(ws);
     a.part_o = reinterpret_cast<float *>(ws + (((size_t)(f.n_pre + f.n_seg) * a.part_rows * sizeof(float2) + 255) & ~size_t(255)));
     cudaError_t e = gdn_device_error_word(&a.err);
     if (e != cudaSuccess) return cuda_fail(e, "device error word lookup");
     cudaStream_t cst = (cudaStream_t)stream;
-    e = launch_k(K_KV_ATTN, cst, [&] { return gdn_launch_kv_shared(a, d->head_dim, bf16, (int)f.pieces, cst); });
-    if (e != cudaSuccess) return cuda_fail(e, "shared blocks' attention kernel");
-    e = launch_k(K_KV_ATTN, cst, [&] { return gdn_launch_kv_suffix(a, d->head_dim, bf16, bound, f.rows_max, f.few, cst); });
+    if (!f.together) {
+        e = launch_k(K_KV_ATTN, cst, [&] { return gdn_launch_kv_shared(a, d->head_dim, bf16, (int)f.pieces, cst); });
+        if (e != cudaSuccess) return cuda_fail(e, "shared blocks' attention kernel");
+    }
+    e = launch_k(K_KV_ATTN, cst, [&] {
+        return f.few ? gdn_launch_kv_few(a, d->head_dim, bound, f.together ? (int)f.pieces : 0, f.rows_max, cst)
+                     : gdn_launch_kv_suffix(a, d->head_dim, bf16, bound, f.rows_max, cst);
+    });
     if (e != cudaSuccess) return cuda_fail(e, "own keys' attention kernel");
     e = launch_k(K_KV_JOIN, cst, [&] { return gdn_launch_kv_shared_join(a, d->head_dim, bf16, bound, cst); });
     return e != cudaSuccess ? cuda_fail(e, "attention join kernel") : GDN_OK;

@@ -18,6 +18,9 @@
 // and leave as the segment's partial result (or the result, where there is one segment only).
 // Bound: HBM. 64 tokens over 500 to 16,384 keys (32/8 heads of 128): 107 us, 5.2 TB/s read; the registers hold one unit of
 // loads ahead at 12 warps an SM. One token over 41,802 keys (16/2 heads of 256): 22 us, latency and the join's launch.
+//
+// Groups of requests with shared blocks (kKvFew): CTAs [0, n_own) of x take the units, over their own keys; each other one takes R
+// consecutive rows (row, head) of a group over the shared blocks, as rows of one unit that ends where they do.
 #pragma once
 
 #include "kv_attn.cuh"
@@ -125,16 +128,37 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
     grid_dep_wait();
     grid_dep_launch();
     const int ui = a.unit0 + blockIdx.x, h = blockIdx.y;
-    const KvUnit u = kv_load_unit(a.units, ui);   // inside the map whatever the count
-    if (ui >= a.counts[0]) return;
-    const int start = PART == kKvSuffix ? a.starts[ui] : 0;   // the first block of the pass
-    // own keys past shared ones: a short pass, so the rows' own block is a segment (and a CTA) by itself
-    const int seg0 = kv_part_seg0<PART>(a, start);
-    const int last_seg = PART == kKvSuffix ? seg0 + kv_own_segs(a, u.block, start) - 1 : u.block / a.seg_blocks;
-    const int n_row = u.count * a.G;
-    if (!kv_part_unit_ok<PART>(a, u, start) || n_row > R) {
-        if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
-        return;
+    KvUnit u;
+    // first block of the pass; segments [seg0, last_seg] of seg_len blocks, the rows' own block in segment own_seg; first row
+    int start = 0, seg0 = 0, last_seg, own_seg, seg_len = a.seg_blocks, n_row, r0 = 0;
+    const bool tile = PART == kKvFew && (int)blockIdx.x >= a.n_own;   // a row tile of a group, over its shared blocks
+    if (tile) {
+        // as rows of one unit that starts where the shared blocks end, without its own block
+        int4 rec;
+        r0 = kv_group_of_tile<R>(a, blockIdx.x - a.n_own, rec);
+        if (r0 < 0) return;
+        const int blocks = min(rec.w, (a.max_len - 1) / kKvBlock);   // blocks past max_len are of units that are left out
+        if (!kv_group_ok(a, rec) || blocks < 1) {
+            if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
+            return;
+        }
+        u = {rec.z, blocks, -1, 0, rec.y, rec.x, 0, 0};
+        seg_len = a.pre_blocks;
+        last_seg = (blocks - 1) / seg_len;
+        own_seg = INT32_MAX;
+        n_row = min(R, u.count * a.G - r0);
+    } else {
+        u = kv_load_unit(a.units, ui);   // inside the map whatever the count
+        if (ui >= a.counts[0]) return;
+        if (PART == kKvFew) start = a.starts[ui];
+        // own keys past shared ones: a short pass, so the rows' own block is a segment (and a CTA) by itself
+        seg0 = kv_part_seg0<PART>(a, start);
+        own_seg = last_seg = PART == kKvFew ? seg0 + kv_own_segs(a, u.block, start) - 1 : u.block / a.seg_blocks;
+        n_row = u.count * a.G;
+        if (!kv_part_unit_ok<PART>(a, u, start) || n_row > R) {
+            if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
+            return;
+        }
     }
     if (seg0 + (int)blockIdx.z > last_seg) return;
     extern __shared__ __align__(16) unsigned char token_smem[];
@@ -170,8 +194,8 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
 #pragma unroll
                 for (int i = 0; i < W; i += VB / 4) ld_words<VB / 4>(&vb[x][y][i], src + (16 * x + (y & 1) + 8 * (y >> 1)) * D + 8 * 4 * i);
     };
-    int blk = (seg0 + blockIdx.z) * a.seg_blocks + warp;
-    if (PART == kKvSuffix && blockIdx.z == 0) blk = start + warp;
+    int blk = (seg0 + blockIdx.z) * seg_len + warp;
+    if (PART == kKvFew && !tile && blockIdx.z == 0) blk = start + warp;
     int page = page_of(blk);
     if (page >= 0) {
         load_k(page, 0);
@@ -179,7 +203,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
     }
     // q's fragments, by warp 0: per k-step the lane's columns 0, 1 and 2, 3 of rows g (and g + 8), scaled, in fp16
     const bf *q = static_cast<const bf *>(a.q);
-    auto q_row = [&](int r) { return q + ((int64_t)(u.row + r / a.G) * a.Hq + h * a.G + r % a.G) * D + 16 * tq; };
+    auto q_row = [&](int r) { return q + ((int64_t)(u.row + (r0 + r) / a.G) * a.Hq + h * a.G + (r0 + r) % a.G) * D + 16 * tq; };
     if (warp == 0) {
 #pragma unroll
         for (int f = 0; f < NT; ++f) {
@@ -387,7 +411,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                 x.x = fmaf(f, y.x, x.x); x.y = fmaf(f, y.y, x.y);
                 x.z = fmaf(f, y.z, x.z); x.w = fmaf(f, y.w, x.w);
             }
-            const int tok = r / a.G, head = h * a.G + r % a.G;
+            const int tok = (r0 + r) / a.G, head = h * a.G + (r0 + r) % a.G;
             if (PART == kKvWhole && last_seg == 0) {
                 const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);   // no key: zero; NaN stays
                 const __nv_bfloat162 p0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), p1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
@@ -395,7 +419,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                     make_uint2(*reinterpret_cast<const uint32_t *>(&p0), *reinterpret_cast<const uint32_t *>(&p1));
             } else {
                 const int64_t pr = PART == kKvWhole ? kv_part_row(a, ui, seg, tok, head)
-                                                    : kv_shared_part_row(a, a.n_pre + seg - seg0, u.row + tok, head);
+                                                    : kv_shared_part_row(a, tile ? seg : a.n_pre + seg - seg0, u.row + tok, head);
                 *reinterpret_cast<float4 *>(a.part_o + pr * D + col) = x;
                 if (col == 0) a.part_ml[pr] = make_float2(M, L);
             }
@@ -414,10 +438,10 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[i][f][k] = 0.f;
         }
-        const int seg_end = (seg + 1) * a.seg_blocks, next_seg = seg + gridDim.z;
+        const int seg_end = (seg + 1) * seg_len, next_seg = seg + gridDim.z;
 #pragma unroll 1
         for (; blk < min(seg_end, u.block); blk += kTokenWarps) {
-            const int next = page_of(blk + kTokenWarps < seg_end ? blk + kTokenWarps : next_seg * a.seg_blocks + warp);
+            const int next = page_of(blk + kTokenWarps < seg_end ? blk + kTokenWarps : next_seg * seg_len + warp);
             const int64_t ph = (int64_t)page * a.Hkv + h;
             const float ks = a.scale_log2 * a.c.k_scale[ph], vs = a.c.v_scale[ph];
             float move = 1.f;
@@ -505,7 +529,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
             page = next;
         }
         // nothing is loaded ahead past the last segment (told apart here, so that no register is kept for it)
-        if (seg == last_seg) {
+        if (seg == own_seg) {
             if (own0 < u.first + u.count) own_block();
             merge(seg);
             return;
@@ -513,10 +537,11 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
         merge(seg);
         if (next_seg > last_seg) return;
         seg = next_seg;
-        blk = seg * a.seg_blocks + warp;
+        blk = seg * seg_len + warp;
     }
 }
 
+// n_units: CTAs along x, units and (kKvFew) row tiles of groups
 template <int D, int R, int PART = kKvWhole>
 cudaError_t launch_token(const KvAttn &a, int n_units, cudaStream_t st) {
     using P = TokenPlan<D, R>;
@@ -530,7 +555,7 @@ cudaError_t launch_token(const KvAttn &a, int n_units, cudaStream_t st) {
     cudaError_t e = gdn_sm_count(&sms);
     if (e != cudaSuccess) return e;
     const int64_t chains = (int64_t)n_units * a.Hkv, z = (16LL * sms + chains - 1) / chains;
-    const dim3 grid((unsigned)n_units, (unsigned)a.Hkv, (unsigned)std::min<int64_t>(a.n_seg, z));
+    const dim3 grid((unsigned)n_units, (unsigned)a.Hkv, (unsigned)std::min<int64_t>(PART == kKvFew ? std::max(a.n_seg, a.n_pre) : a.n_seg, z));
     e = gdn_launch_pdl(kv_attn_token_kernel<D, R, PART>, grid, 32 * kTokenWarps, P::kBytes, st, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

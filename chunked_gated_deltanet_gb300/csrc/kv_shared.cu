@@ -8,7 +8,8 @@
 // The parts run in the kernels of kv_attn_prompt.cuh, kv_attn_token.cuh and kv_attn_simt.cuh, each built for its part (KvPart),
 // so that the shared blocks' loop has no mask and no raw block in it: 8,000 x 16 rows over 37,760 shared keys (d = 128) take
 // 1.71 ms, 1.45 PFLOP/s, where the same loop with the raw blocks' code beside it reaches 1.18. A row's group stands in consecutive
-// packed rows, so a tile of it is filled across requests.
+// packed rows, so a tile of it is filled across requests. Single tokens of small families take both parts in one launch
+// (kv_attn_token.cuh); kv_api.cu has the rule.
 #include "kv_attn_prompt.cuh"
 #include "kv_attn_simt.cuh"
 #include "kv_attn_token.cuh"
@@ -261,12 +262,14 @@ cudaError_t gdn_launch_kv_group(const gdn::KvCache &c, const int32_t *rows, cons
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t gdn_launch_kv_suffix(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int rows_max, int few, cudaStream_t st) {
+cudaError_t gdn_launch_kv_suffix(const gdn::KvAttn &a, int d, int bf16, int unit_bound, int rows_max, cudaStream_t st) {
     using namespace gdn;
-    const cudaError_t e = !bf16 ? launch_simt_part<kKvSuffix>(a, d, unit_bound, rows_max, st)
-                          : few ? launch_token_part<kKvSuffix>(a, d, unit_bound, rows_max, st)
-                                : launch_prompt_part<kKvSuffix>(a, d, unit_bound, st);
+    const cudaError_t e = bf16 ? launch_prompt_part<kKvSuffix>(a, d, unit_bound, st) : launch_simt_part<kKvSuffix>(a, d, unit_bound, rows_max, st);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t gdn_launch_kv_few(const gdn::KvAttn &a, int d, int unit_bound, int tiles, int rows_max, cudaStream_t st) {
+    return gdn::launch_token_part<gdn::kKvFew>(a, d, unit_bound + tiles, rows_max, st);
 }
 
 cudaError_t gdn_launch_kv_shared(const gdn::KvAttn &a, int d, int bf16, int n_pieces, cudaStream_t st) {

@@ -298,7 +298,7 @@ def test_a_captured_step_replays(cuda_device):
 
 @pytest.mark.parametrize("d", [128, 256])
 def test_wait_timeout_is_reported_and_context_survives(cuda_device, d):
-    m = Shared((8, 2), d, BF, n_slots=4, seed=9)
+    m = Shared((48, 2), d, BF, n_slots=4, seed=9)
     m.step([0], [260], check=False)
     m.fork(0, 1, 2)
     torch.cuda.synchronize()

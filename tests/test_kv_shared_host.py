@@ -48,7 +48,7 @@ def test_shared_attention_refusals(lib):
     assert call(n=-1) == E and call(n=1 << 28) == E          # 2^28 rows of 16 heads
     assert call(max_new=0) == E and call(max_len=0) == E and call(max_suffix=0) == E
     assert call(max_len=1 << 31) == E and call(max_suffix=1 << 31) == E
-    assert call(max_len=(1 << 31) - 1) == E                    # segments
+    assert call(max_len=(1 << 31) - 1, max_new=8) == E         # more segments than a launch can have
     need = gdn.gdn_kv_shared_workspace(_desc(), 8, 1000, 1000)
     assert call(ws=None) == gdn.GDN_ERR_WORKSPACE and call(ws=P + 8) == gdn.GDN_ERR_WORKSPACE
     assert call(ws_bytes=600) == gdn.GDN_ERR_WORKSPACE and need > 600
