@@ -274,11 +274,12 @@ constexpr int kSharedPieces = 2 * gdn::kSharedSms;   // shared pieces beyond one
 // of several by the kernel, which knows how long each one's are, n_pre segments at most. Own keys in the form of max_new.
 // together: single tokens of few forks or over few keys, where one launch takes the shared blocks of tiles of 8 or 16 rows beside
 // the own keys (kv_attn_token.cuh). It reads the shared bytes once per tile, mostly from L2, at some 7 TB/s (d = 64, where the
-// arithmetic is more a byte: 4.2); the tensor core's tiles of up to 256 rows read them once, take 0.75 to 1.05 us a block on an
-// SM, and 7 us more for the two launches and their joins, 12 for pieces of several groups, which fill the SMs unevenly. The two
-// times so estimated choose. Measured, together and tensor core (us; 16/4 heads, d = 128): 2 forks over 1,000 keys 12 and 17,
-// 16 over 8,000 23 and 23, 4 over 40,000 25 and 31, 8 over 40,000 39 and 31; 8 families of 4 over 8,000 32 and 43, 12 of 1 to 16
-// over 500 to 5,600 68 and 75, 8 of 8 over 40,000 221 and 152.
+// arithmetic is more a byte: 4.2; tiles of 16 rows: 0.45 of that). The tensor core's tiles of up to 256 rows read them once,
+// take 0.75 to 1.05 us a block on an SM, and 7 us more for the two launches and their joins, 12 for pieces of several groups,
+// which fill the SMs unevenly. The two times so estimated choose; tiles of 16 rows of d = 256 lose throughout (29 and 25 over
+// 8,000 keys). Measured, together and tensor core (us; 16/4 heads, d = 128): 2 forks over 1,000 keys 12 and 17, 16 over 8,000
+// 23 and 23, 4 over 40,000 25 and 31, 8 over 40,000 39 and 31; 8 families of 4 over 8,000 32 and 43, 12 of 1 to 16 over 500 to
+// 5,600 68 and 75, 8 of 8 over 40,000 221 and 152.
 struct SharedForm {
     bool few, together;
     int rows_max, tok_stride, seg_blocks, pre_blocks;
@@ -305,13 +306,14 @@ SharedForm shared_form(const gdn_attn_desc *d, int64_t n_rows, int64_t n_groups,
     const int64_t blocks = most_shared(max_len), least = least_pieces(blocks), rows = n_rows * d->n_q_heads;
     f.n_pre = std::min(blocks, std::max(least, (int64_t)kSharedPieces * R / rows));
     f.pre_blocks = gdn::kKvMaxSegBlocks;
-    if (f.few) {
-        const int rows_max = f.rows_max <= 8 ? 8 : kFewRows;
+    const int rows_max = f.rows_max <= 8 ? 8 : kFewRows;
+    if (f.few && !(rows_max > 8 && d->head_dim == 256)) {
         const int64_t row_tiles = std::min((n_rows * G + n_groups * (rows_max - 1)) / rows_max, n_rows * G), ctas = row_tiles * d->n_kv_heads;
         // tiles when the last one of a group is filled by chance (row_tiles is the most there can be); us
         const double waste = (double)std::max(rows_max - G, 0) / (2 * rows_max);
         const double like = std::min((double)row_tiles, std::max((double)n_groups, (double)(n_rows * G) / rows_max + n_groups * waste));
-        const double reads = like * d->n_kv_heads * blocks * (2 * kKvBlock * d->head_dim) / (d->head_dim == 64 ? 4.2e6 : 7e6);
+        const double rate = (d->head_dim == 64 ? 4.2e6 : 7e6) * (rows_max == 8 ? 1 : 0.45);
+        const double reads = like * d->n_kv_heads * blocks * (2 * kKvBlock * d->head_dim) / rate;
         const double block_us = d->head_dim == 64 ? 0.75 : d->head_dim == 128 ? 0.85 : 1.05;
         const double chains = (double)items * blocks * block_us / gdn::kSharedSms + (n_groups > 1 ? 12 : 7);
         if ((f.together = reads < chains)) {   // about four CTAs an SM, a warp's share two blocks at least

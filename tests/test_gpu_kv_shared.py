@@ -67,6 +67,22 @@ def test_row_tiles(cuda_device, d):
         m.shared_step(list(range(k)), [new] * k, [0, k], rows_check=[0, 1, k - 1])
 
 
+@pytest.mark.parametrize("heads,new", [((4, 1), 1), ((6, 1), 1), ((8, 1), 1), ((12, 1), 1), ((16, 1), 1), ((5, 1), 3), ((2, 2), 8)],
+                         ids=lambda x: f"{x[0]}q{x[1]}kv" if isinstance(x, tuple) else f"{x}new")
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_row_tiles_of_tokens(cuda_device, d, heads, new):
+    """Single tokens and a few: three groups over prefixes of many segments, whose tiles of 8 or 16 rows end inside a request."""
+    m = Shared(heads, d, BF, n_pages=300, n_slots=20, max_blocks=50, seed=7)
+    m.step([0, 7, 14], [2600, 1000, 70], check=False)
+    m.fork(0, *range(1, 7))
+    m.fork(7, *range(8, 14))
+    m.fork(14, *range(15, 20))
+    m.step([3, 9, 16], [300, 64, 1], check=False)
+    m.shared_step(list(range(20)), [new] * 20, [0, 7, 14, 20], q_size=3.0)
+    m.shared_step([3, 0, 1, 8, 9], [new, 1, new, 1, new], [0, 3, 5])
+    m.check_contents()
+
+
 @both
 @pytest.mark.parametrize("heads", [(8, 2), (24, 1)], ids=["few", "many"])
 def test_as_the_unshared_attention(cuda_device, heads, dtype):
