@@ -86,9 +86,11 @@ struct RopeArgs {
 
 // A warp per row and share of its heads, LPH lanes a head, two 16-byte vectors a lane: the two that a lane's pairs lie in
 // where it rotates (i and i + rotary_dim / 2: one of each half; neighbours: two in a row), any other two where not. So a
-// lane's angles are the same for all heads of the row: one sincospi a pair and row, no exchange but the norm's sum.
-// Bound: HBM, every element in and out once: 47,880 rows of 32 + 8 + 8 heads of 128, 192 us, 6.1 TB/s. One row: 6 us in a graph,
-// its heads over as many warps as they fill (three dependent reads: position, table, elements).
+// lane's angles are the same for all heads of the row; the lanes of a column in the warp's HPW heads share them out, one
+// sincospi a pair and row (all of them in every lane: 194 us on the case below).
+// Bound: HBM, every element in and out once: 47,880 rows of 32 + 8 + 8 heads of 128, 188 us, 6.2 TB/s. One pass of heads at a
+// time: with two under way it takes 215 us, with 5 CTAs an SM in place of 4 199, with 3 218. One row: 6 us in a graph, its heads
+// over as many warps as they fill (three dependent reads: position, table, elements).
 template <typename InT, int D>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
     using V = RopeVec<InT>;
@@ -106,18 +108,24 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
     // the lane's two vectors, in elements
     const int c0 = turns ? (a.interleaved ? 2 * t * N : t * N) : 2 * t * N;
     const int c1 = turns && !a.interleaved ? c0 + a.rotary_dim / 2 : c0 + N;
-    float cs[N], sn[N];
-    if (turns) {
+    // the lanes of a pair's column in the HPW heads share out its N angles
+    constexpr int kOwn = N / HPW;
+    float cs[N], sn[N], own_cs[kOwn], own_sn[kOwn];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const unsigned long long phase = (unsigned long long)pos * a.table[t * N + i];
-            sincospif((float)(int)(phase >> 32) * 0x1p-31f, &sn[i], &cs[i]);
-            sn[i] *= a.magnitude;
-            cs[i] *= a.magnitude;
+    for (int i = 0; i < kOwn; ++i) {
+        own_cs[i] = own_sn[i] = 0.f;
+        if (turns) {
+            const unsigned long long phase = (unsigned long long)pos * a.table[t * N + lane / LPH * kOwn + i];
+            sincospif((float)(int)(phase >> 32) * 0x1p-31f, &own_sn[i], &own_cs[i]);
         }
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        cs[i] = __shfl_sync(0xffffffffu, own_cs[i % kOwn], i / kOwn * LPH + t) * a.magnitude;
+        sn[i] = __shfl_sync(0xffffffffu, own_sn[i % kOwn], i / kOwn * LPH + t) * a.magnitude;
+    }
     const int step = HPW * a.splits;
-#pragma unroll 2
+#pragma unroll 1
     for (int h0 = share * HPW; h0 < a.heads; h0 += step) {
         const int h = h0 + lane / LPH;
         const bool live = h < a.heads;
