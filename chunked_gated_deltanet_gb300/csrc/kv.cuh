@@ -92,6 +92,7 @@ struct KvAttn {
     int pre_blocks, n_pre;          // segments of the shared blocks, cut every pre_blocks (one group) or *cut; most of them
     int *cut;                       // several groups: the cut of the shared blocks, chosen on the GPU
     int head_dim, own_apart;
+    int beside;                     // few rows: the launch before is the shared blocks' (KvBeside)
     int n_own;                      // few rows: CTAs [0, n_own) take units, the others row tiles of the groups
     int max_suffix;                 // the caller's bound on a request's tokens past its group's shared blocks
 };
@@ -100,6 +101,21 @@ struct KvAttn {
 // group's shared blocks; the groups' rows over the shared blocks; the last two side by side (few rows). These leave partial
 // results, by packed row.
 enum KvPart { kKvWhole = 0, kKvSuffix = 1, kKvShared = 2, kKvFew = 3 };
+
+// A launch over own keys runs beside the one over shared blocks before it, on the SMs that its last pieces leave: it reads
+// nothing that one writes, and what came before that one is complete, as it lets the next launch start only after its own wait.
+// So the wait stands at the end, in one CTA alone (the others make room for further ones): the join, which waits for this
+// launch, thereby starts after both.
+struct KvBeside {
+    bool on;
+    __device__ explicit KvBeside(bool beside) : on(beside) {
+        if (!on) grid_dep_wait();
+        grid_dep_launch();
+    }
+    __device__ ~KvBeside() {
+        if (on && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) grid_dep_wait();
+    }
+};
 
 // Segment of a block, and a segment's first block.
 __device__ __forceinline__ int kv_seg_of(const KvAttn &a, int block) { return a.seg_blocks ? block / a.seg_blocks : kv_grown_seg(block); }

@@ -438,6 +438,7 @@ GDN_API gdn_status gdn_kv_attention_shared(const gdn_attn_desc *d, const gdn_kv_
     const bool bf16 = d->in_dtype == GDN_BF16;
     a.cut = g->max_groups > 1 && !f.together ? reinterpret_cast<int *>(ws) : nullptr;
     a.n_own = bound;
+    a.beside = !f.together;
     ws += 256;
     a.part_ml = reinterpret_cast<float2 *>(ws);
     a.part_o = reinterpret_cast<float *>(ws + (((size_t)(f.n_pre + f.n_seg) * a.part_rows * sizeof(float2) + 255) & ~size_t(255)));

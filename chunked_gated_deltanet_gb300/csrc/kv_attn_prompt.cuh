@@ -185,8 +185,7 @@ __global__ void __launch_bounds__(PromptPlan<D>::NT, 1) kv_attn_prompt_kernel(co
     using P = PromptPlan<D>;
     using bf = __nv_bfloat16;
     constexpr int NS = P::NS;
-    grid_dep_wait();
-    grid_dep_launch();
+    const KvBeside beside(PART == kKvSuffix);
     int h = blockIdx.y, ui = 0, rt = 0, seg = 0, n_tok = 0, seg0 = 0, last_seg = 0, r0 = 0, cut = 0;
     KvUnit u;
     if constexpr (PART == kKvShared) {

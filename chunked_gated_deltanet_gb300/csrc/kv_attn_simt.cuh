@@ -89,8 +89,7 @@ template <int D, int PART = kKvWhole>
 __global__ void __launch_bounds__(256) kv_attn_simt_kernel(const KvAttn a, int row_tiles) {
     using P = SimtPlan<D>;
     constexpr int R = P::R, LD = P::LD, PLD = P::PLD, CT = D / 16;
-    grid_dep_wait();
-    grid_dep_launch();
+    const KvBeside beside(PART == kKvSuffix);
     int h = blockIdx.y, ui = 0, r0 = 0, seg = blockIdx.z, seg0 = 0, last_seg = 0, start = 0, cut = a.seg_blocks;
     KvUnit u;
     if constexpr (PART == kKvShared) {

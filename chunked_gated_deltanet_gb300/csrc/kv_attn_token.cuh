@@ -125,8 +125,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
     constexpr int UK = P::UK, NA = P::NA, J = P::J, W = P::W, NO = P::NO, NT = P::NT, NU = P::NU;
     constexpr int VB = NO < 16 ? NO : 16;   // bytes of a value row that a lane reads at once
     auto col = [](int g, int i) { return i / VB * (8 * VB) + g * VB + i % VB; };   // column i of lane group g
-    grid_dep_wait();
-    grid_dep_launch();
+    const KvBeside beside(PART == kKvFew && a.beside);
     const int ui = a.unit0 + blockIdx.x, h = blockIdx.y;
     KvUnit u;
     // first block of the pass; segments [seg0, last_seg] of seg_len blocks, the rows' own block in segment own_seg; first row
