@@ -272,14 +272,14 @@ namespace {
 constexpr int kSharedPieces = 2 * gdn::kSharedSms;   // shared pieces beyond one cut of every row tile
 // How a shared-prefix call's keys are cut. The shared blocks into pieces (kv_shared_piece.cuh): of one group here, from max_len;
 // of several by the kernel, which knows how long each one's are, n_pre segments at most. Own keys in the form of max_new.
-// together: single tokens of few forks or over few keys, where one launch takes the shared blocks of tiles of 8 or 16 rows beside
-// the own keys (kv_attn_token.cuh). It reads the shared bytes once per tile, mostly from L2, at some 7 TB/s (d = 64, where the
-// arithmetic is more a byte: 4.2; tiles of 16 rows: 0.45 of that). The tensor core's tiles of up to 256 rows read them once,
-// take 0.75 to 1.05 us a block on an SM, and 7 us more for the two launches and their joins, 12 for pieces of several groups,
-// which fill the SMs unevenly. The two times so estimated choose; tiles of 16 rows of d = 256 lose throughout (29 and 25 over
-// 8,000 keys). Measured, together and tensor core (us; 16/4 heads, d = 128): 2 forks over 1,000 keys 12 and 17, 16 over 8,000
-// 23 and 23, 4 over 40,000 25 and 31, 8 over 40,000 39 and 31; 8 families of 4 over 8,000 32 and 43, 12 of 1 to 16 over 500 to
-// 5,600 68 and 75, 8 of 8 over 40,000 221 and 152.
+// together: single tokens of a few forks, or of many small families, where one launch takes the shared blocks of tiles of 8 or 16
+// rows beside the own keys (kv_attn_token.cuh). It reads the shared bytes once per tile, mostly from L2, at some 7 TB/s (d = 64,
+// where the arithmetic is more a byte: 4.2; tiles of 16 rows: 0.45 of that). The tensor core's tiles of up to 256 rows read them
+// once, take 0.75 to 1.05 us a block on an SM, and 1.5 us more for the second launch, 5 for pieces of several groups, which fill
+// the SMs unevenly. The two times so estimated choose; with d = 256 one group, and tiles of 16 rows, lose throughout (2 forks
+// over 8,000 keys 21 and 19, 29 and 25). Measured, together and tensor core (us; 16/4 heads, d = 128): 2 forks over 1,000 keys
+// 12.3 and 12.4, over 40,000 21 and 25, 8 over 8,000 19 and 17; 8 families of 4 over 8,000 33 and 37, of 8 58 and 39, of 4 over
+// 40,000 93 and 140; 12 of 1 to 16 over 500 to 5,600 (32/8) 69 and 62; d = 64, 8/8 heads, 8 of 8 over 40,000 113 and 268.
 struct SharedForm {
     bool few, together;
     int rows_max, tok_stride, seg_blocks, pre_blocks;
@@ -307,7 +307,7 @@ SharedForm shared_form(const gdn_attn_desc *d, int64_t n_rows, int64_t n_groups,
     f.n_pre = std::min(blocks, std::max(least, (int64_t)kSharedPieces * R / rows));
     f.pre_blocks = gdn::kKvMaxSegBlocks;
     const int rows_max = f.rows_max <= 8 ? 8 : kFewRows;
-    if (f.few && !(rows_max > 8 && d->head_dim == 256)) {
+    if (f.few && !(d->head_dim == 256 && (n_groups == 1 || rows_max > 8))) {
         const int64_t row_tiles = std::min((n_rows * G + n_groups * (rows_max - 1)) / rows_max, n_rows * G), ctas = row_tiles * d->n_kv_heads;
         // tiles when the last one of a group is filled by chance (row_tiles is the most there can be); us
         const double waste = (double)std::max(rows_max - G, 0) / (2 * rows_max);
@@ -315,7 +315,7 @@ SharedForm shared_form(const gdn_attn_desc *d, int64_t n_rows, int64_t n_groups,
         const double rate = (d->head_dim == 64 ? 4.2e6 : 7e6) * (rows_max == 8 ? 1 : 0.45);
         const double reads = like * d->n_kv_heads * blocks * (2 * kKvBlock * d->head_dim) / rate;
         const double block_us = d->head_dim == 64 ? 0.75 : d->head_dim == 128 ? 0.85 : 1.05;
-        const double chains = (double)items * blocks * block_us / gdn::kSharedSms + (n_groups > 1 ? 12 : 7);
+        const double chains = (double)items * blocks * block_us / gdn::kSharedSms + (n_groups > 1 ? 5 : 1.5);
         if ((f.together = reads < chains)) {   // about four CTAs an SM, a warp's share two blocks at least
             const int64_t segs = std::max<int64_t>(1, std::min((4 * gdn::kSharedSms + ctas - 1) / ctas, blocks / 8));
             f.rows_max = rows_max;
