@@ -88,7 +88,7 @@ struct RopeArgs {
 // where it rotates (i and i + rotary_dim / 2: one of each half; neighbours: two in a row), any other two where not. So a
 // lane's angles are the same for all heads of the row; the lanes of a column in the warp's HPW heads share them out, one
 // sincospi a pair and row (all of them in every lane: 194 us on the case below).
-// Bound: HBM, every element in and out once: 47,880 rows of 32 + 8 + 8 heads of 128, 188 us, 6.2 TB/s. One pass of heads at a
+// Bound: HBM, every element in and out once: 47,880 rows of 32 + 8 + 8 heads of 128, 188 us, 6.3 TB/s. One pass of heads at a
 // time: with two under way it takes 215 us, with 5 CTAs an SM in place of 4 199, with 3 218. One row: 6 us in a graph, its heads
 // over as many warps as they fill (three dependent reads: position, table, elements).
 template <typename InT, int D>
