@@ -265,6 +265,61 @@ def test_another_stream(cuda_device):
     m.shared_step([0, 1, 2], [1, 2, 1], [0, 3], stream=torch.cuda.Stream())
 
 
+@pytest.mark.parametrize("heads,d,dtype,new", [((16, 2), 256, BF, 1), ((16, 2), 128, BF, 40), ((4, 2), 64, F32, 5), ((8, 8), 64, BF, 1)],
+                         ids=["few", "many", "fp32", "together"])
+def test_calls_on_one_workspace_in_a_row(cuda_device, heads, d, dtype, new):
+    """Own keys run beside the shared blocks, joins after both: two batches in turn on one workspace, eager and in a graph, give
+    the bits that each gives alone, whichever part takes longer."""
+    m = Shared(heads, d, dtype, n_pages=400, n_slots=8, max_blocks=140, seed=2)
+    m.step([0, 4], [6000, 200], check=False)
+    m.fork(0, 1, 2, 3)
+    m.fork(4, 5, 6, 7)
+    m.step([2], [900], check=False)          # one short own part and one long one
+    m.step([6], [2500], check=False)         # own keys longer than what is shared
+    calls, alone = [], []
+    for slots in ([0, 1, 2, 3], [4, 5, 6, 7]):
+        n = 4 * new
+        plan = gdn.KvPlan.new(n, 4, m.dev)
+        groups = gdn.KvGroups.new(plan, 1)
+        q, k, v = (m.draw(n, h).to(m.dev) for h in (m.hq, m.hkv, m.hkv))
+        gdn.gdn_kv_plan(m.desc, m.cache, m.i32(slots), m.i32([new] * 4), plan)
+        gdn.gdn_kv_append(m.desc, m.cache, plan, k, v)
+        gdn.gdn_kv_group(m.desc, m.cache, plan, m.i32([0, 4]), groups)
+        calls.append((plan, groups, q, k, v))
+    ws = gdn.kv_shared_workspace(m.desc, 4 * new, 7000, 2800, m.dev)
+
+    def attend(i, out):
+        plan, groups, q, k, v = calls[i]
+        gdn.gdn_kv_attention_shared(m.desc, m.cache, plan, groups, q, k, v, out, ws, new, 7000, 2800)
+
+    outs = [torch.empty_like(calls[0][2]) for _ in range(24)]
+    for i in range(2):
+        ws.fill_(255)
+        attend(i, outs[i])
+        torch.cuda.synchronize()
+        alone.append(outs[i].clone())
+        assert not outs[i].isnan().any()
+    for first in (0, 1):
+        ws.fill_(255)
+        for j, out in enumerate(outs):
+            out.fill_(float("nan")) if j % 5 == 0 else None
+            attend((j + first) % 2, out)
+        for j, out in enumerate(outs):
+            assert torch.equal(out, alone[(j + first) % 2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for j, out in enumerate(outs):
+            attend(j % 2, out)
+    for _ in range(3):
+        ws.fill_(255)
+        for out in outs:
+            out.zero_()
+        graph.replay()
+        for j, out in enumerate(outs):
+            assert torch.equal(out, alone[j % 2])
+    assert gdn.gdn_device_status() == gdn.GDN_OK
+
+
 def test_a_captured_step_replays(cuda_device):
     """Batched forks, then plan, append, grouping and attention of their tokens from one graph; each replay advances the
     slots, over the end of a block."""
