@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(kGroupThreads) kv_group_kernel(const KvCache c
 }
 
 // Every row of a unit: the segments of its group's shared blocks, then its own ones. W warps of a CTA to a (token, query
-// head), each every W-th segment; their sums are added in order. Few rows have many segments (W = 8: one latency for four a
-// warp; 1,024 rows of 22 segments, d = 256: 10 us), many rows few (128,000 rows of 4 or 5, d = 128: 58 us, 4.9 TB/s).
+// head), each every W-th segment; their sums are added in order. Few rows have many segments and leave room for more warps
+// (launch_shared_join), many rows few (128,000 rows of 4 or 5, d = 128: 58 us, 4.9 TB/s).
 template <typename InT, int D, int W>
 __global__ void __launch_bounds__(256) kv_shared_join_kernel(const KvAttn a) {
     grid_dep_wait();
@@ -144,11 +144,14 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(const KvAttn a) {
     if (ui >= a.counts[0] || !kv_suffix_unit_ok(a, u, start)) return;
     const int pre = (start + cut - 1) / cut, n = pre + kv_own_segs(a, u.block, start);
     constexpr int V = D == 64 ? 2 : 4, N = D / (32 * V), B = W == 8 ? 4 : 2;   // B segments loaded together
-    __shared__ float so[W > 1 ? W : 1][D], sl[W > 1 ? W : 1];
+    __shared__ float so[W > 1 ? 8 : 1][D], sl[W > 1 ? 8 : 1];   // a warp's sums, W > 1
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, mine = warp % W;
     const int n_row = u.count * a.Hq;
-    for (int r = blockIdx.y * (8 / W) + warp / W; r < n_row; r += gridDim.y * (8 / W)) {
-        const int64_t row = (int64_t)u.row * a.Hq + r;
+    for (int r0 = blockIdx.y * (8 / W); r0 < n_row; r0 += gridDim.y * (8 / W)) {   // 8 / W rows, the same passes in every warp
+        const int r = r0 + warp / W;
+        const bool live = r < n_row;
+        if (W == 1 && !live) break;
+        const int64_t row = (int64_t)u.row * a.Hq + (live ? r : r0);
         auto at = [&](int s) { return (s < pre ? s : a.n_pre + s - pre) * a.part_rows + row; };
         float2 ml[B];
         float v[B][N][V];
@@ -201,22 +204,24 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(const KvAttn a) {
 #pragma unroll
                 for (int k = 0; k < V; ++k) dst[V * (lane + 32 * j) + k] = from_f<InT>(o[j][k] * inv);
         } else {
-            __syncthreads();   // the row before is read
+            __syncthreads();   // the rows before are read
 #pragma unroll
             for (int j = 0; j < N; ++j)
 #pragma unroll
-                for (int k = 0; k < V; ++k) so[mine][V * (lane + 32 * j) + k] = o[j][k];
-            if (lane == 0) sl[mine] = l;
+                for (int k = 0; k < V; ++k) so[warp][V * (lane + 32 * j) + k] = o[j][k];
+            if (lane == 0) sl[warp] = l;
             __syncthreads();
-            if (t < D) {
-                float x = 0.f, L = 0.f;
+            if (!live) continue;
+            const int w0 = warp - mine;   // the row's first warp
+            float L = 0.f;
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    x += so[w][t];
-                    L += sl[w];
-                }
-                const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-                dst[t] = from_f<InT>(x * inv);
+            for (int w = 0; w < W; ++w) L += sl[w0 + w];
+            const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+            for (int c = 32 * mine + lane; c < D; c += 32 * W) {
+                float x = 0.f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) x += so[w0 + w][c];
+                dst[c] = from_f<InT>(x * inv);
             }
         }
     }
@@ -229,12 +234,20 @@ cudaError_t launch_simt_part(const KvAttn &a, int d, int n, int rows_max, cudaSt
     return launch_simt_many<256, PART>(a, n, rows_max, st);
 }
 
+template <typename InT, int D, int W>
+cudaError_t launch_join_warps(const KvAttn &a, int unit_bound, int most, cudaStream_t st) {   // most: CTAs of a unit
+    const int per_unit = (a.tok_stride * a.Hq * W + 7) / 8;
+    return gdn_launch_pdl(kv_shared_join_kernel<InT, D, W>, dim3((unsigned)unit_bound, (unsigned)std::min(per_unit, most)), 256, 0, st, a);
+}
+// As many warps a row as one wave of CTAs has room for, about: 128 rows of 4 segments (d = 128) with 8 warps 6 us, with 4 8; 1,024
+// of 22 (d = 256) 12 and 10; 1,984 of 3 to 9 (d = 128) 12 and 10, with 2 8. Beyond, a warp a row, CTAs of several rows: 128,000
+// rows with up to 48 CTAs a unit 61, with 64 63, with 128 74. (Event times, 2 us above the kernels'.)
 template <typename InT, int D>
 cudaError_t launch_shared_join(const KvAttn &a, int unit_bound, cudaStream_t st) {
-    const int per_unit = a.tok_stride * a.Hq;
-    if (a.part_rows <= 4096)   // few rows
-        return gdn_launch_pdl(kv_shared_join_kernel<InT, D, 8>, dim3((unsigned)unit_bound, (unsigned)std::min(per_unit, 4096)), 256, 0, st, a);
-    return gdn_launch_pdl(kv_shared_join_kernel<InT, D, 1>, dim3((unsigned)unit_bound, (unsigned)std::min((per_unit + 7) / 8, 64)), 256, 0, st, a);
+    if (a.part_rows <= 512) return launch_join_warps<InT, D, 8>(a, unit_bound, 4096, st);
+    if (a.part_rows <= 8 * kSharedSms) return launch_join_warps<InT, D, 4>(a, unit_bound, 4096, st);
+    if (a.part_rows <= 4096) return launch_join_warps<InT, D, 2>(a, unit_bound, 4096, st);
+    return launch_join_warps<InT, D, 1>(a, unit_bound, 48, st);
 }
 
 }  // namespace gdn
