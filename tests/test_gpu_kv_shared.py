@@ -367,6 +367,56 @@ def test_a_captured_step_replays(cuda_device):
     m.check_contents()
 
 
+@pytest.mark.parametrize("heads,d,dtype,new", [((8, 1), 256, BF, 1), ((16, 1), 128, BF, 3), ((4, 2), 64, F32, 2), ((8, 2), 128, BF, 1)],
+                         ids=["few", "many", "fp32", "together"])
+def test_a_captured_step_with_other_batches(cuda_device, heads, d, dtype, new):
+    """One graph of plan, append, grouping and attention replayed for two families in turn, whose slots, shared blocks and
+    lengths differ: every launch reads what the replay's own plan and grouping wrote."""
+    m = Shared(heads, d, dtype, n_pages=120, n_slots=8, max_blocks=30, seed=6)
+    m.step([0, 4], [700, 130], check=False)
+    m.fork(0, 1, 2, 3)
+    m.fork(4, 5, 6, 7)
+    m.step([2, 7], [100, 200], check=False)
+    families = [[0, 1, 2, 3], [4, 7, 5, 6]]
+    n = 4 * new
+    dst, bounds, news = m.i32(families[0]), m.i32([0, 4]), m.i32([new] * 4)
+    plan = gdn.KvPlan.new(n, 4, m.dev)
+    groups = gdn.KvGroups.new(plan, 1)
+    ws = gdn.kv_shared_workspace(m.desc, n, 1000, 400, m.dev)
+    q, k, v = (m.draw(n, h).to(m.dev) for h in (m.hq, m.hkv, m.hkv))
+    out = torch.zeros_like(q)
+
+    def step():
+        gdn.gdn_kv_plan(m.desc, m.cache, dst, news, plan)
+        gdn.gdn_kv_append(m.desc, m.cache, plan, k, v)
+        gdn.gdn_kv_group(m.desc, m.cache, plan, bounds, groups)
+        gdn.gdn_kv_attention_shared(m.desc, m.cache, plan, groups, q, k, v, out, ws, new, 1000, 400)
+
+    def advance(replay, slots):
+        x = m.draw(n, m.hq), m.draw(n, m.hkv), m.draw(n, m.hkv)
+        for t, y in zip((q, k, v), x):
+            t.copy_(y)
+        dst.copy_(torch.tensor(slots, dtype=torch.int32))
+        before = [len(m.slots[s].k) for s in slots]
+        replay()
+        got = out.double().cpu().numpy()
+        for i, s in enumerate(slots):
+            rows = slice(i * new, (i + 1) * new)
+            m.slots[s].k += list(x[1][rows].float().numpy())
+            m.slots[s].v += list(x[2][rows].float().numpy())
+            ref, bound = m.attention(s, before[i], x[0][rows].double().numpy())
+            assert (np.abs(got[rows] - ref) <= bound).all(), (s, before[i])
+
+    advance(step, families[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for j in range(12):
+        advance(graph.replay, families[(j + 1) % 2])
+    assert gdn.gdn_device_status() == gdn.GDN_OK
+    m.check_contents()
+
+
 @pytest.mark.parametrize("d", [128, 256])
 def test_wait_timeout_is_reported_and_context_survives(cuda_device, d):
     m = Shared((48, 2), d, BF, n_slots=4, seed=9)
