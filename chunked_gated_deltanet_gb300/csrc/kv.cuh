@@ -127,11 +127,13 @@ __device__ __forceinline__ bool kv_attn_unit_ok(const KvAttn &a, const KvUnit &u
            kv_seg_of(a, u.block) < a.n_seg;
 }
 
-// Shared-prefix calls. Segments of a unit's own keys, those of its blocks [start, block) and of its own block, which few rows
-// have as a segment by itself and many rows in the last one.
+// Shared-prefix calls. Segments of a unit's own keys, those of its blocks [start, block) and of its own block. Many rows: cut at
+// absolute multiples of seg_blocks, the own block in the last one. Few rows: cut every seg_blocks from `start` on, so that each
+// but the last complete one has a block for every warp (the kernel's loads a segment ahead count on that), and the own block a
+// segment by itself.
 __device__ __forceinline__ int kv_own_segs(const KvAttn &a, int block, int start) {
     if (!a.own_apart) return block / a.seg_blocks - start / a.seg_blocks + 1;
-    return (block > start ? (block - 1) / a.seg_blocks - start / a.seg_blocks + 1 : 0) + 1;
+    return (block - start + a.seg_blocks - 1) / a.seg_blocks + 1;
 }
 // A unit's first block that is its own (its group's shared blocks lie before it); outside the sizes
 // given with the call the unit is left out like any other.
@@ -145,7 +147,7 @@ __device__ __forceinline__ bool kv_part_unit_ok(const KvAttn &a, const KvUnit &u
     if constexpr (PART != kKvWhole) return kv_suffix_unit_ok(a, u, start);
     else return kv_attn_unit_ok(a, u);
 }
-// Segments of a unit's own keys are cut at absolute multiples of seg_blocks too; the first starts at `start`.
+// Many rows: the segment that a unit's own keys start in, at `start`.
 template <int PART>
 __device__ __forceinline__ int kv_part_seg0(const KvAttn &a, int start) { return PART == kKvWhole ? 0 : start / a.seg_blocks; }
 // Row of a shared-prefix call's partial results: (packed row, query head); the shared blocks' segments come first.

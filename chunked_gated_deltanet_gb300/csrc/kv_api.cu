@@ -285,12 +285,12 @@ struct SharedForm {
     int rows_max, tok_stride, seg_blocks, pre_blocks;
     int64_t n_seg, n_pre, pieces;   // pieces: together, row tiles
 };
-// Own keys of few rows: 256 keys, a block a warp, and the open block apart, as there is little of them and a CTA's time is
-// that of its longest chain of reads.
+// Own keys of few rows: 256 keys from the first own block on, a block a warp, and the open block apart, as there is little of
+// them and a CTA's time is that of its longest chain of reads.
 int suffix_seg_blocks(const gdn_attn_desc *d, bool few) { return d->in_dtype == GDN_FP32 ? 8 : few ? 4 : 64; }
 int64_t suffix_segs(const gdn_attn_desc *d, int64_t max_suffix, bool few) {
-    const int seg = suffix_seg_blocks(d, few);
-    return ((max_suffix - 1) / kKvBlock + seg - 1) / seg + 1 + (few ? 1 : 0);
+    const int seg = suffix_seg_blocks(d, few);   // kv_own_segs
+    return ((max_suffix - 1) / kKvBlock + seg - 1) / seg + 1;
 }
 int64_t most_shared(int64_t max_len) { return std::max<int64_t>((max_len - 1) / kKvBlock, 1); }
 int64_t least_pieces(int64_t blocks) { return (blocks + gdn::kKvMaxSegBlocks - 1) / gdn::kKvMaxSegBlocks; }

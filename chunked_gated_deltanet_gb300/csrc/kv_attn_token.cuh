@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
     const KvBeside beside(PART == kKvFew && a.beside);
     const int ui = a.unit0 + blockIdx.x, h = blockIdx.y;
     KvUnit u;
-    // first block of the pass; segments [seg0, last_seg] of seg_len blocks, the rows' own block in segment own_seg; first row
-    int start = 0, seg0 = 0, last_seg, own_seg, seg_len = a.seg_blocks, n_row, r0 = 0;
+    // first block of the pass; segments [0, last_seg] of seg_len blocks from there, the rows' own block in segment own_seg; first row
+    int start = 0, last_seg, own_seg, seg_len = a.seg_blocks, n_row, r0 = 0;
     const bool tile = PART == kKvFew && (int)blockIdx.x >= a.n_own;   // a row tile of a group, over its shared blocks
     if (tile) {
         // as rows of one unit that starts where the shared blocks end, without its own block
@@ -151,15 +151,14 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
         if (ui >= a.counts[0]) return;
         if (PART == kKvFew) start = a.starts[ui];
         // own keys past shared ones: a short pass, so the rows' own block is a segment (and a CTA) by itself
-        seg0 = kv_part_seg0<PART>(a, start);
-        own_seg = last_seg = PART == kKvFew ? seg0 + kv_own_segs(a, u.block, start) - 1 : u.block / a.seg_blocks;
+        own_seg = last_seg = PART == kKvFew ? kv_own_segs(a, u.block, start) - 1 : u.block / a.seg_blocks;
         n_row = u.count * a.G;
         if (!kv_part_unit_ok<PART>(a, u, start) || n_row > R) {
             if (threadIdx.x == 0) atomicOr(a.err, kErrKvBounds);
             return;
         }
     }
-    if (seg0 + (int)blockIdx.z > last_seg) return;
+    if ((int)blockIdx.z > last_seg) return;
     extern __shared__ __align__(16) unsigned char token_smem[];
     float *so = reinterpret_cast<float *>(token_smem + P::kSo);
     float2 *sml = reinterpret_cast<float2 *>(token_smem + P::kMl);
@@ -193,8 +192,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
 #pragma unroll
                 for (int i = 0; i < W; i += VB / 4) ld_words<VB / 4>(&vb[x][y][i], src + (16 * x + (y & 1) + 8 * (y >> 1)) * D + 8 * 4 * i);
     };
-    int blk = (seg0 + blockIdx.z) * seg_len + warp;
-    if (PART == kKvFew && !tile && blockIdx.z == 0) blk = start + warp;
+    int blk = start + blockIdx.z * seg_len + warp;
     int page = page_of(blk);
     if (page >= 0) {
         load_k(page, 0);
@@ -418,7 +416,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
                     make_uint2(*reinterpret_cast<const uint32_t *>(&p0), *reinterpret_cast<const uint32_t *>(&p1));
             } else {
                 const int64_t pr = PART == kKvWhole ? kv_part_row(a, ui, seg, tok, head)
-                                                    : kv_shared_part_row(a, tile ? seg : a.n_pre + seg - seg0, u.row + tok, head);
+                                                    : kv_shared_part_row(a, tile ? seg : a.n_pre + seg, u.row + tok, head);
                 *reinterpret_cast<float4 *>(a.part_o + pr * D + col) = x;
                 if (col == 0) a.part_ml[pr] = make_float2(M, L);
             }
@@ -426,7 +424,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
         __syncthreads();   // read before the next segment's results
     };
 
-    for (int seg = seg0 + blockIdx.z;;) {
+    for (int seg = blockIdx.z;;) {
         lref = 0.f;
 #pragma unroll
         for (int f = 0; f < NT; ++f) {
@@ -437,10 +435,10 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[i][f][k] = 0.f;
         }
-        const int seg_end = (seg + 1) * seg_len, next_seg = seg + gridDim.z;
+        const int seg_end = start + (seg + 1) * seg_len, next_seg = seg + gridDim.z;
 #pragma unroll 1
         for (; blk < min(seg_end, u.block); blk += kTokenWarps) {
-            const int next = page_of(blk + kTokenWarps < seg_end ? blk + kTokenWarps : next_seg * seg_len + warp);
+            const int next = page_of(blk + kTokenWarps < seg_end ? blk + kTokenWarps : start + next_seg * seg_len + warp);
             const int64_t ph = (int64_t)page * a.Hkv + h;
             const float ks = a.scale_log2 * a.c.k_scale[ph], vs = a.c.v_scale[ph];
             float move = 1.f;
@@ -536,7 +534,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, TokenPlan<D, R>::kCtas) kv_a
         merge(seg);
         if (next_seg > last_seg) return;
         seg = next_seg;
-        blk = seg * seg_len + warp;
+        blk = start + seg * seg_len + warp;
     }
 }
 
