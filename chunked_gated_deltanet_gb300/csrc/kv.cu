@@ -52,7 +52,7 @@ struct PlanReq {
 };
 
 // Plan of a batch in one CTA: per request i with ctx tokens held and n_new[i] to come, rows[i] = sum of earlier
-// requests' new tokens, one unit per touched block, one page popped from the free stack per block that completes.
+// requests' new tokens (-1 past the last), one unit per touched block, one page popped from the free stack per block that completes.
 // Sums go in request order, so pages are handed out in unit order. A batch that does not fit (pages, table, unit
 // map, a bad slot or count) leaves the cache as it was, with no unit and the reason in counts[1].
 // Bound: latency (about 1 KB in and out per 16 requests): 3.1 us for one request, 8.6 us for 1,024 prompts. One CTA, or a cluster of kPlanCluster where the map has room for
@@ -61,7 +61,8 @@ struct PlanReq {
 constexpr int kPlanCluster = 8;
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvCache c, const int32_t *slots, const int32_t *n_new,
                                                                 int n, int32_t *rows, int32_t *units, int32_t *counts,
-                                                                int max_units, int32_t *state_out, int32_t *n_free_out) {
+                                                                int max_requests, int max_units, int32_t *state_out,
+                                                                int32_t *n_free_out) {
     grid_dep_wait();
     grid_dep_launch();
     extern __shared__ __align__(16) unsigned char plan_smem[];
@@ -140,6 +141,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvCache c, 
         counts[1] = (int)status;
         *n_free_out = status == 0 ? n_free - total.pages : n_free;
     }
+    // no requests there: an earlier plan's sums would pass for this one's (kv_group_kernel takes a negative one as out of range)
+    if (first)
+        for (int i = n + 1 + t; i <= max_requests; i += kPlanThreads) rows[i] = -1;
     if (status != 0) return;
     __syncthreads();
     // one thread per unit; its request is the last one whose first unit is not after it
@@ -409,7 +413,7 @@ cudaError_t launch_append(const KvCache &c, const int32_t *units, const int32_t 
 }  // namespace gdn
 
 cudaError_t gdn_launch_kv_plan(const gdn::KvCache &c, const int32_t *slots, const int32_t *n_new, int n, int32_t *rows,
-                               int32_t *units, int32_t *counts, int max_units, int32_t *state_out, int32_t *n_free_out,
+                               int32_t *units, int32_t *counts, int max_requests, int max_units, int32_t *state_out, int32_t *n_free_out,
                                cudaStream_t st) {
     using namespace gdn;
     const size_t smem = (size_t)n * sizeof(PlanReq);
@@ -432,7 +436,8 @@ cudaError_t gdn_launch_kv_plan(const gdn::KvCache &c, const int32_t *slots, cons
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, kv_plan_kernel, c, slots, n_new, n, rows, units, counts, max_units, state_out, n_free_out);
+    e = cudaLaunchKernelEx(&cfg, kv_plan_kernel, c, slots, n_new, n, rows, units, counts, max_requests, max_units, state_out,
+                           n_free_out);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -200,7 +200,7 @@ __device__ __forceinline__ int64_t kv_part_row(const KvAttn &a, int unit, int se
 }  // namespace gdn
 
 cudaError_t gdn_launch_kv_plan(const gdn::KvCache &c, const int32_t *slots, const int32_t *n_new, int n, int32_t *rows,
-                               int32_t *units, int32_t *counts, int max_units, int32_t *state_out, int32_t *n_free_out,
+                               int32_t *units, int32_t *counts, int max_requests, int max_units, int32_t *state_out, int32_t *n_free_out,
                                cudaStream_t st);
 cudaError_t gdn_launch_kv_append(const gdn::KvCache &c, const int32_t *units, const int32_t *counts, int unit_bound,
                                  const void *k, const void *v, int64_t n_rows, int Hkv, int d, int bf16, unsigned *err,

@@ -147,8 +147,8 @@ GDN_API gdn_status gdn_kv_plan(const gdn_attn_desc *d, const gdn_kv_cache *c, co
         return fail(GDN_ERR_INVALID_ARG, "state_out must be 8-byte aligned, n_free_out 4-byte");
     cudaStream_t cst = (cudaStream_t)stream;
     const cudaError_t e = launch_k(K_KV_PLAN, cst, [&] {
-        return gdn_launch_kv_plan(device_cache(c), slots, n_new, n, m->rows, m->units, m->counts, m->max_units, state_out,
-                                  n_free_out, cst);
+        return gdn_launch_kv_plan(device_cache(c), slots, n_new, n, m->rows, m->units, m->counts, m->max_requests, m->max_units,
+                                  state_out, n_free_out, cst);
     });
     return e != cudaSuccess ? cuda_fail(e, "plan kernel") : GDN_OK;
 }

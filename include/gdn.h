@@ -366,7 +366,7 @@ typedef struct gdn_kv_cache {
 } gdn_kv_cache;
 
 /* A plan's device buffers: rows [max_requests + 1] (prefix sums of the new
- * tokens), units [max_units][8] and counts [2] = {units, status}. A unit is the
+ * tokens; -1 behind the plan's last request), units [max_units][8] and counts [2] = {units, status}. A unit is the
  * new tokens of one request inside one block, in request and position order:
  * {slot, block, page or -1 while the block stays open, offset of the first new
  * token, their number, row of the first one in the packed inputs, tail buffer
