@@ -6,9 +6,10 @@
 //   (y_0, y_1) -> magnitude (y_0 cos a - y_1 sin a, y_0 sin a + y_1 cos a),
 // the other elements as they are. fp32 from the loaded values to the one rounding at the end.
 //
-// The angle is a whole number of 2^-64 turns: f_i / 2 pi as a 64-bit fraction (the table), times p modulo 2^64. That is exact
-// but for the fraction's rounding, p 2^-65 turns, at any position, and costs one 64-bit product; its upper 32 bits in units
-// of half turns are what sincospi takes, in [-1, 1).
+// The angle is a whole number of 2^-64 turns: f_i / 2 pi as a 64-bit fraction (the table), times p modulo 2^64: one 64-bit
+// product, without an error of its own at any position. Its upper 32 bits in units of half turns are what sincospi takes, in
+// [-1, 1), rounded to fp32. Two errors are left: the table's, as it is made in fp64 (a power, two quotients, some 2^-50.2 of
+// f_i / 2 pi <= 0.16 at worst), about p 2^-53 turns; and the fp32 argument's, 2^-26 turns whatever p is.
 #include <cmath>
 
 #include "common.cuh"
@@ -88,9 +89,10 @@ struct RopeArgs {
 // where it rotates (i and i + rotary_dim / 2: one of each half; neighbours: two in a row), any other two where not. So a
 // lane's angles are the same for all heads of the row; the lanes of a column in the warp's HPW heads share them out, one
 // sincospi a pair and row (all of them in every lane: 194 us on the case below).
-// Bound: HBM, every element in and out once: 47,880 rows of 32 + 8 + 8 heads of 128, 188 us, 6.3 TB/s. One pass of heads at a
-// time: with two under way it takes 215 us, with 5 CTAs an SM in place of 4 199, with 3 218. One row: 6 us in a graph, its heads
-// over as many warps as they fill (three dependent reads: position, table, elements).
+// Bound: HBM, every element in and out once: 47,880 rows of 32 + 8 + 8 heads of 128, 186 us, 6.3 TB/s; 24,000 such rows in fp32
+// 179 us, 6.6 TB/s, with the norm or without. One pass of heads at a time: with two under way it takes 215 us, with 5 CTAs an SM
+// in place of 4 199, with 3 218. One row: 6 us in a graph, its heads over as many warps as they fill (three dependent reads:
+// position, table, elements).
 template <typename InT, int D>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
     using V = RopeVec<InT>;

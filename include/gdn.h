@@ -537,7 +537,10 @@ gdn_status gdn_kv_attention_shared(const gdn_attn_desc *desc, const gdn_kv_cache
  * GDN_ROPE_LINEAR: f_i / factor. GDN_ROPE_PARTS ("NTK-by-parts" of Peng et al.,
  * "YaRN", 2023): with t_i = original_len f_i / (2 pi) turns within the trained
  * length and c_i = (t_i - beta_slow) / (beta_fast - beta_slow) held to [0, 1],
- * c_i f_i + (1 - c_i) f_i / factor. */
+ * c_i f_i + (1 - c_i) f_i / factor. Here c_i runs over turns, as in that paper's
+ * formula; programs that let it run over i between two whole numbers get other
+ * f_i. The table is the caller's buffer, so theirs, or any others, can be
+ * written to it: entry i is f_i / (2 pi) 2^64, rounded, modulo 2^64. */
 enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 };   /* pairs (i, i + rotary_dim / 2), or (2 i, 2 i + 1) */
 enum { GDN_ROPE_NONE = 0, GDN_ROPE_LINEAR = 1, GDN_ROPE_PARTS = 2 };
 typedef struct gdn_rope_desc {
@@ -570,7 +573,8 @@ gdn_status gdn_kv_positions(const gdn_kv_map *map, int64_t n_rows, int32_t *posi
  * own contiguous input; other overlaps are refused. positions: int32 device
  * [n_rows]; rows of a negative position are left as they are. q_weight,
  * k_weight: in_dtype [d] device, NULL for no norm. fp32 arithmetic, one rounding
- * at the end; an angle is exact to p 2^-53 turns. */
+ * at the end; an angle is off by about p 2^-53 turns of the table and 2^-26 of
+ * the fp32 argument of its sine and cosine. */
 gdn_status gdn_rope(const gdn_attn_desc *desc, const gdn_rope_desc *rope, const uint64_t *table, const int32_t *positions,
                     const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                     const void *q_weight, const void *k_weight, void *q_out, void *k_out, void *v_out, int64_t n_rows,
