@@ -78,9 +78,11 @@ __device__ bool fork_batch_ok(const int32_t *src, const int32_t *dst, int n, int
 // source's, and the pages that lost their last name go on the free stack in the order of their numbers, so that the
 // stack does not depend on the order of the atomics. The other CTAs copy the open blocks' rows (nothing they read is
 // written here: no source is a target).
-// Bound: latency, five passes between cluster barriers (check, names, drops, count and push of freed pages), and past some ten
-// thousand table entries the atomics on a few sources' pages. 16 forks of 187 blocks: 10 us in a graph; 256 forks and releases
-// of 8 to 653 blocks: 21 us.
+// Bound: latency, five passes between cluster barriers (check, names, drops, count and push of freed pages), 6 us in a graph of
+// such calls for 16 forks of 187 blocks; past some ten thousand entries (pairs times the longest one's blocks) the passes of
+// names and drops over them on the cluster's eight SMs, 0.1 us a thousand: 256 forks of 187 blocks 12 us, of 653 24, 1,024 of 187
+// 28. Not the atomics on a few sources' pages: forks of one, 12 or as many sources take 21, 25 and 24 us (256 of 653), 34, 27
+// and 28 (1,024 of 187). 256 forks and releases of 8 to 653 blocks: 19 to 21 us.
 __global__ void __launch_bounds__(kPageThreads) kv_fork_batch_kernel(const KvCache c, const int32_t *src, const int32_t *dst, int n,
                                                                      int Hkv, int row_vec, unsigned *err) {
     grid_dep_wait();
